@@ -29,7 +29,8 @@
  *     error nothing is launched and no output is touched. Launch failures
  *     return MOE_ERR_HIP. A device fault surfaces at the caller's next
  *     synchronisation. No C++ exception crosses this interface.
- *   - M = 0 is valid: the call returns MOE_OK and launches nothing.
+ *   - M = 0 is valid: the call returns MOE_OK and launches nothing (except
+ *     where an output does not depend on M: the operators at the end say so).
  *   - bf16 and fp16 values travel as uint16_t bit patterns.
  *
  * Canonical weight format (input of moe_w4a16_repack, a reading of the
@@ -53,6 +54,9 @@
  * routing, grouping, layer structure and bf16 activations, with the weights
  * in the OCP Microscaling (MX) v1.0 MXFP4 format: FP4 e2m1 codes and one E8M0
  * scale per 32 input channels.
+ *
+ * Operators beside the layer (moe_balance_*, moe_lora_* at the end): what
+ * trains the router and adapts the frozen weights to a task or a request.
  */
 #ifndef MOE_W4A16_H
 #define MOE_W4A16_H
@@ -345,6 +349,101 @@ int moe_mxfp4_layer(const float* logits, const uint16_t* x_bf16, int32_t M, int3
                     int32_t* num_tokens_post_pad, int64_t cap, const void* w13_packed, const void* w2_packed,
                     void* workspace, int64_t workspace_bytes, uint16_t* out_bf16, void* stream,
                     void* const* stage_events);
+
+/*
+ * ---- Balance loss of the router -------------------------------------------
+ * Beside moe_route_align, for training the router: per-expert counts, the loss
+ * that keeps the experts evenly used, and its gradient with respect to the
+ * logits. With p = softmax(logits[t, :]) over the E experts, and for each
+ * sequence s of T valid tokens
+ *   c[s, e] = how often e stands in the tokens' topk_ids,
+ *   P[s, e] = sum of p[t, e] over the tokens,
+ *   loss[s] = E / (top_k * T^2) * sum_e c[s, e] * P[s, e]
+ * (1 when the choices and the probabilities are uniform; T = 0 gives 0). The
+ * counts are constants of the gradient:
+ *   grad_logits[t, e] = grad_loss[s] * E / (top_k * T^2) * p[t, e] *
+ *                       (c[s, e] - sum_j c[s, j] * p[t, j]).
+ *
+ *   logits      fp32 [M, E]. -inf gives an expert probability 0; a row of
+ *               nothing but -inf has all probabilities 0 and no gradient.
+ *   topk_ids    int32 [M, top_k] of moe_route_align; entries outside [0, E)
+ *               (dropped choices) are not counted.
+ *   seq_offsets int32 [S + 1], ascending: sequence s has the rows
+ *               [seq_offsets[s], seq_offsets[s + 1]); NULL (S = 1 only): all
+ *               rows. Rows of no sequence are not read, and their rows of
+ *               grad_logits are left as they were.
+ *   row_valid   uint8 [M] or NULL: rows with 0 (padding) are not counted and
+ *               their logits are not read; their rows of grad_logits are 0.
+ *   expert_counts int32 [S, E], prob_sums fp32 [S, E], seq_tokens int32 [S]
+ *               (T), loss fp32 [S]: out, all of it written. With M = 0 too:
+ *               zeros.
+ *   workspace   >= moe_balance_workspace_bytes(M, E, S) bytes, 16-byte
+ *               aligned; contents on entry do not matter.
+ * The backward call takes expert_counts and seq_tokens as the forward wrote
+ * them. A data-parallel job may sum expert_counts, prob_sums and seq_tokens
+ * over its ranks before it uses them. Results are identical on every call.
+ * Limits: those of moe_route_align, 1 <= S <= 65535.
+ */
+int64_t moe_balance_workspace_bytes(int32_t M, int32_t E, int32_t S); /* host; -1 on invalid sizes */
+int moe_balance_loss(const float* logits, const int32_t* topk_ids, int32_t M, int32_t E, int32_t top_k,
+                     const int32_t* seq_offsets, int32_t S, const uint8_t* row_valid, int32_t* expert_counts,
+                     float* prob_sums, int32_t* seq_tokens, float* loss, void* workspace, int64_t workspace_bytes,
+                     void* stream);
+int moe_balance_loss_backward(const float* logits, int32_t M, int32_t E, int32_t top_k, const int32_t* seq_offsets,
+                              int32_t S, const uint8_t* row_valid, const int32_t* expert_counts,
+                              const int32_t* seq_tokens, const float* grad_loss, float* grad_logits, void* stream);
+
+/*
+ * ---- Low-rank adapters of many requests ------------------------------------
+ * The expert weights are frozen 4-bit codes; what is trained and what differs
+ * from request to request are low-rank adapters. These calls add them to a
+ * projection that all requests share: the router's (fp32 logits), the layer
+ * as a whole (bf16 out), or any other. Row t of the batch has adapter
+ * a = adapter_ids[t], or none if that is outside [0, L):
+ *   h[t]   = A_a x[t]
+ *   out[t] = base[t] + scales[a] * B_a h[t]            (no adapter: base[t])
+ * and backwards, from grad_out,
+ *   dh[t]  = scales[a] * B_a^T grad_out[t]
+ *   dx[t]  = dx_base[t] + A_a^T dh[t]                  (no adapter: dx_base[t])
+ *   grad_a[a] = sum of dh[t] x[t]^T, grad_b[a] = scales[a] * sum of
+ *   grad_out[t] h[t]^T over the rows t of adapter a (no rows: zeros).
+ *
+ *   x_bf16      bf16 [M, K], row stride ldx (elements).
+ *   adapter_ids int32 [M], in any order; rows are grouped by adapter inside
+ *               the call.
+ *   a_bf16      bf16 [L, rank, K], b_bf16 bf16 [L, N, rank]: contiguous. An
+ *               adapter of a smaller rank is stored with zero rows of A.
+ *   scales      fp32 [L], or NULL: 1.
+ *   base, out   [M, N] of out_dtype, row strides ld_base and ld_out. base may
+ *               be NULL (zeros) or the same matrix as out (in place: rows
+ *               without an adapter are then not touched).
+ *   h           fp32 [M, rank]: out, for the backward call (rows without an
+ *               adapter are 0), or NULL.
+ *   dx_base, dx bf16 [M, K], as base and out; dx may be NULL (then dx_base is).
+ *   grad_a, grad_b fp32 [L, rank, K], [L, N, rank]: every element written.
+ *               With M = 0 too: zeros.
+ *   workspace   >= moe_lora_workspace_bytes(M, L, K, N, rank, backward) bytes.
+ * out and dx are accumulated in fp32 and rounded once; h and dh stay fp32.
+ * Results are identical on every call.
+ * x, a, b, dx_base, dx, h, grad_a, grad_b and workspace are 16-byte aligned,
+ * ldx, ld_dx_base and ld_dx multiples of 8; base, out and grad_out need their
+ * elements' alignment only (16-byte aligned rows of a multiple of 16 bytes are
+ * faster). Buffers other than base = out and dx_base = dx must not overlap.
+ * Limits: 1 <= L <= 1024; rank a multiple of 8 up to 128; K a multiple of 8;
+ * K, N <= 2^20; M <= 2^24.
+ */
+enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1 };
+int64_t moe_lora_workspace_bytes(int32_t M, int32_t L, int32_t K, int32_t N, int32_t rank,
+                                 int32_t backward); /* host; -1 on invalid sizes */
+int moe_lora_forward(const uint16_t* x_bf16, int64_t ldx, const int32_t* adapter_ids, int32_t M, int32_t L, int32_t K,
+                     int32_t N, int32_t rank, const uint16_t* a_bf16, const uint16_t* b_bf16, const float* scales,
+                     const void* base, int64_t ld_base, void* out, int64_t ld_out, int32_t out_dtype, float* h,
+                     void* workspace, int64_t workspace_bytes, void* stream);
+int moe_lora_backward(const void* grad_out, int64_t ld_grad_out, int32_t out_dtype, const uint16_t* x_bf16,
+                      int64_t ldx, const int32_t* adapter_ids, const float* h, int32_t M, int32_t L, int32_t K,
+                      int32_t N, int32_t rank, const uint16_t* a_bf16, const uint16_t* b_bf16, const float* scales,
+                      const uint16_t* dx_base, int64_t ld_dx_base, uint16_t* dx, int64_t ld_dx, float* grad_a,
+                      float* grad_b, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Measurement helpers (not part of the layer). They measure what this GPU
  * sustains, so that a layer kernel's rate can be stated as a fraction of the

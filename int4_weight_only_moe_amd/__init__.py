@@ -10,6 +10,7 @@ that allocate the buffers a layer call needs.
 """
 from __future__ import annotations
 
+from contextlib import nullcontext
 from dataclasses import dataclass
 
 import torch
@@ -21,6 +22,8 @@ from ._binding import (  # noqa: F401
     moe_w4a16_preferred_block_m, moe_w4a16_repack, moe_w4a16_unpack, moe_w4a16_workspace_bytes,
     moe_mxfp4_fc1, moe_mxfp4_fc2, moe_mxfp4_forward, moe_mxfp4_layer, moe_mxfp4_packed_bytes, moe_mxfp4_repack,
     moe_mxfp4_unpack, status_string, moe_calib_read_granule, moe_calib_hbm_read, moe_calib_mfma_f16,
+    MOE_DTYPE_BF16, MOE_DTYPE_F32, moe_balance_loss, moe_balance_loss_backward, moe_balance_workspace_bytes,
+    moe_lora_backward, moe_lora_forward, moe_lora_workspace_bytes,
 )
 
 FORMATS = ("int4", "mxfp4")  # weight formats: INT4 g32 + fp16 scales, MXFP4 (e2m1 + E8M0 per 32)
@@ -124,3 +127,110 @@ def layer(logits: torch.Tensor, x: torch.Tensor, rb: RouteBuffers, I: int, w13_p
          rb.block_expert_ids, rb.expert_offsets, rb.num_tokens_post_pad, w13_packed, w2_packed,
          workspace, out, cap=rb.cap, stream=stream, stage_events=stage_events)
     return out
+
+
+# ------------------------------------------------------------------ operators beside the layer
+def _memory_of(stream, device):
+    """A context in which torch allocates for `stream`: what the helpers below
+    allocate themselves is used on it, and is reused only in its order."""
+    if stream is None:
+        return nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+@dataclass
+class BalanceBuffers:
+    """Outputs of moe_balance_loss for S sequences of up to M tokens in all, and its workspace."""
+    M: int
+    E: int
+    S: int
+    expert_counts: torch.Tensor
+    prob_sums: torch.Tensor
+    seq_tokens: torch.Tensor
+    loss: torch.Tensor
+    workspace: torch.Tensor
+
+
+def alloc_balance_buffers(M: int, E: int, S: int = 1, device="cuda") -> BalanceBuffers:
+    nbytes = moe_balance_workspace_bytes(M, E, S)
+    if nbytes < 0:
+        raise ValueError("unsupported sizes")
+    i32, f32 = dict(dtype=torch.int32, device=device), dict(dtype=torch.float32, device=device)
+    return BalanceBuffers(M, E, S, torch.empty((S, E), **i32), torch.empty((S, E), **f32), torch.empty(S, **i32),
+                          torch.empty(S, **f32), torch.empty(nbytes, dtype=torch.uint8, device=device))
+
+
+def balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, bufs: BalanceBuffers,
+                 seq_offsets: torch.Tensor | None = None, row_valid: torch.Tensor | None = None,
+                 stream=None) -> BalanceBuffers:
+    """The balance loss of each sequence, its tokens' choices per expert and
+    its sums of probabilities. seq_offsets: int32 [S + 1] (None: one sequence
+    of all rows); row_valid: bool [M] (None: all rows count)."""
+    moe_balance_loss(logits, topk_ids, bufs.expert_counts, bufs.prob_sums, bufs.seq_tokens, bufs.loss, bufs.workspace,
+                     seq_offsets=seq_offsets, row_valid=row_valid, stream=stream)
+    return bufs
+
+
+def balance_loss_backward(logits: torch.Tensor, top_k: int, expert_counts: torch.Tensor, seq_tokens: torch.Tensor,
+                          grad_loss: torch.Tensor, seq_offsets: torch.Tensor | None = None,
+                          row_valid: torch.Tensor | None = None, grad_logits: torch.Tensor | None = None,
+                          stream=None) -> torch.Tensor:
+    """The gradient of sum(grad_loss * loss) with respect to the logits, fp32
+    [M, E]. Rows of no sequence are left as they were in grad_logits (zeros
+    if it is allocated here)."""
+    if grad_logits is None:
+        with _memory_of(stream, logits.device):
+            grad_logits = torch.empty_like(logits) if seq_offsets is None else torch.zeros_like(logits)
+    moe_balance_loss_backward(logits, top_k, expert_counts, seq_tokens, grad_loss, grad_logits,
+                              seq_offsets=seq_offsets, row_valid=row_valid, stream=stream)
+    return grad_logits
+
+
+def _lora_workspace(x, lora_a, lora_b, backward, stream):
+    M, K = x.shape
+    nbytes = moe_lora_workspace_bytes(M, lora_a.shape[0], K, lora_b.shape[1], lora_a.shape[1], backward)
+    if nbytes < 0:
+        raise ValueError("unsupported adapter sizes")
+    with _memory_of(stream, x.device):
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=x.device)
+
+
+def lora_forward(x: torch.Tensor, adapter_ids: torch.Tensor, lora_a: torch.Tensor, lora_b: torch.Tensor,
+                 scales: torch.Tensor | None = None, base: torch.Tensor | None = None,
+                 out: torch.Tensor | None = None, h: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """out[t] = base[t] + scales[a] * B_a (A_a x[t]) with a = adapter_ids[t]
+    (outside [0, L): no adapter, out[t] = base[t]). x bf16 [M, K]; adapter_ids
+    int32 [M]; lora_a bf16 [L, rank, K]; lora_b bf16 [L, N, rank]; base and out
+    bf16 or fp32 [M, N] (out allocated like base, else bf16; out=base adds in
+    place). h: fp32 [M, rank] to keep A x in for lora_backward."""
+    if out is None:
+        with _memory_of(stream, x.device):
+            out = torch.empty((x.shape[0], lora_b.shape[1]), dtype=base.dtype if base is not None else torch.bfloat16,
+                              device=x.device)
+    if workspace is None:
+        workspace = _lora_workspace(x, lora_a, lora_b, False, stream)
+    moe_lora_forward(x, adapter_ids, lora_a, lora_b, out, workspace, scales=scales, base=base, h=h, stream=stream)
+    return out
+
+
+def lora_backward(grad_out: torch.Tensor, x: torch.Tensor, adapter_ids: torch.Tensor, h: torch.Tensor,
+                  lora_a: torch.Tensor, lora_b: torch.Tensor, scales: torch.Tensor | None = None,
+                  dx_base: torch.Tensor | None = None, need_dx: bool = True, grads: tuple | None = None,
+                  workspace: torch.Tensor | None = None, stream=None) -> tuple:
+    """Gradients of lora_forward: (dx bf16 [M, K] = dx_base + the adapters'
+    part, grad_a fp32 like lora_a, grad_b fp32 like lora_b). need_dx=False
+    leaves dx out (None). grads: buffers of an earlier call to write into."""
+    if grads is None:
+        with _memory_of(stream, x.device):
+            grads = (torch.empty(x.shape, dtype=torch.bfloat16, device=x.device) if need_dx else None,
+                     torch.empty(lora_a.shape, dtype=torch.float32, device=x.device),
+                     torch.empty(lora_b.shape, dtype=torch.float32, device=x.device))
+    dx, grad_a, grad_b = grads
+    if workspace is None:
+        workspace = _lora_workspace(x, lora_a, lora_b, True, stream)
+    moe_lora_backward(grad_out, x, adapter_ids, h, lora_a, lora_b, grad_a, grad_b, workspace, scales=scales, dx=dx,
+                      dx_base=dx_base, stream=stream)
+    return grads

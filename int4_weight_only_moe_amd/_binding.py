@@ -25,6 +25,10 @@ MOE_ERR_WORKSPACE = -4
 MOE_ERR_HIP = -5
 MOE_ERR_SCRATCH = -6
 
+MOE_DTYPE_BF16 = 0
+MOE_DTYPE_F32 = 1
+_SIDE_DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32}
+
 KIND_W13 = 0
 KIND_W2 = 1
 GROUP = 32
@@ -54,6 +58,16 @@ _SIGNATURES = {
     "moe_mxfp4_repack": (ctypes.c_int, [_vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp]),
     "moe_mxfp4_unpack": (ctypes.c_int, [_vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp]),
 }
+_SIGNATURES["moe_balance_workspace_bytes"] = (_i64, [_i32, _i32, _i32])
+_SIGNATURES["moe_balance_loss"] = (ctypes.c_int, [_vp, _vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
+                                                  _i64, _vp])
+_SIGNATURES["moe_balance_loss_backward"] = (ctypes.c_int, [_vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp,
+                                                           _vp])
+_SIGNATURES["moe_lora_workspace_bytes"] = (_i64, [_i32, _i32, _i32, _i32, _i32, _i32])
+_SIGNATURES["moe_lora_forward"] = (ctypes.c_int, [_vp, _i64, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp,
+                                                  _i64, _vp, _i64, _i32, _vp, _vp, _i64, _vp])
+_SIGNATURES["moe_lora_backward"] = (ctypes.c_int, [_vp, _i64, _i32, _vp, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
+                                                   _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp])
 _SIGNATURES["moe_calib_read_granule"] = (_i64, [])
 _SIGNATURES["moe_calib_hbm_read"] = (ctypes.c_int, [_vp, _i64, _i32, _vp, _vp])
 _SIGNATURES["moe_calib_mfma_f16"] = (ctypes.c_int, [_i64, _i32, _vp, _vp])
@@ -325,6 +339,148 @@ def moe_mxfp4_fc2(*args, **kw) -> None:
 def moe_mxfp4_layer(*args, **kw) -> None:
     """moe_w4a16_layer with moe_mxfp4_repack weights."""
     moe_w4a16_layer(*args, _prefix="moe_mxfp4", **kw)
+
+
+# ------------------------------------------------------------------ operators beside the layer
+def _shaped(t: torch.Tensor | None, dtype, shape: tuple, what: str, device: torch.device) -> int:
+    """The pointer of a contiguous tensor of this type and shape on this device (None: NULL)."""
+    if t is None:
+        return 0
+    if t.device != device:
+        raise ValueError(f"{what} must be on {device}, got {t.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{what} must have shape {shape}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
+def _matrix(t: torch.Tensor | None, dtype, shape: tuple, what: str, device: torch.device) -> tuple:
+    """(pointer, row stride) of a matrix whose rows are contiguous (None: NULL)."""
+    if t is None:
+        return 0, 0
+    if t.device != device:
+        raise ValueError(f"{what} must be on {device}, got {t.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{what} must have shape {shape}, got {tuple(t.shape)}")
+    rows, cols = t.stride()
+    if cols != 1 and shape[1] > 1:
+        raise ValueError(f"{what} must have contiguous rows")
+    if shape[0] <= 1:  # the stride of a single row says nothing
+        rows = -(-shape[1] // 8) * 8
+    return t.data_ptr(), rows
+
+
+def _on_device(device: torch.device, name: str, stream, *args) -> None:
+    """Call an entry point with `device` current, on `stream` or that device's current stream."""
+    if device.type != "cuda":
+        raise ValueError(f"{name} needs device tensors")
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _check(name, getattr(lib(), name)(*args, _stream(stream)))
+    _check(name, getattr(lib(), name)(*args, _stream(stream)))
+
+
+def moe_balance_workspace_bytes(M: int, E: int, S: int) -> int:
+    return lib().moe_balance_workspace_bytes(M, E, S)
+
+
+def _balance_inputs(logits, seq_offsets, S, row_valid):
+    if logits.dim() != 2:
+        raise ValueError("logits must be a matrix [M, E]")
+    dev = logits.device
+    M, E = logits.shape
+    if row_valid is not None and row_valid.dtype == torch.bool:
+        row_valid = row_valid.view(torch.uint8)
+    return (dev, M, E, _shaped(logits, torch.float32, (M, E), "logits", dev),
+            _shaped(seq_offsets, torch.int32, (S + 1,), "seq_offsets", dev),
+            _shaped(row_valid, torch.uint8, (M,), "row_valid", dev))
+
+
+def moe_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, expert_counts: torch.Tensor,
+                     prob_sums: torch.Tensor, seq_tokens: torch.Tensor, loss: torch.Tensor, workspace: torch.Tensor,
+                     seq_offsets: torch.Tensor | None = None, row_valid: torch.Tensor | None = None,
+                     stream=None) -> None:
+    """row_valid: bool or uint8 [M]. S is the length of `loss`."""
+    S = loss.numel()
+    dev, M, E, p_logits, p_off, p_valid = _balance_inputs(logits, seq_offsets, S, row_valid)
+    k = topk_ids.shape[-1]
+    _on_device(dev, "moe_balance_loss", stream, p_logits, _shaped(topk_ids, torch.int32, (M, k), "topk_ids", dev), M, E,
+               k, p_off, S, p_valid, _shaped(expert_counts, torch.int32, (S, E), "expert_counts", dev),
+               _shaped(prob_sums, torch.float32, (S, E), "prob_sums", dev),
+               _shaped(seq_tokens, torch.int32, (S,), "seq_tokens", dev),
+               _shaped(loss, torch.float32, (S,), "loss", dev),
+               _shaped(workspace, torch.uint8, tuple(workspace.shape), "workspace", dev), workspace.numel())
+
+
+def moe_balance_loss_backward(logits: torch.Tensor, top_k: int, expert_counts: torch.Tensor,
+                              seq_tokens: torch.Tensor, grad_loss: torch.Tensor, grad_logits: torch.Tensor,
+                              seq_offsets: torch.Tensor | None = None, row_valid: torch.Tensor | None = None,
+                              stream=None) -> None:
+    S = seq_tokens.numel()
+    dev, M, E, p_logits, p_off, p_valid = _balance_inputs(logits, seq_offsets, S, row_valid)
+    _on_device(dev, "moe_balance_loss_backward", stream, p_logits, M, E, top_k, p_off, S, p_valid,
+               _shaped(expert_counts, torch.int32, (S, E), "expert_counts", dev),
+               _shaped(seq_tokens, torch.int32, (S,), "seq_tokens", dev),
+               _shaped(grad_loss, torch.float32, (S,), "grad_loss", dev),
+               _shaped(grad_logits, torch.float32, (M, E), "grad_logits", dev))
+
+
+def moe_lora_workspace_bytes(M: int, L: int, K: int, N: int, rank: int, backward: bool = False) -> int:
+    return lib().moe_lora_workspace_bytes(M, L, K, N, rank, int(backward))
+
+
+def _lora_sizes(x, lora_a, lora_b):
+    if x.dim() != 2 or lora_a.dim() != 3 or lora_b.dim() != 3:
+        raise ValueError("x must be [M, K], lora_a [L, rank, K] and lora_b [L, N, rank]")
+    M, K = x.shape
+    L, r, _ = lora_a.shape
+    return M, L, K, lora_b.shape[1], r
+
+
+def _side_dtype(t: torch.Tensor, what: str) -> int:
+    if t.dtype not in _SIDE_DTYPES:
+        raise ValueError(f"{what} must be bfloat16 or float32, got {t.dtype}")
+    return _SIDE_DTYPES[t.dtype]
+
+
+def moe_lora_forward(x: torch.Tensor, adapter_ids: torch.Tensor, lora_a: torch.Tensor, lora_b: torch.Tensor,
+                     out: torch.Tensor, workspace: torch.Tensor, scales: torch.Tensor | None = None,
+                     base: torch.Tensor | None = None, h: torch.Tensor | None = None, stream=None) -> None:
+    M, L, K, N, r = _lora_sizes(x, lora_a, lora_b)
+    dev, bf16, f32 = x.device, torch.bfloat16, torch.float32
+    kind = _side_dtype(out, "out")
+    px, ldx = _matrix(x, bf16, (M, K), "x", dev)
+    pb, ldb = _matrix(base, out.dtype, (M, N), "base", dev)
+    po, ldo = _matrix(out, out.dtype, (M, N), "out", dev)
+    _on_device(dev, "moe_lora_forward", stream, px, ldx, _shaped(adapter_ids, torch.int32, (M,), "adapter_ids", dev),
+               M, L, K, N, r, _shaped(lora_a, bf16, (L, r, K), "lora_a", dev),
+               _shaped(lora_b, bf16, (L, N, r), "lora_b", dev), _shaped(scales, f32, (L,), "scales", dev), pb, ldb,
+               po, ldo, kind, _shaped(h, f32, (M, r), "h", dev),
+               _shaped(workspace, torch.uint8, tuple(workspace.shape), "workspace", dev), workspace.numel())
+
+
+def moe_lora_backward(grad_out: torch.Tensor, x: torch.Tensor, adapter_ids: torch.Tensor, h: torch.Tensor,
+                      lora_a: torch.Tensor, lora_b: torch.Tensor, grad_a: torch.Tensor, grad_b: torch.Tensor,
+                      workspace: torch.Tensor, scales: torch.Tensor | None = None, dx: torch.Tensor | None = None,
+                      dx_base: torch.Tensor | None = None, stream=None) -> None:
+    M, L, K, N, r = _lora_sizes(x, lora_a, lora_b)
+    dev, bf16, f32 = x.device, torch.bfloat16, torch.float32
+    kind = _side_dtype(grad_out, "grad_out")
+    pg, ldg = _matrix(grad_out, grad_out.dtype, (M, N), "grad_out", dev)
+    px, ldx = _matrix(x, bf16, (M, K), "x", dev)
+    pb, ldb = _matrix(dx_base, bf16, (M, K), "dx_base", dev)
+    pd, ldd = _matrix(dx, bf16, (M, K), "dx", dev)
+    _on_device(dev, "moe_lora_backward", stream, pg, ldg, kind, px, ldx,
+               _shaped(adapter_ids, torch.int32, (M,), "adapter_ids", dev), _shaped(h, f32, (M, r), "h", dev), M, L, K,
+               N, r, _shaped(lora_a, bf16, (L, r, K), "lora_a", dev), _shaped(lora_b, bf16, (L, N, r), "lora_b", dev),
+               _shaped(scales, f32, (L,), "scales", dev), pb, ldb, pd, ldd,
+               _shaped(grad_a, f32, (L, r, K), "grad_a", dev), _shaped(grad_b, f32, (L, N, r), "grad_b", dev),
+               _shaped(workspace, torch.uint8, tuple(workspace.shape), "workspace", dev), workspace.numel())
 
 
 # ------------------------------------------------------------------ measurement helpers

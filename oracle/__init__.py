@@ -331,3 +331,77 @@ def layer(x: np.ndarray, logits: np.ndarray, k: int, experts, tokens_subset=None
     """Routing followed by the expert MLPs and the combine."""
     ids, w = route(logits, k)
     return moe_forward(x, ids, w, experts, tokens_subset), ids, w
+
+
+# ------------------------------------------------------------------ operators beside the layer
+def balance(logits, ids, offsets=None, valid=None):
+    """Balance loss of each sequence in float64: dict of counts [S, E], probs
+    (sums of probabilities) [S, E], tokens [S] and loss [S]."""
+    logits = np.asarray(logits, np.float64)
+    M, E = logits.shape
+    k = ids.shape[1]
+    offsets = [0, M] if offsets is None else list(offsets)
+    S = len(offsets) - 1
+    out = {"counts": np.zeros((S, E), np.int64), "probs": np.zeros((S, E)), "tokens": np.zeros(S, np.int64),
+           "loss": np.zeros(S)}
+    for s in range(S):
+        for t in range(offsets[s], offsets[s + 1]):
+            if valid is not None and not valid[t]:
+                continue
+            out["tokens"][s] += 1
+            out["probs"][s] += _softmax_or_zero(logits[t])
+            for e in ids[t]:
+                if 0 <= e < E:
+                    out["counts"][s, e] += 1
+        T = out["tokens"][s]
+        if T:
+            out["loss"][s] = E / (k * T * T) * float(out["counts"][s] @ out["probs"][s])
+    return out
+
+
+def _softmax_or_zero(row):
+    if np.all(row == -np.inf):
+        return np.zeros_like(row)
+    e = np.exp(row - row.max())
+    return e / e.sum()
+
+
+def balance_backward(logits, k, counts, tokens, grad_loss, offsets=None, valid=None):
+    """Gradient of sum(grad_loss * loss) by the logits (rows of no sequence: nan)."""
+    logits = np.asarray(logits, np.float64)
+    M, E = logits.shape
+    offsets = [0, M] if offsets is None else list(offsets)
+    g = np.full((M, E), np.nan)
+    for s in range(len(offsets) - 1):
+        for t in range(offsets[s], offsets[s + 1]):
+            g[t] = 0.0
+            if valid is None or valid[t]:
+                p = _softmax_or_zero(logits[t])
+                w = float(grad_loss[s]) * E / (k * float(tokens[s]) ** 2)
+                g[t] = w * p * (counts[s] - float(counts[s] @ p))
+    return g
+
+
+def lora_forward(x, ids, a, b, scales, base):
+    """(out, h) in float64: out = base + scale * B (A x) by row, h = A x."""
+    x, a, b, base = (np.asarray(v, np.float64) for v in (x, a, b, base))
+    L, r, _ = a.shape
+    out, h = base.copy(), np.zeros((x.shape[0], r))
+    for i in range(L):
+        rows = np.nonzero(ids == i)[0]
+        h[rows] = x[rows] @ a[i].T
+        out[rows] += float(scales[i]) * (h[rows] @ b[i].T)
+    return out, h
+
+
+def lora_backward(dout, x, ids, h, a, b, scales, dx_base):
+    """(dx, da, db) in float64."""
+    dout, x, h, a, b, dx_base = (np.asarray(v, np.float64) for v in (dout, x, h, a, b, dx_base))
+    dx, da, db = dx_base.copy(), np.zeros(a.shape), np.zeros(b.shape)
+    for i in range(a.shape[0]):
+        rows = np.nonzero(ids == i)[0]
+        dh = float(scales[i]) * (dout[rows] @ b[i])
+        dx[rows] += dh @ a[i]
+        da[i] = dh.T @ x[rows]
+        db[i] = float(scales[i]) * (dout[rows].T @ h[rows])
+    return dx, da, db
