@@ -6,20 +6,22 @@
 //   dh_t = s_a B_a^T dout_t                dx_t  = dxbase_t + A_a^T dh_t
 //   dA_a = sum_t dh_t x_t^T                dB_a  = s_a sum_t dout_t h_t^T
 //
-// The rows are grouped by adapter as the layer groups its assignments by
-// expert: lists padded to 64 rows, so a workgroup's tile holds rows of one
-// adapter. Four kernels do the products on the matrix cores:
-//   down    contracts a wide side with a [r, W] operand (h, dh): fp32 partial
-//           sums of each split of W;
-//   up      expands r values to a wide side and adds the base (out, dx);
-//   finish  adds dh's partial sums and lays dh and s h out rank-major;
-//   outer   sums rows' outer products (dA, dB).
-// With r <= 128 every one of them moves the wide side once and is bound by
-// that traffic, so the products are made exact where that is free: bf16
-// operands multiply exactly into fp32, and an fp32 factor (h, dh, an fp32
-// side) enters as bf16 parts of 8 bits each, three (24 bits: all of fp32)
-// where the result is fp32, two (16 bits, 2^-17 relative: 2^-8 of what the
-// result's rounding costs) where it is bf16.
+// The rows are grouped by adapter into tiles of up to 64 rows of one adapter
+// (rows without one are the last group). The kernels:
+//   group   the grouping, one workgroup; a forward of up to 256 rows has none:
+//           there each workgroup finds its tile's rows from the ids;
+//   down    contracts a wide side with a [r, W] operand (h, dh) in splits of W;
+//   up      adds the splits, expands r values to a wide side and adds the base
+//           (out, dx);
+//   prep    backward: the transposed weights, and s h rank-major;
+//   join    backward: dh, the sum of its splits, as it is and rank-major;
+//   outer   sums rows' outer products (dA, dB), reduce joins what was cut.
+// With r <= 128 each of them moves the wide side once and is bound by that
+// traffic, so the products are made exact where that is free: bf16 operands
+// multiply exactly into fp32, and an fp32 factor (h, dh, an fp32 side) enters
+// as bf16 parts of 8 bits each, three (24 bits: all of fp32) where the result
+// is fp32, two (16 bits, 2^-17 relative against the 2^-8 of the result's own
+// rounding) where it is bf16.
 #include <type_traits>
 
 #include "device_common.h"
@@ -93,52 +95,258 @@ __device__ __forceinline__ void load8(const float* __restrict__ row, int w, int 
   }
 }
 
-// The rows of tile `tile` of the grouping, in LDS: rows past the adapter's
-// last repeat the first (their results are dropped). Returns the row count.
-__device__ __forceinline__ int load_tile_rows(const int32_t* __restrict__ sorted, int tile, int M, int* rows,
-                                              int* count) {
-  if (threadIdx.x < 64) {
-    const int first = sorted[tile * kLoraTile];
-    const int row = sorted[tile * kLoraTile + threadIdx.x];
-    rows[threadIdx.x] = row < M ? row : first;
-    const uint64_t live = __ballot(row < M);
-    if (threadIdx.x == 0) *count = __builtin_popcountll(live);
+// Whether every lane of `live` holds the same key as its first one.
+__device__ __forceinline__ bool one_key(int key, uint64_t live) {
+  const int first = __builtin_amdgcn_readfirstlane(__shfl(key, (int)__builtin_ctzll(live | (uint64_t(1) << 63)), 64));
+  return (__ballot(key == first) & live) == live;
+}
+
+// Lanes of `live` whose key equals this lane's (keys below 2^nbits).
+__device__ __forceinline__ uint64_t same_key(int key, int nbits, uint64_t live) {
+  if (one_key(key, live)) return live;
+  uint64_t m = live;
+  for (int b = 0; b < nbits; ++b) {
+    const bool bit = (key >> b) & 1;
+    const uint64_t bal = __ballot(bit);
+    m &= bit ? bal : ~bal;
+  }
+  return m;
+}
+
+__device__ __forceinline__ int bits_below(uint64_t m) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
+}
+
+// ------------------------------------------------------------------ group
+constexpr int kGroupThreads = 1024;
+constexpr int kGroupWaves = kGroupThreads / 64;
+constexpr int kMaxKeys = 1025;  // 1024 adapters and "none"
+
+struct GroupArgs {
+  const int32_t* ids;       // [M]
+  int M, L;
+  int32_t* sorted;          // rows by adapter, each list padded to 64 with M
+  int32_t* block_adapter;   // a tile's adapter, L: rows without one
+  int32_t* offsets;         // [L + 2]: each list's first position; [L] the first row without an adapter
+};
+
+// Stable grouping by one workgroup: each wave walks a contiguous range of the
+// rows 64 at a time, counts its rows per adapter (one LDS update per distinct
+// adapter of a step, so rows of one adapter in a run cost no more than mixed
+// ones), the counts become each wave's first positions, and a second walk
+// places the rows. The ids are read twice; 8192 rows take 8 steps a wave.
+__global__ __launch_bounds__(kGroupThreads) void lora_group_kernel(GroupArgs p) {
+  __shared__ int cnt[kGroupWaves][kMaxKeys];
+  __shared__ int off[kMaxKeys + 1];
+  __shared__ int wave_tot[kGroupWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int keys = p.L + 1;
+  const int nbits = 32 - __clz(p.L);
+  for (int i = tid; i < keys; i += kGroupThreads)
+#pragma unroll
+    for (int w = 0; w < kGroupWaves; ++w) cnt[w][i] = 0;
+  __syncthreads();
+  const int seg = ((p.M + kGroupWaves - 1) / kGroupWaves + 63) / 64 * 64;
+  const int f0 = wave * seg < p.M ? wave * seg : p.M;
+  const int f1 = f0 + seg < p.M ? f0 + seg : p.M;
+  constexpr int kAhead = 8;  // ids a lane loads at once
+  auto walk = [&](auto step) {
+    for (int fb = f0; fb < f1; fb += 64 * kAhead) {
+      int key[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int f = fb + 64 * i + lane;
+        const int id = p.ids[f < f1 ? f : f1 - 1];
+        key[i] = id >= 0 && id < p.L ? id : p.L;
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (fb + 64 * i >= f1) break;
+        const uint64_t live = __ballot(fb + 64 * i + lane < f1);
+        const uint64_t same = same_key(key[i], nbits, live);
+        if (fb + 64 * i + lane < f1) step(fb + 64 * i + lane, key[i], bits_below(same), __builtin_popcountll(same));
+      }
+    }
+  };
+  walk([&](int, int key, int before, int total) {
+    if (before == 0) cnt[wave][key] += total;
+  });
+  __syncthreads();
+  // exclusive scan of the adapters' padded counts, one adapter a thread
+  int total = 0;
+  if (tid < p.L) {
+#pragma unroll
+    for (int w = 0; w < kGroupWaves; ++w) total += cnt[w][tid];
+  }
+  const int padded = (total + kLoraTile - 1) / kLoraTile * kLoraTile;
+  int incl = padded;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(incl, d, 64);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 63) wave_tot[wave] = incl;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kGroupWaves; ++w) {
+    before += w < wave ? wave_tot[w] : 0;
+    all += wave_tot[w];
+  }
+  // a list's rows, then the padding; the waves' counts become first positions
+  auto lay = [&](int key, int first, int count, int room) {
+    off[key] = first;
+    p.offsets[key] = first;
+    for (int i = first + count; i < first + room; ++i) p.sorted[i] = p.M;
+    int run = first;
+#pragma unroll
+    for (int w = 0; w < kGroupWaves; ++w) {
+      const int c = cnt[w][key];
+      cnt[w][key] = run;
+      run += c;
+    }
+  };
+  if (tid < p.L) lay(tid, before + incl - padded, total, padded);
+  if (tid == kGroupThreads - 1) {  // rows without an adapter
+    int none = 0;
+    for (int w = 0; w < kGroupWaves; ++w) none += cnt[w][p.L];
+    const int room = (none + kLoraTile - 1) / kLoraTile * kLoraTile;
+    lay(p.L, all, none, room);
+    off[p.L + 1] = all + room;
+    p.offsets[p.L + 1] = all + room;
   }
   __syncthreads();
-  return *count;
+  const int tiles = off[p.L + 1] / kLoraTile;
+  for (int b = tid; b < tiles; b += kGroupThreads) {
+    int lo = 0, hi = p.L;  // the last list that starts at or before the tile
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (off[mid] <= b * kLoraTile) lo = mid; else hi = mid - 1;
+    }
+    p.block_adapter[b] = lo;
+  }
+  walk([&](int row, int key, int before_me, int total_same) {
+    // every lane reads the running position before the first lane advances it
+    // (one wave: its LDS operations complete in order)
+    const int base = cnt[wave][key];
+    p.sorted[base + before_me] = row;
+    if (before_me == 0) cnt[wave][key] = base + total_same;
+  });
+}
+
+// ------------------------------------------------------------------ a workgroup's tile
+struct TileArgs {
+  const int32_t* ids;            // [M]
+  const int32_t* sorted;         // the grouping, or null: a small batch
+  const int32_t* block_adapter;
+  const int32_t* offsets;        // [L + 2]
+  int M, L;
+};
+struct Tile {
+  int rows[kLoraTile];  // rows past the last repeat the first (their results are dropped)
+  int key[kLoraSmallRows];
+  int wave_leaders[kLoraSmallRows / 64];
+  int count, adapter, first_rank;
+};
+
+// The tile's rows in LDS. Returns their number, 0 if there is no such tile.
+// A small batch: row t leads a tile if it is the 64 i-th row of its adapter;
+// the tiles count in the order of their leaders.
+__device__ __forceinline__ int find_tile(const TileArgs& p, Tile& sh, int tile) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  if (p.sorted) {
+    if (tile * kLoraTile >= p.offsets[p.L + 1]) return 0;
+    if (tid < kLoraTile) {
+      const int first = p.sorted[tile * kLoraTile];
+      const int row = p.sorted[tile * kLoraTile + tid];
+      sh.rows[tid] = row < p.M ? row : first;
+      const uint64_t live = __ballot(row < p.M);
+      if (tid == 0) {
+        sh.count = __builtin_popcountll(live);
+        sh.adapter = p.block_adapter[tile];
+      }
+    }
+    __syncthreads();
+    return sh.count;
+  }
+  int key = -1;
+  if (tid < p.M) {
+    const int id = p.ids[tid];
+    key = id >= 0 && id < p.L ? id : p.L;
+  }
+  if (tid < kLoraSmallRows) sh.key[tid] = key;
+  if (tid == 0) sh.count = 0;
+  __syncthreads();
+  int rank = 0;
+  for (int u = 0; u < p.M; u += 4) {
+    const int4 k = *(const int4*)(sh.key + u);
+    rank += (u < tid && k.x == key) + (u + 1 < tid && k.y == key) + (u + 2 < tid && k.z == key) +
+            (u + 3 < tid && k.w == key);
+  }
+  const bool leads = key >= 0 && rank % kLoraTile == 0;
+  const uint64_t leaders = __ballot(leads);
+  if (lane == 0 && wave < kLoraSmallRows / 64) sh.wave_leaders[wave] = __builtin_popcountll(leaders);
+  __syncthreads();
+  int before = bits_below(leaders), all = 0;
+#pragma unroll
+  for (int w = 0; w < kLoraSmallRows / 64; ++w) {
+    before += w < wave ? sh.wave_leaders[w] : 0;
+    all += sh.wave_leaders[w];
+  }
+  if (tile >= all) return 0;
+  if (leads && before == tile) {
+    sh.adapter = key;
+    sh.first_rank = rank;
+  }
+  __syncthreads();
+  const int at = rank - sh.first_rank;
+  if (key == sh.adapter && at >= 0 && at < kLoraTile) {
+    sh.rows[at] = tid;
+    atomicAdd(&sh.count, 1);
+  }
+  __syncthreads();
+  const int n = sh.count;
+  if (tid >= n && tid < kLoraTile) sh.rows[tid] = sh.rows[0];
+  __syncthreads();
+  return n;
 }
 
 // ------------------------------------------------------------------ down
+constexpr int kDownThreads = 512;
+constexpr int kDownWaves = kDownThreads / 64;
+
 struct DownArgs {
+  TileArgs tile;
   const void* u;              // [M, W]
   int64_t ldu;
   int W;
   const uint16_t* v;          // [L][r][ldv], zeros from W to ldv
   int64_t v_stride, ldv;
-  int r, M;
-  const int32_t* sorted;
-  const int32_t* block_adapter;
-  const int32_t* npp;
+  int r;
+  int splits, split_steps;    // 64-column steps per split
   float* part;                // [splits][M][r]
-  int split_steps;            // 64-column steps per split
+  float* h;                   // [M][r] or null: receives zeros for rows without an adapter
 };
 
-// part[split][row][j] = sum over the split's columns of v[j][w] * u[row][w].
+// The sum over the split's columns of v[j][w] * u[row][w], as four sums (of
+// waves i and i + 4 each) that the caller adds: red[i][row][j].
 // A step is 64 columns: lane (g, c) takes the 16 columns from 16 g of row c of
 // either operand, as two 8-column fragments, so four lanes read 128
-// consecutive bytes of a bf16 row. The waves take the split's steps in turn.
+// consecutive bytes of a bf16 row. The waves take the split's steps in turn,
+// with the next step's loads issued before the current one's products.
 template <typename TU, int RT, bool VecU, int NSUB>
-__device__ __forceinline__ void down_tile(const DownArgs& p, const int* rows, int adapter, float* red) {
+__device__ __forceinline__ void down_tile(const DownArgs& p, const Tile& sh, float* red) {
   constexpr int kRed = RT * 16 + 4;
+  constexpr bool kF32 = std::is_same<TU, float>::value;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
   const TU* urow[NSUB];
 #pragma unroll
-  for (int ts = 0; ts < NSUB; ++ts) urow[ts] = (const TU*)p.u + (int64_t)rows[ts * kSub + c] * p.ldu;
+  for (int ts = 0; ts < NSUB; ++ts) urow[ts] = (const TU*)p.u + (int64_t)sh.rows[ts * kSub + c] * p.ldu;
   const uint16_t* vrow[RT];
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     const int j = rt * 16 + c < p.r ? rt * 16 + c : p.r - 1;
-    vrow[rt] = p.v + adapter * p.v_stride + j * p.ldv;
+    vrow[rt] = p.v + sh.adapter * p.v_stride + j * p.ldv;
   }
   f32x4_t acc[RT][NSUB];
 #pragma unroll
@@ -148,50 +356,73 @@ __device__ __forceinline__ void down_tile(const DownArgs& p, const int* rows, in
   const int steps = (p.W + 63) / 64;
   const int s0 = blockIdx.y * p.split_steps;
   const int s1 = s0 + p.split_steps < steps ? s0 + p.split_steps : steps;
-  for (int s = s0 + wave; s < s1; s += kWaves) {
+  constexpr bool kAhead = RT <= (kF32 ? 2 : 4);  // two steps' loads fit in the registers
+  struct Frags {
+    bf16x8_t v[RT][2];
+    bf16x8_t u[kF32 ? 1 : NSUB][2];
+    float f[kF32 ? NSUB : 1][2][8];
+  };
+  auto load = [&](int s, Frags& x) {
     const int w = s * 64 + g * 16;
-    bf16x8_t vf[RT][2];
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
+    for (int hh = 0; hh < 2; ++hh) {
+      if constexpr (kF32) {
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) vf[rt][hh] = load8<true>(vrow[rt], w + 8 * hh, (int)p.ldv);
-    if constexpr (std::is_same<TU, float>::value) {
+        for (int ts = 0; ts < NSUB; ++ts) load8<VecU>((const float*)urow[ts], w + 8 * hh, p.W, x.f[ts][hh]);
+      } else {
 #pragma unroll
-      for (int ts = 0; ts < NSUB; ++ts)
+        for (int ts = 0; ts < NSUB; ++ts) x.u[ts][hh] = load8<VecU>((const uint16_t*)urow[ts], w + 8 * hh, p.W);
+      }
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          float f[8];
-          load8<VecU>(urow[ts], w + 8 * hh, p.W, f);
-          bf16x8_t parts[3];
-          split_parts<3>(f, parts);
+      for (int rt = 0; rt < RT; ++rt) x.v[rt][hh] = load8<true>(vrow[rt], w + 8 * hh, (int)p.ldv);
+    }
+  };
+  auto multiply = [&](const Frags& x) {
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+      for (int ts = 0; ts < NSUB; ++ts) {
+        if constexpr (kF32) {
+          bf16x8_t q[3];
+          split_parts<3>(x.f[ts][hh], q);
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-            for (int q = 0; q < 3; ++q) acc[rt][ts] = mfma16x16x32(vf[rt][hh], parts[q], acc[rt][ts]);
+            for (int i = 0; i < 3; ++i) acc[rt][ts] = mfma16x16x32(x.v[rt][hh], q[i], acc[rt][ts]);
+        } else {
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) acc[rt][ts] = mfma16x16x32(x.v[rt][hh], x.u[ts][hh], acc[rt][ts]);
         }
-    } else {
-      bf16x8_t uf[NSUB][2];
-#pragma unroll
-      for (int ts = 0; ts < NSUB; ++ts)
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) uf[ts][hh] = load8<VecU>(urow[ts], w + 8 * hh, p.W);
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-        for (int ts = 0; ts < NSUB; ++ts)
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt) acc[rt][ts] = mfma16x16x32(vf[rt][hh], uf[ts][hh], acc[rt][ts]);
+      }
+  };
+  int s = s0 + wave;
+  if (s < s1) {
+    Frags cur;
+    load(s, cur);
+    for (s += kDownWaves; s < s1; s += kDownWaves) {
+      if constexpr (kAhead) {
+        Frags next;
+        load(s, next);
+        multiply(cur);
+        cur = next;
+      } else {
+        multiply(cur);
+        load(s, cur);
+      }
     }
+    multiply(cur);
   }
-  // the waves' sums, in order; lane (g, c) holds ranks 16 rt + 4 g .. + 3 of row 16 ts + c
-  for (int w = 0; w < kWaves; ++w) {
-    if (wave == w) {
+  // lane (g, c) holds ranks 16 rt + 4 g .. + 3 of row 16 ts + c
+  float* mine = red + (wave & 3) * kLoraTile * kRed;
+#pragma unroll
+  for (int half = 1; half >= 0; --half) {
+    if (wave >> 2 == half) {
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
         for (int ts = 0; ts < NSUB; ++ts) {
-          f32x4_t* at = (f32x4_t*)(red + (ts * kSub + c) * kRed + rt * 16 + 4 * g);
-          *at = w == 0 ? acc[rt][ts] : *at + acc[rt][ts];
+          f32x4_t* at = (f32x4_t*)(mine + (ts * kSub + c) * kRed + rt * 16 + 4 * g);
+          *at = half ? acc[rt][ts] : *at + acc[rt][ts];
         }
     }
     __syncthreads();
@@ -199,169 +430,119 @@ __device__ __forceinline__ void down_tile(const DownArgs& p, const int* rows, in
 }
 
 template <typename TU, int RT, bool VecU>
-__global__ __launch_bounds__(kThreads) void lora_down_kernel(DownArgs p) {
+__global__ __launch_bounds__(kDownThreads) void lora_down_kernel(DownArgs p) {
   constexpr int kRed = RT * 16 + 4;
-  __shared__ int rows[kLoraTile];
-  __shared__ int count;
-  __shared__ __align__(16) float red[kLoraTile * kRed];
-  const int tile = blockIdx.x;
-  if (tile * kLoraTile >= *p.npp) return;
-  const int n = load_tile_rows(p.sorted, tile, p.M, rows, &count);
-  const int adapter = p.block_adapter[tile];
-  if (n <= 16) down_tile<TU, RT, VecU, 1>(p, rows, adapter, red);
-  else if (n <= 32) down_tile<TU, RT, VecU, 2>(p, rows, adapter, red);
-  else down_tile<TU, RT, VecU, 4>(p, rows, adapter, red);
-  const int quads = p.r / 4;
-  for (int i = threadIdx.x; i < n * quads; i += kThreads) {
-    const int t = i / quads, j = (i % quads) * 4;
-    *(float4*)(p.part + ((int64_t)blockIdx.y * p.M + rows[t]) * p.r + j) = *(const float4*)(red + t * kRed + j);
+  constexpr int kQuads = RT * 4;
+  __shared__ __align__(16) Tile sh;
+  __shared__ __align__(16) float red[4 * kLoraTile * kRed];
+  const int tid = threadIdx.x;
+  const int n = find_tile(p.tile, sh, blockIdx.x);
+  if (n == 0) return;
+  if (sh.adapter == p.tile.L) {  // rows without an adapter
+    if (p.h && blockIdx.y == 0)
+      for (int i = tid; i < n * p.r; i += kDownThreads) p.h[(int64_t)sh.rows[i / p.r] * p.r + i % p.r] = 0.0f;
+    return;
+  }
+  if (n <= 16) down_tile<TU, RT, VecU, 1>(p, sh, red);
+  else if (n <= 32) down_tile<TU, RT, VecU, 2>(p, sh, red);
+  else down_tile<TU, RT, VecU, 4>(p, sh, red);
+  float* part = p.part + (int64_t)blockIdx.y * p.tile.M * p.r;
+  for (int i = tid; i < n * kQuads; i += kDownThreads) {
+    const int t = i / kQuads, j = i % kQuads * 4;
+    if (j >= p.r) continue;
+    const f32x4_t* at = (const f32x4_t*)(red + t * kRed + j);
+    constexpr int kNext = kLoraTile * kRed / 4;
+    *(f32x4_t*)(part + (int64_t)sh.rows[t] * p.r + j) = (at[0] + at[kNext]) + (at[2 * kNext] + at[3 * kNext]);
   }
 }
 
 // ------------------------------------------------------------------ up
 struct UpArgs {
-  const float* part;          // [splits][M][r]
-  int splits, M, r, N, L;
-  const int32_t* ids;         // [M]
-  const int32_t* sorted;
-  const int32_t* block_adapter;
-  const int32_t* npp;
-  int tiles;                  // grouping tiles; workgroups past them copy rows without an adapter
+  TileArgs tile;
+  int r, N;
+  const float* part;          // [splits][M][r]: the factor's partial sums
+  int splits;
   const float* scales;        // [L] or null
+  float* h;                   // [M, r] or null, receives the sums
   const uint16_t* b;          // [L][N][r]
   const void* base;           // [M, N] or null
   int64_t ld_base;
   void* out;                  // [M, N]
   int64_t ld_out;
-  float* h;                   // [M, r] or null: receives the sums of the parts
-  int n_block;                // columns per workgroup, a multiple of 256
+  int n_block;                // columns per workgroup
 };
 
+// NT consecutive columns from n of a row (fp32: 4, bf16: 8: 16 bytes).
 template <typename TO, bool Vec>
-__device__ __forceinline__ void load_base(const TO* base, int n, int N, float (&v)[16]) {
-  if constexpr (std::is_same<TO, float>::value) {
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      if constexpr (Vec) {
-        if (n + i < N) {
-          const float4 x = *(const float4*)(base + n + i);
-          v[i] = x.x; v[i + 1] = x.y; v[i + 2] = x.z; v[i + 3] = x.w;
-        }
-      } else {
-#pragma unroll
-        for (int q = i; q < i + 4; ++q)
-          if (n + q < N) v[q] = base[n + q];
-      }
-    }
+__device__ __forceinline__ uint4 load_cols(const TO* row, int n, int N) {
+  constexpr int NT = 16 / sizeof(TO);
+  uint32_t d[4] = {0, 0, 0, 0};
+  if constexpr (Vec) {
+    if (n < N) return *(const uint4*)(row + n);
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; i += 8) {
-      if constexpr (Vec) {
-        if (n + i < N) {
-          const uint4 x = *(const uint4*)(base + n + i);
-          const uint32_t d[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            v[i + 2 * q] = __uint_as_float(d[q] << 16);
-            v[i + 2 * q + 1] = __uint_as_float(d[q] & 0xffff0000u);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int q = i; q < i + 8; ++q)
-          if (n + q < N) v[q] = bf16_value(base[n + q]);
+    for (int i = 0; i < NT; ++i) {
+      if (n + i < N) {
+        if constexpr (sizeof(TO) == 4) d[i] = __float_as_uint(row[n + i]);
+        else d[i / 2] |= (uint32_t)row[n + i] << (16 * (i & 1));
       }
     }
   }
+  return make_uint4(d[0], d[1], d[2], d[3]);
 }
 template <typename TO, bool Vec>
-__device__ __forceinline__ void store_out(TO* out, int n, int N, const float (&v)[16]) {
-  if constexpr (std::is_same<TO, float>::value) {
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      if constexpr (Vec) {
-        if (n + i < N) *(float4*)(out + n + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-      } else {
-#pragma unroll
-        for (int q = i; q < i + 4; ++q)
-          if (n + q < N) out[n + q] = v[q];
-      }
-    }
+__device__ __forceinline__ void store_cols(TO* row, int n, int N, uint4 v) {
+  constexpr int NT = 16 / sizeof(TO);
+  if constexpr (Vec) {
+    if (n < N) *(uint4*)(row + n) = v;
   } else {
+    const uint32_t d[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 16; i += 8) {
-      if constexpr (Vec) {
-        uint32_t d[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) d[q] = bf16_bits(v[i + 2 * q]) | bf16_bits(v[i + 2 * q + 1]) << 16;
-        if (n + i < N) *(uint4*)(out + n + i) = make_uint4(d[0], d[1], d[2], d[3]);
-      } else {
-#pragma unroll
-        for (int q = i; q < i + 8; ++q)
-          if (n + q < N) out[n + q] = (uint16_t)bf16_bits(v[q]);
+    for (int i = 0; i < NT; ++i) {
+      if (n + i < N) {
+        if constexpr (sizeof(TO) == 4) row[n + i] = __uint_as_float(d[i]);
+        else row[n + i] = (uint16_t)(d[i / 2] >> (16 * (i & 1)));
       }
     }
   }
 }
 
-// Rows without an adapter: out = base (nothing to do in place), or zeros; h = 0.
-template <typename TO>
-__device__ void copy_rows(const UpArgs& p) {
-  const int t0 = (blockIdx.x - p.tiles) * kLoraTile;
+// Rows without an adapter: out = base (nothing to do in place), or zeros.
+template <typename TO, bool Vec>
+__device__ __forceinline__ void copy_rows(const UpArgs& p, const Tile& sh, int n) {
+  constexpr int NT = 16 / sizeof(TO);
+  if (p.base == p.out) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int n0 = blockIdx.y * p.n_block;
-  const int n1 = n0 + p.n_block < p.N ? n0 + p.n_block : p.N;
-  const bool in_place = p.base == p.out;
-  for (int i = wave; i < kLoraTile && t0 + i < p.M; i += kWaves) {
-    const int row = t0 + i;
-    const int a = p.ids[row];
-    if (a >= 0 && a < p.L) continue;
-    if (!in_place) {
-      TO* out = (TO*)p.out + (int64_t)row * p.ld_out;
-      const TO* base = p.base ? (const TO*)p.base + (int64_t)row * p.ld_base : nullptr;
-      for (int n = n0 + lane; n < n1; n += 64) out[n] = base ? base[n] : TO(0);
-    }
-    if (p.h && blockIdx.y == 0)
-      for (int j = lane; j < p.r; j += 64) p.h[(int64_t)row * p.r + j] = 0.0f;
+  const int n0 = blockIdx.y * p.n_block, n1 = n0 + p.n_block < p.N ? n0 + p.n_block : p.N;
+  for (int t = wave; t < n; t += kWaves) {
+    TO* out = (TO*)p.out + (int64_t)sh.rows[t] * p.ld_out;
+    const TO* base = (const TO*)p.base + (int64_t)sh.rows[t] * p.ld_base;
+    for (int col = n0 + lane * NT; col < n1; col += 64 * NT)
+      store_cols<TO, Vec>(out, col, p.N, p.base ? load_cols<TO, Vec>(base, col, p.N) : make_uint4(0, 0, 0, 0));
   }
 }
 
-// out[row][n] = base[row][n] + sum_j b[n][j] * (scale * h[row][j]).
-// The factor's bf16 parts are laid one after another along the contraction:
-// 8-wide chunk number q of a lane's fragments is chunk q % (r / 8) of part
-// q / (r / 8), so ranks 8 and 16 fill one 32-wide matrix-core step with their
-// parts. A wave's group is 64 columns: matrix-core tile i takes columns 4 m + i
-// (m its row), so that a lane ends with 16 consecutive columns of one row.
-template <typename TO, int RC, bool Vec>
-__global__ __launch_bounds__(kThreads) void lora_up_kernel(UpArgs p) {
-  constexpr int NP = std::is_same<TO, float>::value ? 3 : 2;
-  constexpr int kChunks = RC / 8;                       // 8-wide chunks of a part
-  constexpr int kSteps = (NP * kChunks + 3) / 4;        // 32-wide steps
-  constexpr int kFrags = kChunks >= 4 ? kChunks / 4 : 1;  // different steps of b
-  constexpr int kPitch = RC + 8;                        // elements, 16-byte multiple
-  __shared__ int rows[kLoraTile];
-  __shared__ int count;
-  __shared__ __align__(16) uint16_t parts[NP][kLoraTile][kPitch];
-  if ((int)blockIdx.x >= p.tiles) {
-    copy_rows<TO>(p);
-    return;
-  }
-  const int tile = blockIdx.x;
-  if (tile * kLoraTile >= *p.npp) return;
-  const int n = load_tile_rows(p.sorted, tile, p.M, rows, &count);
-  const int adapter = p.block_adapter[tile];
-  const int nsub = (n + kSub - 1) / kSub;
-  const float scale = p.scales ? p.scales[adapter] : 1.0f;
-  for (int i = threadIdx.x; i < nsub * kSub * (RC / 4); i += kThreads) {
-    const int t = i / (RC / 4), j = (i % (RC / 4)) * 4;
+constexpr int up_np(bool f32) { return f32 ? 3 : 2; }
+
+// The tile's factor in LDS: the sums of the partial sums, scaled, as bf16 parts.
+template <int RC, int NP>
+__device__ __forceinline__ void up_factor(const UpArgs& p, const Tile& sh, int n, uint16_t* lds) {
+  constexpr int kPitch = RC + 8;
+  const int tid = threadIdx.x;
+  const int rows = (n + kSub - 1) / kSub * kSub;
+  const float scale = p.scales ? p.scales[sh.adapter] : 1.0f;
+  const int64_t split_size = (int64_t)p.tile.M * p.r;
+  for (int i = tid; i < rows * (RC / 4); i += kThreads) {
+    const int t = i / (RC / 4), j = i % (RC / 4) * 4;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (t < n && j < p.r) {
-      const float* at = p.part + (int64_t)rows[t] * p.r + j;
+      const int64_t at = (int64_t)sh.rows[t] * p.r + j;
+#pragma unroll 8
       for (int s = 0; s < p.splits; ++s) {
-        const float4 x = *(const float4*)(at + (int64_t)s * p.M * p.r);
+        const float4 x = *(const float4*)(p.part + s * split_size + at);
         v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
       }
-      if (p.h && blockIdx.y == 0) *(float4*)(p.h + (int64_t)rows[t] * p.r + j) = v;
+      if (p.h && blockIdx.y == 0) *(float4*)(p.h + at) = v;
     }
     float f[4] = {v.x * scale, v.y * scale, v.z * scale, v.w * scale};
 #pragma unroll
@@ -372,280 +553,443 @@ __global__ __launch_bounds__(kThreads) void lora_up_kernel(UpArgs p) {
         bits[e] = bf16_bits(f[e]);
         f[e] -= bf16_value(bits[e]);
       }
-      *(uint2*)&parts[q][t][j] = make_uint2(bits[0] | bits[1] << 16, bits[2] | bits[3] << 16);
+      *(uint2*)(lds + (q * kLoraTile + t) * kPitch + j) = make_uint2(bits[0] | bits[1] << 16, bits[2] | bits[3] << 16);
     }
   }
-  __syncthreads();
+}
 
+// out[row][n] = base[row][n] + sum_j b[n][j] * factor[row][j].
+// The factor's bf16 parts are laid one after another along the contraction:
+// 8-wide chunk number q of a lane's fragments is chunk q % (r / 8) of part
+// q / (r / 8), so ranks 8 and 16 fill one 32-wide matrix-core step with their
+// parts. A wave takes 16 * NT columns: matrix-core tile i has the columns
+// c * NT + i (c its column), so a lane ends with NT consecutive columns, 16
+// bytes, of four rows, and 16 lanes read and write 256 consecutive bytes.
+// What does not depend on the factor is loaded before it is made.
+template <typename TO, int RC, bool Vec, int NSUB>
+__device__ __forceinline__ void up_tile(const UpArgs& p, const Tile& sh, int n, uint16_t* lds) {
+  constexpr int NT = 16 / sizeof(TO);
+  constexpr int NP = sizeof(TO) == 4 ? 3 : 2;
+  constexpr int kChunks = RC / 8;                         // 8-wide chunks of a part
+  constexpr int kSteps = (NP * kChunks + 3) / 4;          // 32-wide steps
+  constexpr int kFrags = kChunks >= 4 ? kChunks / 4 : 1;  // different steps of b
+  constexpr int kPitch = RC + 8;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
-  const uint16_t* b = p.b + (int64_t)adapter * p.N * p.r;
+  const uint16_t* b = p.b + (int64_t)sh.adapter * p.N * p.r;
   const int n_end = (int)(blockIdx.y + 1) * p.n_block < p.N ? (int)(blockIdx.y + 1) * p.n_block : p.N;
-  for (int n0 = blockIdx.y * p.n_block + wave * 64; n0 < n_end; n0 += kWaves * 64) {
-    bf16x8_t bf[4][kFrags];
+  int n0 = blockIdx.y * p.n_block + wave * 16 * NT;
+  bf16x8_t bf[NT][kFrags];
+  uint4 base[4];
+  auto load_b = [&](int col) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int col = n0 + 4 * c + i < p.N ? n0 + 4 * c + i : p.N - 1;
+    for (int i = 0; i < NT; ++i) {
+      const uint16_t* row = b + (int64_t)(col + i < p.N ? col + i : p.N - 1) * p.r;
 #pragma unroll
-      for (int k = 0; k < kFrags; ++k) bf[i][k] = load8<true>(b + (int64_t)col * p.r, ((k * 4 + g) % kChunks) * 8, p.r);
+      for (int k = 0; k < kFrags; ++k) bf[i][k] = load8<true>(row, ((k * 4 + g) % kChunks) * 8, p.r);
     }
+  };
+  auto load_base = [&](int ts, int col) {
 #pragma unroll
-    for (int ts = 0; ts < 4; ++ts) {
-      if (ts >= nsub) break;
-      f32x4_t acc[4];
+    for (int q = 0; q < 4; ++q)
+      base[q] = p.base ? load_cols<TO, Vec>((const TO*)p.base + (int64_t)sh.rows[ts * kSub + 4 * g + q] * p.ld_base, col,
+                                            p.N)
+                       : make_uint4(0, 0, 0, 0);
+  };
+  if (n0 < n_end) {
+    load_b(n0 + c * NT);
+    load_base(0, n0 + c * NT);
+  }
+  up_factor<RC, NP>(p, sh, n, lds);
+  __syncthreads();
+  while (n0 < n_end) {
+    const int col = n0 + c * NT;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int ts = 0; ts < NSUB; ++ts) {
+      f32x4_t acc[NT];
+      uint4 in[4] = {base[0], base[1], base[2], base[3]};
+      if (ts + 1 < NSUB) load_base(ts + 1, col);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) acc[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int k = 0; k < kSteps; ++k) {
         const int chunk = k * 4 + g;
         const int q = chunk / kChunks;
-        bf16x8_t hf = as_bf16x8(*(const uint4*)&parts[q < NP ? q : 0][ts * kSub + c][(chunk % kChunks) * 8]);
+        bf16x8_t hf = as_bf16x8(
+            *(const uint4*)(lds + ((q < NP ? q : 0) * kLoraTile + ts * kSub + c) * kPitch + (chunk % kChunks) * 8));
         if (kSteps * 4 > NP * kChunks && q >= NP) hf = as_bf16x8(make_uint4(0, 0, 0, 0));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] = mfma16x16x32(bf[i][k % kFrags], hf, acc[i]);
+        for (int i = 0; i < NT; ++i) acc[i] = mfma16x16x32(hf, bf[i][k % kFrags], acc[i]);
       }
-      const int t = ts * kSub + c;
-      if (t < n) {
-        const int col = n0 + 16 * g;
-        float v[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = 0.0f;
-        if (p.base) load_base<TO, Vec>((const TO*)p.base + (int64_t)rows[t] * p.ld_base, col, p.N, v);
+      for (int q = 0; q < 4; ++q) {
+        const int t = ts * kSub + 4 * g + q;
+        const uint32_t x[4] = {in[q].x, in[q].y, in[q].z, in[q].w};
+        uint32_t d[4];
+        if constexpr (sizeof(TO) == 4) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < 4; ++i) d[i] = __float_as_uint(__uint_as_float(x[i]) + acc[i][q]);
+        } else {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) v[4 * q + i] += acc[i][q];
-        store_out<TO, Vec>((TO*)p.out + (int64_t)rows[t] * p.ld_out, col, p.N, v);
+          for (int i = 0; i < 4; ++i)
+            d[i] = bf16_bits(__uint_as_float(x[i] << 16) + acc[2 * i][q]) |
+                   bf16_bits(__uint_as_float(x[i] & 0xffff0000u) + acc[2 * i + 1][q]) << 16;
+        }
+        if (t < n)
+          store_cols<TO, Vec>((TO*)p.out + (int64_t)sh.rows[t] * p.ld_out, col, p.N, make_uint4(d[0], d[1], d[2], d[3]));
       }
+    }
+    n0 += kWaves * 16 * NT;
+    if (n0 < n_end) {
+      load_b(n0 + c * NT);
+      load_base(0, n0 + c * NT);
     }
   }
 }
 
-// ------------------------------------------------------------------ transpose
-// in [L][R][C] -> out [L][C][pitch], columns R .. pitch zero, for the adapters
-// that have rows in the batch.
-__global__ __launch_bounds__(kThreads) void lora_transpose_kernel(const uint16_t* __restrict__ in, int R, int C,
-                                                                  int64_t pitch, const int32_t* __restrict__ offsets,
-                                                                  uint16_t* __restrict__ out) {
-  __shared__ uint16_t tile[64][66];
-  const int l = blockIdx.z;
-  if (offsets[l] == offsets[l + 1]) return;
-  const int64_t src = (int64_t)l * R * C, dst = (int64_t)l * C * pitch;
-  const int c0 = blockIdx.x * 64, r0 = blockIdx.y * 64;
-  const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
-  for (int i = y; i < 64; i += kWaves)
-    tile[i][x] = (r0 + i < R && c0 + x < C) ? in[src + (int64_t)(r0 + i) * C + c0 + x] : (uint16_t)0;
-  __syncthreads();
-  for (int i = y; i < 64; i += kWaves)
-    if (c0 + i < C && r0 + x < pitch) out[dst + (int64_t)(c0 + i) * pitch + r0 + x] = tile[x][i];
+template <typename TO, int RC, bool Vec>
+__global__ __launch_bounds__(kThreads) void lora_up_kernel(UpArgs p) {
+  constexpr int NP = sizeof(TO) == 4 ? 3 : 2;
+  __shared__ __align__(16) Tile sh;
+  __shared__ __align__(16) uint16_t lds[NP * kLoraTile * (RC + 8)];
+  const int n = find_tile(p.tile, sh, blockIdx.x);
+  if (n == 0) return;
+  if (sh.adapter == p.tile.L) {
+    copy_rows<TO, Vec>(p, sh, n);
+    return;
+  }
+  if (n <= 16) up_tile<TO, RC, Vec, 1>(p, sh, n, lds);
+  else if (n <= 32) up_tile<TO, RC, Vec, 2>(p, sh, n, lds);
+  else up_tile<TO, RC, Vec, 4>(p, sh, n, lds);
 }
 
-// ------------------------------------------------------------------ finish
-struct FinishArgs {
-  const float* part;          // [splits][M][r]
-  int splits, M, r;
+// ------------------------------------------------------------------ prep
+struct PrepArgs {
+  TileArgs tile;
+  const uint16_t* a;          // [L][r][K]
+  const uint16_t* b;          // [L][N][r]
+  int K, N, r;
+  int64_t n_pad;
+  uint16_t* at;               // [L][K][r], or null
+  uint16_t* bt;               // [L][r][n_pad], zeros from N
+  int a_blocks, b_blocks;     // workgroups per adapter
   const float* h;             // [M][r]
-  const float* scales;        // [L] or null
-  const int32_t* sorted;
-  const int32_t* block_adapter;
-  const int32_t* npp;
+  const float* scales;
   int64_t cap;
-  float* dh;                  // [M][r]
-  uint16_t* dht;              // [3][r][cap]
   uint16_t* ht;               // [3][r][cap]
 };
 
-// dh = scale * (sum of its parts), and the three bf16 parts of dh and of
-// scale * h at [part][rank][position in the grouping], zeros at the padding.
-__global__ __launch_bounds__(kThreads) void lora_finish_kernel(FinishArgs p) {
-  __shared__ int rows[kLoraTile];
-  __shared__ int count;
-  __shared__ float val[kLoraTile][kLoraMaxRank + 1];
-  const int tile = blockIdx.x;
-  if (tile * kLoraTile >= *p.npp) return;
-  const int n = load_tile_rows(p.sorted, tile, p.M, rows, &count);
-  const float scale = p.scales ? p.scales[p.block_adapter[tile]] : 1.0f;
-  for (int side = 0; side < 2; ++side) {
-    for (int i = threadIdx.x; i < kLoraTile * p.r; i += kThreads) {
-      const int t = i / p.r, j = i % p.r;
-      float v = 0.0f;
-      if (t < n) {
-        const int64_t at = (int64_t)rows[t] * p.r + j;
-        if (side == 0) {
-          for (int s = 0; s < p.splits; ++s) v += p.part[(int64_t)s * p.M * p.r + at];
-          v *= scale;
-          p.dh[at] = v;
-        } else {
-          v = p.h[at] * scale;
-        }
-      }
-      val[t][j] = v;
-    }
-    __syncthreads();
-    uint16_t* out = side == 0 ? p.dht : p.ht;
-    for (int i = threadIdx.x; i < kLoraTile * p.r; i += kThreads) {
-      const int t = i & 63, j = i >> 6;
-      float v = val[t][j];
-#pragma unroll
-      for (int q = 0; q < 3; ++q) {
-        const uint32_t bits = bf16_bits(v);
-        v -= bf16_value(bits);
-        out[((int64_t)q * p.r + j) * p.cap + (int64_t)tile * kLoraTile + t] = (uint16_t)bits;
-      }
-    }
-    __syncthreads();
+// One 64 x 64 block of in [R][C] (C a multiple of 8) to out [C][pitch], rows
+// from R on as zeros up to the pitch.
+__device__ __forceinline__ void transpose_block(const uint16_t* __restrict__ in, int R, int C, int64_t pitch,
+                                                uint16_t* __restrict__ out, int r0, int c0, uint16_t* lds) {
+  constexpr int kPitch = 64 + 8;
+  const int tid = threadIdx.x;
+  for (int i = tid; i < 64 * 8; i += kThreads) {
+    const int row = i >> 3, col = (i & 7) * 8;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (r0 + row < R && c0 + col < C) v = *(const uint4*)(in + (int64_t)(r0 + row) * C + c0 + col);
+    *(uint4*)(lds + row * kPitch + col) = v;
   }
+  __syncthreads();
+  for (int i = tid; i < 64 * 8; i += kThreads) {
+    const int col = i >> 3, row = (i & 7) * 8;
+    if (c0 + col >= C || r0 + row >= pitch) continue;
+    uint32_t d[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      d[e] = lds[(row + 2 * e) * kPitch + col] | (uint32_t)lds[(row + 2 * e + 1) * kPitch + col] << 16;
+    *(uint4*)(out + (int64_t)(c0 + col) * pitch + r0 + row) = make_uint4(d[0], d[1], d[2], d[3]);
+  }
+}
+
+// The three bf16 parts of scale * (sum of the splits of part) at [part][rank]
+// [position in the grouping], zeros at the tile's padding; dh, if asked for,
+// receives the scaled sums.
+__device__ __forceinline__ void rank_major(const TileArgs& tile, const Tile& sh, int n, int index, int r,
+                                           const float* part, int splits, const float* scales, float* dh, uint16_t* vt,
+                                           int64_t cap, float* lds) {
+  const int tid = threadIdx.x;
+  const float scale = scales ? scales[sh.adapter] : 1.0f;
+  const int pitch = r + 4, quads = r / 4;
+  for (int i = tid; i < kLoraTile * quads; i += kThreads) {
+    const int t = i / quads, j = i % quads * 4;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (t < n) {
+      const int64_t at = (int64_t)sh.rows[t] * r + j;
+#pragma unroll 4
+      for (int s = 0; s < splits; ++s) {
+        const float4 x = *(const float4*)(part + (int64_t)s * tile.M * r + at);
+        v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+      }
+      v = make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
+      if (dh) *(float4*)(dh + at) = v;
+    }
+    *(float4*)(lds + t * pitch + j) = v;
+  }
+  __syncthreads();
+  for (int i = tid; i < r * 8; i += kThreads) {
+    const int j = i >> 3, t = (i & 7) * 8;
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = lds[(t + e) * pitch + j];
+    bf16x8_t q[3];
+    split_parts<3>(f, q);
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+      *(uint4*)(vt + ((int64_t)e * r + j) * cap + (int64_t)index * kLoraTile + t) = __builtin_bit_cast(uint4, q[e]);
+  }
+}
+
+// blockIdx.y: an adapter, whose weights are transposed if it has rows in the
+// batch; past the adapters: tiles, whose h is laid out rank-major.
+__global__ __launch_bounds__(kThreads) void lora_prep_kernel(PrepArgs p) {
+  __shared__ __align__(16) Tile sh;
+  __shared__ __align__(16) float lds[kLoraTile * (kLoraMaxRank + 4)];
+  const int tid = threadIdx.x;
+  if ((int)blockIdx.y < p.tile.L) {
+    const int l = blockIdx.y;
+    if (p.tile.offsets[l] == p.tile.offsets[l + 1]) return;
+    int i = blockIdx.x;
+    if (i < p.a_blocks) {
+      const int across = (p.K + 63) / 64;
+      const int64_t at = (int64_t)l * p.r * p.K;
+      transpose_block(p.a + at, p.r, p.K, p.r, p.at + at, i / across * 64, i % across * 64, (uint16_t*)lds);
+    } else if ((i -= p.a_blocks) < p.b_blocks) {
+      const int down = (int)((p.n_pad + 63) / 64);
+      transpose_block(p.b + (int64_t)l * p.N * p.r, p.N, p.r, p.n_pad, p.bt + l * p.r * p.n_pad, i % down * 64,
+                      i / down * 64, (uint16_t*)lds);
+    }
+    return;
+  }
+  const int tile = (blockIdx.y - p.tile.L) * gridDim.x + blockIdx.x;
+  const int n = find_tile(p.tile, sh, tile);
+  if (n == 0 || sh.adapter == p.tile.L) return;
+  rank_major(p.tile, sh, n, tile, p.r, p.h, 1, p.scales, nullptr, p.ht, p.cap, lds);
+}
+
+// dh: the sum of its splits, scaled, as it is and rank-major.
+struct JoinArgs {
+  TileArgs tile;
+  int r, splits;
+  const float* part;          // [splits][M][r]
+  const float* scales;
+  float* dh;                  // [M][r]
+  int64_t cap;
+  uint16_t* vt;               // [3][r][cap]
+};
+__global__ __launch_bounds__(kThreads) void lora_join_kernel(JoinArgs p) {
+  __shared__ __align__(16) Tile sh;
+  __shared__ __align__(16) float lds[kLoraTile * (kLoraMaxRank + 4)];
+  const int n = find_tile(p.tile, sh, blockIdx.x);
+  if (n == 0 || sh.adapter == p.tile.L) return;
+  rank_major(p.tile, sh, n, blockIdx.x, p.r, p.part, p.splits, p.scales, p.dh, p.vt, p.cap, lds);
 }
 
 // ------------------------------------------------------------------ outer
 struct OuterArgs {
   const void* u;              // [M, W]
   int64_t ldu;
-  int W, r, M;
+  int W, r, M, L;
   const uint16_t* vt;         // [3][r][cap]
   int64_t cap;
   const int32_t* sorted;
   const int32_t* block_adapter;
-  const int32_t* offsets;     // [L + 1]
-  const int32_t* npp;
-  float* out;                 // [L][r][W], or [L][W][r] (RankMinor)
+  const int32_t* offsets;     // [L + 2]
+  float* out;                 // [L][r][W], or [L][W][r] (rank_minor)
   float* slots;               // [2 * chunks] of the same shape
   int chunk;                  // positions per workgroup, a multiple of 64
+  bool rank_minor;
 };
 
 // sum over an adapter's rows of u[row][w] * v[row][j], for 128 columns and up
-// to 64 ranks a wave. A step takes 32 positions: lane (g, c) loads 8 columns
-// from 8 c of its 8 rows and transposes that 8 x 8 block in registers (the
-// contraction runs over rows). The positions are cut into chunks whatever the
-// adapters' lengths, so the work is even; sums of an adapter within one chunk
-// go to the output, those of one that crosses the chunk's start or end to
+// to 64 ranks a workgroup. A step takes 32 positions: lane (g, c) loads 8
+// columns from 8 c of its 8 rows and transposes that 8 x 8 block in registers
+// (the contraction runs over rows); the four waves take an adapter's steps in
+// turn and join their sums in LDS. The positions are cut into chunks whatever
+// the adapters' lengths, so the work is even; sums of an adapter within one
+// chunk go to the output, those of one that crosses the chunk's start or end to
 // slots 2 c or 2 c + 1, which the reduce kernel adds in order.
-template <typename TU, int JT, bool VecU, bool RankMinor>
+template <typename TU, int JT, bool VecU>
 __global__ __launch_bounds__(kThreads) void lora_outer_kernel(OuterArgs p) {
+  constexpr bool kF32 = std::is_same<TU, float>::value;
+  // the next step's loads go out before this one's products where the
+  // registers hold both (fp32 columns take four times a bf16 step's)
+  constexpr bool kAhead = JT == 1 || (!kF32 && (VecU || JT == 2));
+  constexpr int kVecs = 8 * JT;                         // accumulators of a wave
+  constexpr int kRound = kVecs < 16 ? kVecs : 16;       // of them in LDS at a time
+  constexpr int kPiece = 1024;                          // positions whose rows are in LDS at a time
+  __shared__ f32x4_t joined[kWaves][kRound][64];
+  __shared__ __align__(16) int rows_lds[kPiece];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
-  const int w0 = (blockIdx.x * kWaves + wave) * 128;
+  const int w0 = blockIdx.x * 128;
   const int j0 = blockIdx.z * 64;
-  const int npp = *p.npp;
+  const int npp = p.offsets[p.L];
   const int p0 = blockIdx.y * p.chunk;
-  if (w0 >= p.W || p0 >= npp) return;
+  if (p0 >= npp) return;
   const int p1 = p0 + p.chunk < npp ? p0 + p.chunk : npp;
   f32x4_t acc[8][JT];
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-#pragma unroll
-    for (int jt = 0; jt < JT; ++jt) acc[i][jt] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-  auto flush = [&](int adapter) {
-    const int o0 = p.offsets[adapter], o1 = p.offsets[adapter + 1];
-    const int64_t size = (int64_t)p.r * p.W;
-    float* out = (o0 >= p0 && o1 <= p0 + p.chunk) ? p.out + adapter * size
-                                                  : p.slots + (2 * (int64_t)blockIdx.y + (o0 < p0 ? 0 : 1)) * size;
+  struct Frags {
+    uint32_t d[kF32 ? 1 : 8][4];
+    float f[kF32 ? 8 : 1][8];
+    bf16x8_t v[JT][3];
+  };
+  auto load = [&](int pos, int piece, Frags& x) {
+    const int4 ra = *(const int4*)(rows_lds + pos - piece + 8 * g);
+    const int4 rb = *(const int4*)(rows_lds + pos - piece + 8 * g + 4);
+    const int rows[8] = {ra.x, ra.y, ra.z, ra.w, rb.x, rb.y, rb.z, rb.w};
 #pragma unroll
-    for (int jt = 0; jt < JT; ++jt) {
+    for (int t = 0; t < 8; ++t) {
+      const bool live = rows[t] < p.M;
+      const TU* row = (const TU*)p.u + (int64_t)(live ? rows[t] : 0) * p.ldu;
+      if constexpr (kF32) {
+        load8<VecU>((const float*)row, w0 + 8 * c, p.W, x.f[t]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if constexpr (RankMinor) {
-          const int w = w0 + 8 * c + i, j = j0 + 16 * jt + 4 * g;
-          if (w < p.W && j < p.r) *(f32x4_t*)(out + (int64_t)w * p.r + j) = acc[i][jt];
-        } else {
-          const int j = j0 + 16 * jt + c;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int w = w0 + 32 * g + 8 * q + i;
-            if (w < p.W && j < p.r) out[(int64_t)j * p.W + w] = acc[i][jt][q];
-          }
-        }
-        acc[i][jt] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = 0; i < 8; ++i) x.f[t][i] = live ? x.f[t][i] : 0.0f;
+      } else {
+        const uint4 v = __builtin_bit_cast(uint4, load8<VecU>((const uint16_t*)row, w0 + 8 * c, p.W));
+        x.d[t][0] = live ? v.x : 0; x.d[t][1] = live ? v.y : 0; x.d[t][2] = live ? v.z : 0; x.d[t][3] = live ? v.w : 0;
       }
     }
-  };
-
-  int adapter = p.block_adapter[p0 / kLoraTile];
-  for (int pos = p0; pos < p1; pos += 32) {
-    const int a = p.block_adapter[pos / kLoraTile];
-    if (a != adapter) {
-      flush(adapter);
-      adapter = a;
-    }
-    const int4 ra = *(const int4*)(p.sorted + pos + 8 * g), rb = *(const int4*)(p.sorted + pos + 8 * g + 4);
-    const int rows[8] = {ra.x, ra.y, ra.z, ra.w, rb.x, rb.y, rb.z, rb.w};
-    bf16x8_t vf[JT][3];
 #pragma unroll
     for (int jt = 0; jt < JT; ++jt) {
       const int j = j0 + 16 * jt + c < p.r ? j0 + 16 * jt + c : p.r - 1;
 #pragma unroll
       for (int q = 0; q < 3; ++q)
-        vf[jt][q] = as_bf16x8(*(const uint4*)(p.vt + ((int64_t)q * p.r + j) * p.cap + pos + 8 * g));
+        x.v[jt][q] = as_bf16x8(*(const uint4*)(p.vt + ((int64_t)q * p.r + j) * p.cap + pos + 8 * g));
     }
-    auto mac = [&](int i, bf16x8_t uf, int q) {
+  };
+  auto multiply = [&](const Frags& x) {
 #pragma unroll
-      for (int jt = 0; jt < JT; ++jt)
-        acc[i][jt] = RankMinor ? mfma16x16x32(vf[jt][q], uf, acc[i][jt]) : mfma16x16x32(uf, vf[jt][q], acc[i][jt]);
-    };
-    if constexpr (std::is_same<TU, float>::value) {
-      float f[8][8];
+    for (int i = 0; i < 8; ++i) {
+      auto mac = [&](bf16x8_t uf, int q) {
 #pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        load8<VecU>((const float*)p.u + (int64_t)(rows[t] < p.M ? rows[t] : 0) * p.ldu, w0 + 8 * c, p.W, f[t]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[t][i] = rows[t] < p.M ? f[t][i] : 0.0f;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float col[8] = {f[0][i], f[1][i], f[2][i], f[3][i], f[4][i], f[5][i], f[6][i], f[7][i]};
+        for (int jt = 0; jt < JT; ++jt) acc[i][jt] = mfma16x16x32(x.v[jt][q], uf, acc[i][jt]);
+      };
+      if constexpr (kF32) {
+        const float col[8] = {x.f[0][i], x.f[1][i], x.f[2][i], x.f[3][i], x.f[4][i], x.f[5][i], x.f[6][i], x.f[7][i]};
         bf16x8_t uf[3];
         split_parts<3>(col, uf);
-        mac(i, uf[0], 0);
-        mac(i, uf[0], 1);
-        mac(i, uf[0], 2);
-        mac(i, uf[1], 0);
-        mac(i, uf[1], 1);
-        mac(i, uf[2], 0);
-      }
-    } else {
-      uint32_t d[8][4];
-#pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        uint4 x = __builtin_bit_cast(
-            uint4, load8<VecU>((const uint16_t*)p.u + (int64_t)(rows[t] < p.M ? rows[t] : 0) * p.ldu, w0 + 8 * c, p.W));
-        if (rows[t] >= p.M) x = make_uint4(0, 0, 0, 0);
-        d[t][0] = x.x; d[t][1] = x.y; d[t][2] = x.z; d[t][3] = x.w;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
+        mac(uf[0], 0);
+        mac(uf[0], 1);
+        mac(uf[0], 2);
+        mac(uf[1], 0);
+        mac(uf[1], 1);
+        mac(uf[2], 0);
+      } else {
         // 16-bit element i of rows 2m and 2m + 1
         const uint32_t sel = (i & 1) ? 0x07060302u : 0x05040100u;
-        const bf16x8_t uf = as_bf16x8(make_uint4(__builtin_amdgcn_perm(d[1][i / 2], d[0][i / 2], sel),
-                                                 __builtin_amdgcn_perm(d[3][i / 2], d[2][i / 2], sel),
-                                                 __builtin_amdgcn_perm(d[5][i / 2], d[4][i / 2], sel),
-                                                 __builtin_amdgcn_perm(d[7][i / 2], d[6][i / 2], sel)));
-        mac(i, uf, 0);
-        mac(i, uf, 1);
-        mac(i, uf, 2);
+        const bf16x8_t uf = as_bf16x8(make_uint4(__builtin_amdgcn_perm(x.d[1][i / 2], x.d[0][i / 2], sel),
+                                                 __builtin_amdgcn_perm(x.d[3][i / 2], x.d[2][i / 2], sel),
+                                                 __builtin_amdgcn_perm(x.d[5][i / 2], x.d[4][i / 2], sel),
+                                                 __builtin_amdgcn_perm(x.d[7][i / 2], x.d[6][i / 2], sel)));
+        mac(uf, 0);
+        mac(uf, 1);
+        mac(uf, 2);
       }
     }
+  };
+
+  for (int s0 = p0; s0 < p1;) {
+    const int adapter = p.block_adapter[s0 / kLoraTile];
+    const int o0 = p.offsets[adapter], o1 = p.offsets[adapter + 1];
+    const int s1 = o1 < p1 ? o1 : p1;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int jt = 0; jt < JT; ++jt) acc[i][jt] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int piece = s0; piece < s1; piece += kPiece) {
+      const int end = piece + kPiece < s1 ? piece + kPiece : s1;
+      __syncthreads();
+      for (int i = threadIdx.x * 4; i < end - piece; i += kThreads * 4)
+        *(int4*)(rows_lds + i) = *(const int4*)(p.sorted + piece + i);
+      __syncthreads();
+      int pos = piece + 32 * wave;
+      if (pos < end) {
+        Frags cur;
+        load(pos, piece, cur);
+        for (pos += 32 * kWaves; pos < end; pos += 32 * kWaves) {
+          if constexpr (kAhead) {
+            Frags next;
+            load(pos, piece, next);
+            multiply(cur);
+            cur = next;
+          } else {
+            multiply(cur);
+            load(pos, piece, cur);
+          }
+        }
+        multiply(cur);
+      }
+    }
+    // join: lane (g, c) has columns 8 c + i, ranks 16 jt + 4 g + q. Four
+    // accumulators (half of i, one jt) go to one wave.
+    const int64_t size = (int64_t)p.r * p.W;
+    float* out = (o0 >= p0 && o1 <= p0 + p.chunk) ? p.out + adapter * size
+                                                  : p.slots + (2 * (int64_t)blockIdx.y + (o0 < p0 ? 0 : 1)) * size;
+#pragma unroll
+    for (int r0 = 0; r0 < kVecs; r0 += kRound) {
+#pragma unroll
+      for (int v = 0; v < kRound; ++v) joined[wave][v][lane] = acc[(r0 + v) % 8][(r0 + v) / 8];
+      __syncthreads();
+      for (int v = wave * 4; v < kRound; v += kWaves * 4) {
+        f32x4_t sum[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sum[i] = joined[0][v + i][lane];
+#pragma unroll
+          for (int w = 1; w < kWaves; ++w) sum[i] += joined[w][v + i][lane];
+        }
+        const int w = w0 + 8 * c + v % 8, j = j0 + 16 * ((r0 + v) / 8) + 4 * g;
+        if (j < p.r) {
+          if (p.rank_minor) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (w + i < p.W) *(f32x4_t*)(out + (int64_t)(w + i) * p.r + j) = sum[i];
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              float* at = out + (int64_t)(j + q) * p.W + w;
+              if (w < p.W) *(f32x4_t*)at = f32x4_t{sum[0][q], sum[1][q], sum[2][q], sum[3][q]};
+            }
+          }
+        }
+      }
+      __syncthreads();
+    }
+    s0 = s1;
   }
-  flush(adapter);
 }
 
-// Adapters that cross chunks: their slots, in order; adapters without rows: zeros.
-__global__ __launch_bounds__(kThreads) void lora_reduce_kernel(const int32_t* __restrict__ offsets, int64_t size,
-                                                               int chunk, const float* __restrict__ slots,
-                                                               float* __restrict__ out) {
-  const int a = blockIdx.y;
-  const int o0 = offsets[a], o1 = offsets[a + 1];
+// Adapters that cross chunks: their slots, in order; adapters without rows:
+// zeros. blockIdx.z: dA, dB.
+struct ReduceArgs {
+  const int32_t* offsets;
+  int64_t size[2];
+  int chunk[2];
+  const float* slots[2];
+  float* out[2];
+};
+__global__ __launch_bounds__(kThreads) void lora_reduce_kernel(ReduceArgs p) {
+  const int a = blockIdx.y, z = blockIdx.z;
+  const int o0 = p.offsets[a], o1 = p.offsets[a + 1];
+  const int chunk = p.chunk[z];
   const int c0 = o0 / chunk, c1 = o1 > o0 ? (o1 - 1) / chunk : c0;
   if (o1 > o0 && c0 == c1) return;
+  const int64_t size = p.size[z];
+  const float* slots = p.slots[z];
   for (int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4; i < size;
        i += (int64_t)gridDim.x * kThreads * 4) {
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (o1 > o0) {
       v = *(const float4*)(slots + (2 * (int64_t)c0 + 1) * size + i);
+#pragma unroll 4
       for (int c = c0 + 1; c <= c1; ++c) {
         const float4 x = *(const float4*)(slots + 2 * (int64_t)c * size + i);
         v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
       }
     }
-    *(float4*)(out + a * size + i) = v;
+    *(float4*)(p.out[z] + a * size + i) = v;
   }
 }
 
@@ -654,17 +998,17 @@ bool vec_ok(const void* p, int64_t ld, bool f32) {
   return !p || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % (f32 ? 4 : 8) == 0);
 }
 
-hipError_t launch_down(const DownArgs& p, bool u_f32, int tiles, int splits, hipStream_t stream) {
+hipError_t launch_down(const DownArgs& p, bool u_f32, int tiles, hipStream_t stream) {
   const bool vec = vec_ok(p.u, p.ldu, u_f32) && p.W % (u_f32 ? 4 : 8) == 0;
-  const dim3 grid(tiles, splits);
+  const dim3 grid(tiles, p.splits);
   auto go = [&](auto rt) {
     constexpr int RT = decltype(rt)::value;
     if (u_f32) {
-      if (vec) lora_down_kernel<float, RT, true><<<grid, kThreads, 0, stream>>>(p);
-      else lora_down_kernel<float, RT, false><<<grid, kThreads, 0, stream>>>(p);
+      if (vec) lora_down_kernel<float, RT, true><<<grid, kDownThreads, 0, stream>>>(p);
+      else lora_down_kernel<float, RT, false><<<grid, kDownThreads, 0, stream>>>(p);
     } else {
-      if (vec) lora_down_kernel<uint16_t, RT, true><<<grid, kThreads, 0, stream>>>(p);
-      else lora_down_kernel<uint16_t, RT, false><<<grid, kThreads, 0, stream>>>(p);
+      if (vec) lora_down_kernel<uint16_t, RT, true><<<grid, kDownThreads, 0, stream>>>(p);
+      else lora_down_kernel<uint16_t, RT, false><<<grid, kDownThreads, 0, stream>>>(p);
     }
   };
   if (p.r <= 16) go(std::integral_constant<int, 1>{});
@@ -674,15 +1018,12 @@ hipError_t launch_down(const DownArgs& p, bool u_f32, int tiles, int splits, hip
   return hipGetLastError();
 }
 
-hipError_t launch_up(UpArgs p, bool out_f32, hipStream_t stream) {
+hipError_t launch_up(UpArgs p, bool out_f32, int tiles, hipStream_t stream) {
   const bool vec = vec_ok(p.base, p.ld_base, out_f32) && vec_ok(p.out, p.ld_out, out_f32) &&
                    p.N % (out_f32 ? 4 : 8) == 0;
-  const int64_t rows64 = ceil_div(p.M, kLoraTile);
-  // several column groups a workgroup once the batch fills the chip without
-  int64_t groups = rows64 * ceil_div(p.N, 256) / 1024;
-  groups = groups < 1 ? 1 : (groups > 8 ? 8 : groups);
-  p.n_block = (int)groups * 256;
-  const dim3 grid((unsigned)(p.tiles + rows64), (unsigned)ceil_div(p.N, p.n_block));
+  const int wave_cols = 16 * (out_f32 ? 4 : 8);
+  p.n_block = kWaves * wave_cols;
+  const dim3 grid((unsigned)tiles, (unsigned)ceil_div(p.N, p.n_block));
   auto go = [&](auto rc) {
     constexpr int RC = decltype(rc)::value;
     if (out_f32) {
@@ -701,34 +1042,19 @@ hipError_t launch_up(UpArgs p, bool out_f32, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <bool RankMinor>
-hipError_t launch_outer(const OuterArgs& p, bool u_f32, int L, hipStream_t stream) {
+hipError_t launch_outer(const OuterArgs& p, bool u_f32, hipStream_t stream) {
   const bool vec = vec_ok(p.u, p.ldu, u_f32) && p.W % (u_f32 ? 4 : 8) == 0;
-  if (p.M > 0) {
-    const dim3 grid((unsigned)ceil_div(p.W, 128 * kWaves), (unsigned)ceil_div(p.cap, p.chunk),
-                    (unsigned)ceil_div(p.r, 64));
-    auto go = [&](auto jt) {
-      constexpr int JT = decltype(jt)::value;
-      if constexpr (RankMinor) {  // dB: the output side, either type
-        if (u_f32 && vec) lora_outer_kernel<float, JT, true, true><<<grid, kThreads, 0, stream>>>(p);
-        else if (u_f32) lora_outer_kernel<float, JT, false, true><<<grid, kThreads, 0, stream>>>(p);
-        else if (vec) lora_outer_kernel<uint16_t, JT, true, true><<<grid, kThreads, 0, stream>>>(p);
-        else lora_outer_kernel<uint16_t, JT, false, true><<<grid, kThreads, 0, stream>>>(p);
-      } else {  // dA: x, bf16 with aligned rows
-        lora_outer_kernel<uint16_t, JT, true, false><<<grid, kThreads, 0, stream>>>(p);
-      }
-    };
-    if (p.r <= 16) go(std::integral_constant<int, 1>{});
-    else if (p.r <= 32) go(std::integral_constant<int, 2>{});
-    else go(std::integral_constant<int, 4>{});
-    const hipError_t err = hipGetLastError();
-    if (err != hipSuccess) return err;
-  }
-  const int64_t size = (int64_t)p.r * p.W;
-  int64_t blocks = ceil_div(size, 4 * kThreads);
-  if (blocks > 1024) blocks = 1024;
-  lora_reduce_kernel<<<dim3((unsigned)blocks, (unsigned)L), kThreads, 0, stream>>>(p.offsets, size, p.chunk, p.slots,
-                                                                                   p.out);
+  const dim3 grid((unsigned)ceil_div(p.W, 128), (unsigned)ceil_div(p.cap, p.chunk), (unsigned)ceil_div(p.r, 64));
+  auto go = [&](auto jt) {
+    constexpr int JT = decltype(jt)::value;
+    if (u_f32 && vec) lora_outer_kernel<float, JT, true><<<grid, kThreads, 0, stream>>>(p);
+    else if (u_f32) lora_outer_kernel<float, JT, false><<<grid, kThreads, 0, stream>>>(p);
+    else if (vec) lora_outer_kernel<uint16_t, JT, true><<<grid, kThreads, 0, stream>>>(p);
+    else lora_outer_kernel<uint16_t, JT, false><<<grid, kThreads, 0, stream>>>(p);
+  };
+  if (p.r <= 16) go(std::integral_constant<int, 1>{});
+  else if (p.r <= 32) go(std::integral_constant<int, 2>{});
+  else go(std::integral_constant<int, 4>{});
   return hipGetLastError();
 }
 
@@ -738,28 +1064,31 @@ int64_t align256(int64_t v) { return (v + 255) & ~int64_t(255); }
 
 LoraLayout lora_layout(int64_t M, int64_t L, int64_t K, int64_t N, int64_t r, bool backward) {
   LoraLayout o{};
-  const int64_t touched = M < L ? M : L;
-  o.cap = ceil_div(M + touched * (kLoraTile - 1), kLoraTile) * kLoraTile;
+  o.small = !backward && M <= kLoraSmallRows;
+  const int64_t lists = M < L + 1 ? M : L + 1;  // adapters with rows, and the rows without one
+  o.cap = ceil_div(M + lists * (kLoraTile - 1), kLoraTile) * kLoraTile;
+  // a small batch has no padded lists: at most one tile per list and 64 rows
+  o.tiles = (int)(o.small ? (M < M / kLoraTile + lists ? M : M / kLoraTile + lists) : o.cap / kLoraTile);
   // splits of the contraction: enough workgroups for the chip, each wave at
-  // least one 64-column step, and no more than 16 partial sums to add
+  // least one 64-column step, and no more than 8 partial sums to add
   const int64_t steps = ceil_div(backward ? N : K, 64);
-  const int64_t tiles = ceil_div(M, kLoraTile) + touched / 2;
-  int64_t splits = tiles > 0 ? ceil_div(512, tiles) : 1;
-  if (splits > ceil_div(steps, kWaves)) splits = ceil_div(steps, kWaves);
-  if (splits > 16) splits = 16;
-  const int64_t split_steps = ceil_div(steps, splits);
-  o.splits = (int)ceil_div(steps, split_steps);
+  int64_t splits = M > 0 ? ceil_div(256, ceil_div(M, kLoraTile)) : 1;
+  if (splits > 8) splits = 8;
+  if (splits > ceil_div(steps, kDownWaves)) splits = ceil_div(steps, kDownWaves);
+  o.split_steps = (int)ceil_div(steps, splits);
+  o.splits = (int)ceil_div(steps, o.split_steps);
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t off = at;
     at += align256(bytes);
     return off;
   };
-  o.sorted_off = take(o.cap * 4);
-  o.block_off = take(o.cap / kLoraTile * 4);
-  o.offs_off = take((L + 1) * 4);
-  o.npp_off = take(4);
   o.part_off = take(o.splits * M * r * 4);
+  if (!o.small) {
+    o.sorted_off = take(o.cap * 4);
+    o.block_off = take(o.cap / kLoraTile * 4);
+    o.offs_off = take((L + 2) * 4);
+  }
   if (backward) {
     o.n_pad = ceil_div(N, 8) * 8;
     o.at_off = take(L * K * r * 2);
@@ -767,12 +1096,13 @@ LoraLayout lora_layout(int64_t M, int64_t L, int64_t K, int64_t N, int64_t r, bo
     o.dh_off = take(M * r * 4);
     o.dht_off = take(3 * r * o.cap * 2);
     o.ht_off = take(3 * r * o.cap * 2);
-    // rows per partial gradient: at least 8 r, so that the partial sums are at
-    // most a quarter of the rows' bytes, and at most about 2048 waves
+    // positions per workgroup of the weight gradients: at least 8 r, so that
+    // the partial sums are at most a quarter of the rows' bytes, and enough
+    // workgroups for the chip
     auto chunk = [&](int64_t W) {
-      int64_t c = 8 * r;
-      const int64_t even = M * ceil_div(W, 128) / 2048;
-      c = c > even ? c : even;
+      int64_t c = M * ceil_div(W, 128) * ceil_div(r, 64) / 512;
+      c = c > 8 * r ? c : 8 * r;
+      c = c > 128 ? c : 128;
       return ceil_div(c, kLoraTile) * kLoraTile;
     };
     o.a_chunk = (int)chunk(K);
@@ -784,82 +1114,100 @@ LoraLayout lora_layout(int64_t M, int64_t L, int64_t K, int64_t N, int64_t r, bo
   return o;
 }
 
+namespace {
+
+// The grouping (none for a small batch) and the arguments that name it.
+hipError_t group_rows(const LoraArgs& a, const LoraLayout& o, TileArgs& t, hipStream_t stream) {
+  t = TileArgs{};
+  t.ids = a.ids; t.M = a.M; t.L = a.L;
+  if (o.small) return hipSuccess;
+  GroupArgs g{};
+  g.ids = a.ids; g.M = a.M; g.L = a.L;
+  g.sorted = (int32_t*)(a.ws + o.sorted_off);
+  g.block_adapter = (int32_t*)(a.ws + o.block_off);
+  g.offsets = (int32_t*)(a.ws + o.offs_off);
+  t.sorted = g.sorted; t.block_adapter = g.block_adapter; t.offsets = g.offsets;
+  lora_group_kernel<<<1, kGroupThreads, 0, stream>>>(g);
+  return hipGetLastError();
+}
+
+}  // namespace
+
 hipError_t launch_lora_forward(const LoraArgs& a, hipStream_t stream) {
   const LoraLayout o = lora_layout(a.M, a.L, a.K, a.N, a.r, false);
-  int32_t* sorted = (int32_t*)(a.ws + o.sorted_off);
-  int32_t* block = (int32_t*)(a.ws + o.block_off);
-  int32_t* offsets = (int32_t*)(a.ws + o.offs_off);
-  int32_t* npp = (int32_t*)(a.ws + o.npp_off);
-  float* part = (float*)(a.ws + o.part_off);
-  const int tiles = (int)(o.cap / kLoraTile);
-  hipError_t err = launch_align(a.ids, a.M, a.L, kLoraTile, sorted, block, offsets, npp, stream);
+  TileArgs t;
+  hipError_t err = group_rows(a, o, t, stream);
   if (err != hipSuccess) return err;
   DownArgs d{};
+  d.tile = t;
   d.u = a.x; d.ldu = a.ldx; d.W = a.K;
-  d.v = a.a; d.v_stride = (int64_t)a.r * a.K; d.ldv = a.K;
-  d.r = a.r; d.M = a.M; d.sorted = sorted; d.block_adapter = block; d.npp = npp; d.part = part;
-  d.split_steps = (int)ceil_div(ceil_div(a.K, 64), o.splits);
-  err = launch_down(d, false, tiles, o.splits, stream);
-  if (err != hipSuccess) return err;
+  d.v = a.a; d.v_stride = (int64_t)a.r * a.K; d.ldv = a.K; d.r = a.r;
+  d.splits = o.splits; d.split_steps = o.split_steps;
+  d.part = (float*)(a.ws + o.part_off); d.h = a.h;
   UpArgs u{};
-  u.part = part; u.splits = o.splits; u.M = a.M; u.r = a.r; u.N = a.N; u.L = a.L;
-  u.ids = a.ids; u.sorted = sorted; u.block_adapter = block; u.npp = npp; u.tiles = tiles;
-  u.scales = a.scales; u.b = a.b; u.base = a.base; u.ld_base = a.ld_base; u.out = a.out; u.ld_out = a.ld_out;
-  u.h = a.h;
-  return launch_up(u, a.y_f32, stream);
+  u.tile = t; u.r = a.r; u.N = a.N;
+  u.b = a.b; u.base = a.base; u.ld_base = a.ld_base; u.out = a.out; u.ld_out = a.ld_out;
+  u.part = d.part; u.splits = o.splits; u.scales = a.scales; u.h = a.h;
+  err = launch_down(d, false, o.tiles, stream);
+  if (err != hipSuccess) return err;
+  return launch_up(u, a.y_f32, o.tiles, stream);
 }
 
 hipError_t launch_lora_backward(const LoraArgs& a, hipStream_t stream) {
   const LoraLayout o = lora_layout(a.M, a.L, a.K, a.N, a.r, true);
-  int32_t* sorted = (int32_t*)(a.ws + o.sorted_off);
-  int32_t* block = (int32_t*)(a.ws + o.block_off);
-  int32_t* offsets = (int32_t*)(a.ws + o.offs_off);
-  int32_t* npp = (int32_t*)(a.ws + o.npp_off);
-  float* part = (float*)(a.ws + o.part_off);
-  uint16_t* at = (uint16_t*)(a.ws + o.at_off);
-  uint16_t* bt = (uint16_t*)(a.ws + o.bt_off);
-  float* dh = (float*)(a.ws + o.dh_off);
-  uint16_t* dht = (uint16_t*)(a.ws + o.dht_off);
-  uint16_t* ht = (uint16_t*)(a.ws + o.ht_off);
-  const int tiles = (int)(o.cap / kLoraTile);
-  hipError_t err = launch_align(a.ids, a.M, a.L, kLoraTile, sorted, block, offsets, npp, stream);
+  TileArgs t;
+  hipError_t err = group_rows(a, o, t, stream);
   if (err != hipSuccess) return err;
+  ReduceArgs red{};
+  red.offsets = t.offsets;
+  red.size[0] = (int64_t)a.r * a.K; red.size[1] = (int64_t)a.r * a.N;
+  red.chunk[0] = o.a_chunk; red.chunk[1] = o.b_chunk;
+  red.slots[0] = (float*)(a.ws + o.a_slots_off); red.slots[1] = (float*)(a.ws + o.b_slots_off);
+  red.out[0] = a.da; red.out[1] = a.db;
   if (a.M > 0) {
-    if (a.dx) {
-      lora_transpose_kernel<<<dim3((unsigned)ceil_div(a.K, 64), (unsigned)ceil_div(a.r, 64), a.L), kThreads, 0, stream>>>(
-          a.a, a.r, a.K, a.r, offsets, at);
-      if ((err = hipGetLastError()) != hipSuccess) return err;
-    }
-    lora_transpose_kernel<<<dim3((unsigned)ceil_div(a.r, 64), (unsigned)ceil_div(o.n_pad, 64), a.L), kThreads, 0, stream>>>(
-        a.b, a.N, a.r, o.n_pad, offsets, bt);
+    PrepArgs f{};
+    f.tile = t; f.a = a.a; f.b = a.b; f.K = a.K; f.N = a.N; f.r = a.r; f.n_pad = o.n_pad;
+    f.at = (uint16_t*)(a.ws + o.at_off); f.bt = (uint16_t*)(a.ws + o.bt_off);
+    const int64_t ranks = ceil_div(a.r, 64);
+    f.a_blocks = a.dx ? (int)(ranks * ceil_div(a.K, 64)) : 0;
+    f.b_blocks = (int)(ranks * ceil_div(o.n_pad, 64));
+    f.h = a.h; f.scales = a.scales; f.cap = o.cap; f.ht = (uint16_t*)(a.ws + o.ht_off);
+    const int64_t across = f.a_blocks + f.b_blocks;
+    lora_prep_kernel<<<dim3((unsigned)across, (unsigned)(a.L + ceil_div(o.tiles, across))), kThreads, 0, stream>>>(f);
     if ((err = hipGetLastError()) != hipSuccess) return err;
     DownArgs d{};
+    d.tile = t;
     d.u = a.dout; d.ldu = a.ld_dout; d.W = a.N;
-    d.v = bt; d.v_stride = a.r * o.n_pad; d.ldv = o.n_pad;
-    d.r = a.r; d.M = a.M; d.sorted = sorted; d.block_adapter = block; d.npp = npp; d.part = part;
-    d.split_steps = (int)ceil_div(ceil_div(a.N, 64), o.splits);
-    if ((err = launch_down(d, a.y_f32, tiles, o.splits, stream)) != hipSuccess) return err;
-    FinishArgs f{};
-    f.part = part; f.splits = o.splits; f.M = a.M; f.r = a.r; f.h = a.h; f.scales = a.scales;
-    f.sorted = sorted; f.block_adapter = block; f.npp = npp; f.cap = o.cap; f.dh = dh; f.dht = dht; f.ht = ht;
-    lora_finish_kernel<<<tiles, kThreads, 0, stream>>>(f);
+    d.v = f.bt; d.v_stride = a.r * o.n_pad; d.ldv = o.n_pad; d.r = a.r;
+    d.splits = o.splits; d.split_steps = o.split_steps;
+    d.part = (float*)(a.ws + o.part_off);
+    if ((err = launch_down(d, a.y_f32, o.tiles, stream)) != hipSuccess) return err;
+    JoinArgs j{};
+    j.tile = t; j.r = a.r; j.splits = o.splits; j.part = d.part; j.scales = a.scales;
+    j.dh = (float*)(a.ws + o.dh_off); j.cap = o.cap; j.vt = (uint16_t*)(a.ws + o.dht_off);
+    lora_join_kernel<<<o.tiles, kThreads, 0, stream>>>(j);
     if ((err = hipGetLastError()) != hipSuccess) return err;
     if (a.dx) {
       UpArgs u{};
-      u.part = dh; u.splits = 1; u.M = a.M; u.r = a.r; u.N = a.K; u.L = a.L;
-      u.ids = a.ids; u.sorted = sorted; u.block_adapter = block; u.npp = npp; u.tiles = tiles;
-      u.b = at; u.base = a.dx_base; u.ld_base = a.ld_dx_base; u.out = a.dx; u.ld_out = a.ld_dx;
-      if ((err = launch_up(u, false, stream)) != hipSuccess) return err;
+      u.tile = t; u.r = a.r; u.N = a.K; u.part = j.dh; u.splits = 1;
+      u.b = f.at; u.base = a.dx_base; u.ld_base = a.ld_dx_base; u.out = a.dx; u.ld_out = a.ld_dx;
+      if ((err = launch_up(u, false, o.tiles, stream)) != hipSuccess) return err;
     }
+    OuterArgs w{};
+    w.r = a.r; w.M = a.M; w.L = a.L; w.cap = o.cap;
+    w.sorted = t.sorted; w.block_adapter = t.block_adapter; w.offsets = t.offsets;
+    w.u = a.x; w.ldu = a.ldx; w.W = a.K; w.vt = j.vt; w.out = a.da;
+    w.slots = (float*)(a.ws + o.a_slots_off); w.chunk = o.a_chunk;
+    if ((err = launch_outer(w, false, stream)) != hipSuccess) return err;
+    w.u = a.dout; w.ldu = a.ld_dout; w.W = a.N; w.vt = f.ht; w.out = a.db; w.rank_minor = true;
+    w.slots = (float*)(a.ws + o.b_slots_off); w.chunk = o.b_chunk;
+    if ((err = launch_outer(w, a.y_f32, stream)) != hipSuccess) return err;
   }
-  OuterArgs w{};
-  w.r = a.r; w.M = a.M; w.cap = o.cap; w.sorted = sorted; w.block_adapter = block; w.offsets = offsets; w.npp = npp;
-  w.u = a.x; w.ldu = a.ldx; w.W = a.K; w.vt = dht; w.out = a.da;
-  w.slots = (float*)(a.ws + o.a_slots_off); w.chunk = o.a_chunk;
-  if ((err = launch_outer<false>(w, false, a.L, stream)) != hipSuccess) return err;
-  w.u = a.dout; w.ldu = a.ld_dout; w.W = a.N; w.vt = ht; w.out = a.db;
-  w.slots = (float*)(a.ws + o.b_slots_off); w.chunk = o.b_chunk;
-  return launch_outer<true>(w, a.y_f32, a.L, stream);
+  const int64_t widest = red.size[0] > red.size[1] ? red.size[0] : red.size[1];
+  int64_t blocks = ceil_div(widest, 4 * kThreads);
+  if (blocks > 1024) blocks = 1024;
+  lora_reduce_kernel<<<dim3((unsigned)blocks, (unsigned)a.L, 2), kThreads, 0, stream>>>(red);
+  return hipGetLastError();
 }
 
 }  // namespace moe

@@ -71,27 +71,26 @@ struct LoraArgs {
   uint8_t* ws;
 };
 
-// Workspace of one call. Forward: the grouping, and the partial products of
-// x A^T of each split of K. Backward adds the transposed weights, dh, the
-// transposed factors of the weight gradients and their partial sums.
+// Workspace of one call. Forward: the grouping (not for a small batch, which
+// its kernels group themselves) and the partial products of each split of K.
+// Backward adds the transposed weights, dh, the rank-major factors of the
+// weight gradients and their partial sums.
+constexpr int kLoraSmallRows = 256;  // rows up to which a forward needs no grouping launch
 struct LoraLayout {
-  int64_t cap;                              // padded rows the grouping may reach
-  int splits;                               // forward: of K; backward: of N
-  int64_t sorted_off, block_off, offs_off, npp_off, part_off;
-  int64_t at_off, bt_off, n_pad;            // backward: A^T [L, K, r], B^T [L, r, n_pad]
-  int64_t dh_off, dht_off, ht_off;          // backward: dh [M, r]; [3][r][cap] bf16 parts of dh and s*h
-  int64_t a_slots_off, b_slots_off;         // backward: partial gradients [slots][r * K], [slots][N * r]
-  int a_chunk, b_chunk;                     // rows per partial of dA and dB
+  int64_t cap;                                  // padded rows the grouping may reach
+  int tiles;                                    // workgroups' tiles: cap / 64, or a small batch's bound
+  int splits, split_steps;                      // of the contraction (forward K, backward N), in 64-column steps
+  bool small;
+  int64_t sorted_off, block_off, offs_off, part_off;
+  int64_t at_off, bt_off, n_pad;                // backward: A^T [L, K, r], B^T [L, r, n_pad]
+  int64_t dh_off, dht_off, ht_off;              // backward: dh [M, r]; [3][r][cap] bf16 parts of dh and s*h
+  int64_t a_slots_off, b_slots_off;             // backward: partial gradients [slots][r * K], [slots][N * r]
+  int a_chunk, b_chunk;                         // positions per partial of dA and dB
   int64_t total;
 };
 LoraLayout lora_layout(int64_t M, int64_t L, int64_t K, int64_t N, int64_t r, bool backward);
 
 hipError_t launch_lora_forward(const LoraArgs& a, hipStream_t stream);
 hipError_t launch_lora_backward(const LoraArgs& a, hipStream_t stream);
-
-// The grouping of moe_route_align from given ids (route_align.hip): ids [n]
-// in [0, E), any other value is in no group.
-hipError_t launch_align(const int32_t* ids, int n, int E, int block_m, int32_t* sorted_ids, int32_t* block_expert,
-                        int32_t* offsets, int32_t* npp, hipStream_t stream);
 
 }  // namespace moe

@@ -16,7 +16,6 @@
 //               4096 assignments on a grid of workgroups, one per segment of
 //               the assignments.
 #include "internal.h"
-#include "operators.h"
 #include "device_common.h"
 #include "route_common.h"
 
@@ -371,26 +370,6 @@ __global__ __launch_bounds__(kAlignThreads) void route_align_small_kernel(
                                    npp);
 }
 
-}  // namespace
-
-hipError_t launch_align(const int32_t* ids, int n, int E, int block_m, int32_t* sorted_ids, int32_t* block_expert,
-                        int32_t* offsets, int32_t* npp, hipStream_t stream) {
-  if (n >= kAlignGridMinIds) {
-    // segments of at least kAlignGridSegIds assignments, at most
-    // kAlignGridMaxBlocks workgroups (each histograms all n ids)
-    const int64_t per = ((int64_t)n + kAlignGridMaxBlocks - 1) / kAlignGridMaxBlocks;
-    const int seg = (int)(per > kAlignGridSegIds ? (per + 1023) / 1024 * 1024 : kAlignGridSegIds);
-    const int grid = (n + seg - 1) / seg;
-    align_grid_kernel<<<grid, kAlignThreads, 0, stream>>>(ids, n, E, block_m, seg, sorted_ids, block_expert, offsets,
-                                                          npp);
-  } else {
-    align_kernel<<<1, kAlignThreads, 0, stream>>>(ids, n, E, block_m, sorted_ids, block_expert, offsets, npp);
-  }
-  return hipGetLastError();
-}
-
-namespace {
-
 template <int VPL>
 hipError_t launch_vpl(const float* logits, int M, int E, int k, int block_m, int32_t* topk_ids,
                       float* topk_w, int32_t* sorted_ids, int32_t* block_expert, int32_t* offsets,
@@ -404,7 +383,20 @@ hipError_t launch_vpl(const float* logits, int M, int E, int k, int block_m, int
   topk_kernel<VPL><<<blocks, 64 * kTopkWavesPerBlock, 0, stream>>>(logits, M, E, k, topk_ids, topk_w);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  return launch_align(topk_ids, M * k, E, block_m, sorted_ids, block_expert, offsets, npp, stream);
+  const int MK = M * k;
+  if (MK >= kAlignGridMinIds) {
+    // segments of at least kAlignGridSegIds assignments, at most
+    // kAlignGridMaxBlocks workgroups (each histograms all M*k ids)
+    const int64_t per = ((int64_t)MK + kAlignGridMaxBlocks - 1) / kAlignGridMaxBlocks;
+    const int seg = (int)(per > kAlignGridSegIds ? (per + 1023) / 1024 * 1024 : kAlignGridSegIds);
+    const int grid = (MK + seg - 1) / seg;
+    align_grid_kernel<<<grid, kAlignThreads, 0, stream>>>(topk_ids, MK, E, block_m, seg, sorted_ids, block_expert,
+                                                          offsets, npp);
+  } else {
+    align_kernel<<<1, kAlignThreads, 0, stream>>>(topk_ids, MK, E, block_m, sorted_ids, block_expert, offsets,
+                                                  npp);
+  }
+  return hipGetLastError();
 }
 
 }  // namespace
