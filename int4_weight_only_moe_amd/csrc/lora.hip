@@ -255,15 +255,17 @@ struct Tile {
 __device__ __forceinline__ int find_tile(const TileArgs& p, Tile& sh, int tile) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   if (p.sorted) {
+    // all loads at once: the lists' buffers have room for every tile of the grid
+    const int first = p.sorted[tile * kLoraTile];
+    const int row = p.sorted[tile * kLoraTile + lane];
+    const int adapter = p.block_adapter[tile];
     if (tile * kLoraTile >= p.offsets[p.L + 1]) return 0;
     if (tid < kLoraTile) {
-      const int first = p.sorted[tile * kLoraTile];
-      const int row = p.sorted[tile * kLoraTile + tid];
       sh.rows[tid] = row < p.M ? row : first;
       const uint64_t live = __ballot(row < p.M);
       if (tid == 0) {
         sh.count = __builtin_popcountll(live);
-        sh.adapter = p.block_adapter[tile];
+        sh.adapter = adapter;
       }
     }
     __syncthreads();
@@ -311,10 +313,34 @@ __device__ __forceinline__ int find_tile(const TileArgs& p, Tile& sh, int tile) 
   return n;
 }
 
-// ------------------------------------------------------------------ down
-constexpr int kDownThreads = 512;
-constexpr int kDownWaves = kDownThreads / 64;
+// 16 bytes of a row of W elements from element w, zeros past its end. Vec: the
+// row is 16-byte aligned and W a multiple of 16 bytes' elements.
+template <typename T, bool Vec>
+__device__ __forceinline__ uint4 load16(const T* __restrict__ row, int w, int W) {
+  constexpr int kN = 16 / sizeof(T);
+  if constexpr (Vec) {
+    const uint4 v = *(const uint4*)(row + (w < W ? w : 0));
+    return w < W ? v : make_uint4(0, 0, 0, 0);
+  } else {
+    uint32_t d[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const T x = row[w + i < W ? w + i : 0];
+      if constexpr (sizeof(T) == 4) d[i] = w + i < W ? __float_as_uint(x) : 0u;
+      else d[i / 2] |= (w + i < W ? (uint32_t)x : 0u) << (16 * (i & 1));
+    }
+    return make_uint4(d[0], d[1], d[2], d[3]);
+  }
+}
 
+// Orders a wave's own LDS writes before its later reads (the hardware runs one
+// wave's LDS operations in order; this keeps the compiler from moving them).
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// ------------------------------------------------------------------ down
 struct DownArgs {
   TileArgs tile;
   const void* u;              // [M, W]
@@ -323,136 +349,144 @@ struct DownArgs {
   const uint16_t* v;          // [L][r][ldv], zeros from W to ldv
   int64_t v_stride, ldv;
   int r;
-  int splits, split_steps;    // 64-column steps per split
+  int splits, split_steps;    // 128-byte steps per split
   float* part;                // [splits][M][r]
   float* h;                   // [M][r] or null: receives zeros for rows without an adapter
 };
 
-// The sum over the split's columns of v[j][w] * u[row][w], as four sums (of
-// waves i and i + 4 each) that the caller adds: red[i][row][j].
-// A step is 64 columns: lane (g, c) takes the 16 columns from 16 g of row c of
-// either operand, as two 8-column fragments, so four lanes read 128
-// consecutive bytes of a bf16 row. The waves take the split's steps in turn,
-// with the next step's loads issued before the current one's products.
+// A step is 128 bytes of the rows of u: 64 bf16 or 32 fp32 columns.
+template <typename TU, int RT>
+struct DownShape {
+  static constexpr int kCols = 128 / sizeof(TU);
+  static constexpr int kVChunks = kCols / 8;  // 16-byte chunks of a row of v
+  static constexpr int kStage = kLoraTile * 128 + RT * 16 * kVChunks * 16;
+  static constexpr int kSums = kLoraTile * RT * 16 * 4;
+  static constexpr int kWaveBytes = kStage > kSums ? kStage : kSums;  // a wave's LDS
+};
+
+// A wave's sums over its steps of v[j][w] * u[row][w], left in its LDS as
+// [row][rank] with the 16-byte chunks of a row exchanged by row.
+// The matrix core wants lane (g, c) to hold 8 columns of row c, but a load
+// instruction runs at full rate only where neighbouring lanes read
+// neighbouring bytes (16 bytes a row and lane ran at a quarter of it: 40 us
+// against 27 for x [8192, 7168] alone, ranks 64). So eight lanes read a row's
+// 128 bytes, and the step goes through the wave's own part of LDS (no other
+// wave takes part, so no barrier), chunks exchanged by row so that the 16 rows
+// of a fragment lie in different banks. The next step's loads are in flight
+// while this one is multiplied.
 template <typename TU, int RT, bool VecU, int NSUB>
-__device__ __forceinline__ void down_tile(const DownArgs& p, const Tile& sh, float* red) {
-  constexpr int kRed = RT * 16 + 4;
+__device__ __forceinline__ void down_tile(const DownArgs& p, const Tile& sh, uint4* lds) {
   constexpr bool kF32 = std::is_same<TU, float>::value;
+  using Shape = DownShape<TU, RT>;
+  constexpr int kVC = Shape::kVChunks;
+  constexpr int kLoadsU = NSUB * 2, kLoadsV = RT * kVC / 4;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
-  const TU* urow[NSUB];
+  const TU* urow[kLoadsU];
 #pragma unroll
-  for (int ts = 0; ts < NSUB; ++ts) urow[ts] = (const TU*)p.u + (int64_t)sh.rows[ts * kSub + c] * p.ldu;
-  const uint16_t* vrow[RT];
+  for (int i = 0; i < kLoadsU; ++i) urow[i] = (const TU*)p.u + (int64_t)sh.rows[i * 8 + (lane >> 3)] * p.ldu;
+  const uint16_t* vrow[kLoadsV];
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    const int j = rt * 16 + c < p.r ? rt * 16 + c : p.r - 1;
-    vrow[rt] = p.v + sh.adapter * p.v_stride + j * p.ldv;
+  for (int i = 0; i < kLoadsV; ++i) {
+    const int j = (i * 64 + lane) / kVC;
+    vrow[i] = p.v + sh.adapter * p.v_stride + (j < p.r ? j : p.r - 1) * p.ldv;
   }
+  uint4* vlds = lds + kLoraTile * 8;
   f32x4_t acc[RT][NSUB];
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
     for (int ts = 0; ts < NSUB; ++ts) acc[rt][ts] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  const int steps = (p.W + 63) / 64;
+  const int steps = (p.W + Shape::kCols - 1) / Shape::kCols;
   const int s0 = blockIdx.y * p.split_steps;
   const int s1 = s0 + p.split_steps < steps ? s0 + p.split_steps : steps;
-  constexpr bool kAhead = RT <= (kF32 ? 2 : 4);  // two steps' loads fit in the registers
-  struct Frags {
-    bf16x8_t v[RT][2];
-    bf16x8_t u[kF32 ? 1 : NSUB][2];
-    float f[kF32 ? NSUB : 1][2][8];
+  uint4 u[kLoadsU], v[kLoadsV];
+  auto load = [&](int s) {
+#pragma unroll
+    for (int i = 0; i < kLoadsU; ++i)
+      u[i] = load16<TU, VecU>(urow[i], s * Shape::kCols + (lane & 7) * (16 / (int)sizeof(TU)), p.W);
+#pragma unroll
+    for (int i = 0; i < kLoadsV; ++i)
+      v[i] = load16<uint16_t, true>(vrow[i], s * Shape::kCols + (lane % kVC) * 8, (int)p.ldv);
   };
-  auto load = [&](int s, Frags& x) {
-    const int w = s * 64 + g * 16;
+  int s = s0 + wave;
+  if (s < s1) load(s);
+  for (; s < s1; s += kWaves) {
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      if constexpr (kF32) {
-#pragma unroll
-        for (int ts = 0; ts < NSUB; ++ts) load8<VecU>((const float*)urow[ts], w + 8 * hh, p.W, x.f[ts][hh]);
-      } else {
-#pragma unroll
-        for (int ts = 0; ts < NSUB; ++ts) x.u[ts][hh] = load8<VecU>((const uint16_t*)urow[ts], w + 8 * hh, p.W);
-      }
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) x.v[rt][hh] = load8<true>(vrow[rt], w + 8 * hh, (int)p.ldv);
+    for (int i = 0; i < kLoadsU; ++i) {
+      const int row = i * 8 + (lane >> 3);
+      lds[row * 8 + ((lane & 7) ^ (row & 7))] = u[i];
     }
-  };
-  auto multiply = [&](const Frags& x) {
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh)
+    for (int i = 0; i < kLoadsV; ++i) {
+      const int j = (i * 64 + lane) / kVC;
+      vlds[j * kVC + ((lane % kVC) ^ (j & (kVC - 1)))] = v[i];
+    }
+    wave_lds_fence();
+    if (s + kWaves < s1) load(s + kWaves);
+#pragma unroll
+    for (int ks = 0; ks < kVC / 4; ++ks) {
+      bf16x8_t vf[RT];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+        vf[rt] = as_bf16x8(vlds[(rt * 16 + c) * kVC + ((ks * 4 + g) ^ (c & (kVC - 1)))]);
 #pragma unroll
       for (int ts = 0; ts < NSUB; ++ts) {
+        const uint4* row = lds + (ts * kSub + c) * 8;
         if constexpr (kF32) {
+          const uint4 lo = row[(2 * g) ^ (c & 7)], hi = row[(2 * g + 1) ^ (c & 7)];
+          const float f[8] = {__uint_as_float(lo.x), __uint_as_float(lo.y), __uint_as_float(lo.z), __uint_as_float(lo.w),
+                              __uint_as_float(hi.x), __uint_as_float(hi.y), __uint_as_float(hi.z), __uint_as_float(hi.w)};
           bf16x8_t q[3];
-          split_parts<3>(x.f[ts][hh], q);
+          split_parts<3>(f, q);
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-            for (int i = 0; i < 3; ++i) acc[rt][ts] = mfma16x16x32(x.v[rt][hh], q[i], acc[rt][ts]);
+            for (int i = 0; i < 3; ++i) acc[rt][ts] = mfma16x16x32(vf[rt], q[i], acc[rt][ts]);
         } else {
+          const bf16x8_t uf = as_bf16x8(row[(ks * 4 + g) ^ (c & 7)]);
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt) acc[rt][ts] = mfma16x16x32(x.v[rt][hh], x.u[ts][hh], acc[rt][ts]);
+          for (int rt = 0; rt < RT; ++rt) acc[rt][ts] = mfma16x16x32(vf[rt], uf, acc[rt][ts]);
         }
       }
-  };
-  int s = s0 + wave;
-  if (s < s1) {
-    Frags cur;
-    load(s, cur);
-    for (s += kDownWaves; s < s1; s += kDownWaves) {
-      if constexpr (kAhead) {
-        Frags next;
-        load(s, next);
-        multiply(cur);
-        cur = next;
-      } else {
-        multiply(cur);
-        load(s, cur);
-      }
     }
-    multiply(cur);
+    wave_lds_fence();
   }
   // lane (g, c) holds ranks 16 rt + 4 g .. + 3 of row 16 ts + c
-  float* mine = red + (wave & 3) * kLoraTile * kRed;
 #pragma unroll
-  for (int half = 1; half >= 0; --half) {
-    if (wave >> 2 == half) {
+  for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int ts = 0; ts < NSUB; ++ts) {
-          f32x4_t* at = (f32x4_t*)(mine + (ts * kSub + c) * kRed + rt * 16 + 4 * g);
-          *at = half ? acc[rt][ts] : *at + acc[rt][ts];
-        }
+    for (int ts = 0; ts < NSUB; ++ts) {
+      const int row = ts * kSub + c;
+      *(f32x4_t*)(lds + row * RT * 4 + ((rt * 4 + g) ^ (row & (RT * 4 - 1)))) = acc[rt][ts];
     }
-    __syncthreads();
-  }
 }
 
 template <typename TU, int RT, bool VecU>
-__global__ __launch_bounds__(kDownThreads) void lora_down_kernel(DownArgs p) {
-  constexpr int kRed = RT * 16 + 4;
+__global__ __launch_bounds__(kThreads) void lora_down_kernel(DownArgs p) {
+  constexpr int kWaveChunks = DownShape<TU, RT>::kWaveBytes / 16;
   constexpr int kQuads = RT * 4;
   __shared__ __align__(16) Tile sh;
-  __shared__ __align__(16) float red[4 * kLoraTile * kRed];
+  __shared__ uint4 lds[kWaves * kWaveChunks];
   const int tid = threadIdx.x;
   const int n = find_tile(p.tile, sh, blockIdx.x);
   if (n == 0) return;
   if (sh.adapter == p.tile.L) {  // rows without an adapter
     if (p.h && blockIdx.y == 0)
-      for (int i = tid; i < n * p.r; i += kDownThreads) p.h[(int64_t)sh.rows[i / p.r] * p.r + i % p.r] = 0.0f;
+      for (int i = tid; i < n * p.r; i += kThreads) p.h[(int64_t)sh.rows[i / p.r] * p.r + i % p.r] = 0.0f;
     return;
   }
-  if (n <= 16) down_tile<TU, RT, VecU, 1>(p, sh, red);
-  else if (n <= 32) down_tile<TU, RT, VecU, 2>(p, sh, red);
-  else down_tile<TU, RT, VecU, 4>(p, sh, red);
+  uint4* mine = lds + (tid >> 6) * kWaveChunks;
+  if (n <= 16) down_tile<TU, RT, VecU, 1>(p, sh, mine);
+  else if (n <= 32) down_tile<TU, RT, VecU, 2>(p, sh, mine);
+  else down_tile<TU, RT, VecU, 4>(p, sh, mine);
+  __syncthreads();
   float* part = p.part + (int64_t)blockIdx.y * p.tile.M * p.r;
-  for (int i = tid; i < n * kQuads; i += kDownThreads) {
-    const int t = i / kQuads, j = i % kQuads * 4;
-    if (j >= p.r) continue;
-    const f32x4_t* at = (const f32x4_t*)(red + t * kRed + j);
-    constexpr int kNext = kLoraTile * kRed / 4;
-    *(f32x4_t*)(part + (int64_t)sh.rows[t] * p.r + j) = (at[0] + at[kNext]) + (at[2 * kNext] + at[3 * kNext]);
+  for (int i = tid; i < n * kQuads; i += kThreads) {
+    const int t = i / kQuads, quad = i % kQuads;
+    if (quad * 4 >= p.r) continue;
+    const f32x4_t* at = (const f32x4_t*)(lds + t * kQuads + (quad ^ (t & (kQuads - 1))));
+    *(f32x4_t*)(part + (int64_t)sh.rows[t] * p.r + quad * 4) =
+        (at[0] + at[kWaveChunks]) + (at[2 * kWaveChunks] + at[3 * kWaveChunks]);
   }
 }
 
@@ -472,33 +506,37 @@ struct UpArgs {
   int n_block;                // columns per workgroup
 };
 
-// NT consecutive columns from n of a row (fp32: 4, bf16: 8: 16 bytes).
+// Four consecutive columns from n of a row, as raw bits (fp32: one word each,
+// bf16: two words in all). Vec: the row is 16-byte aligned and N % 4 == 0.
 template <typename TO, bool Vec>
-__device__ __forceinline__ uint4 load_cols(const TO* row, int n, int N) {
-  constexpr int NT = 16 / sizeof(TO);
+__device__ __forceinline__ uint4 load4(const TO* row, int n, int N) {
   uint32_t d[4] = {0, 0, 0, 0};
   if constexpr (Vec) {
-    if (n < N) return *(const uint4*)(row + n);
+    if (n >= N) return make_uint4(0, 0, 0, 0);
+    if constexpr (sizeof(TO) == 4) return *(const uint4*)(row + n);
+    const uint2 v = *(const uint2*)(row + n);
+    return make_uint4(v.x, v.y, 0, 0);
   } else {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
+    for (int i = 0; i < 4; ++i) {
       if (n + i < N) {
         if constexpr (sizeof(TO) == 4) d[i] = __float_as_uint(row[n + i]);
         else d[i / 2] |= (uint32_t)row[n + i] << (16 * (i & 1));
       }
     }
+    return make_uint4(d[0], d[1], d[2], d[3]);
   }
-  return make_uint4(d[0], d[1], d[2], d[3]);
 }
 template <typename TO, bool Vec>
-__device__ __forceinline__ void store_cols(TO* row, int n, int N, uint4 v) {
-  constexpr int NT = 16 / sizeof(TO);
+__device__ __forceinline__ void store4(TO* row, int n, int N, uint4 v) {
   if constexpr (Vec) {
-    if (n < N) *(uint4*)(row + n) = v;
+    if (n >= N) return;
+    if constexpr (sizeof(TO) == 4) *(uint4*)(row + n) = v;
+    else *(uint2*)(row + n) = make_uint2(v.x, v.y);
   } else {
     const uint32_t d[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
+    for (int i = 0; i < 4; ++i) {
       if (n + i < N) {
         if constexpr (sizeof(TO) == 4) row[n + i] = __uint_as_float(d[i]);
         else row[n + i] = (uint16_t)(d[i / 2] >> (16 * (i & 1)));
@@ -510,15 +548,14 @@ __device__ __forceinline__ void store_cols(TO* row, int n, int N, uint4 v) {
 // Rows without an adapter: out = base (nothing to do in place), or zeros.
 template <typename TO, bool Vec>
 __device__ __forceinline__ void copy_rows(const UpArgs& p, const Tile& sh, int n) {
-  constexpr int NT = 16 / sizeof(TO);
   if (p.base == p.out) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int n0 = blockIdx.y * p.n_block, n1 = n0 + p.n_block < p.N ? n0 + p.n_block : p.N;
   for (int t = wave; t < n; t += kWaves) {
     TO* out = (TO*)p.out + (int64_t)sh.rows[t] * p.ld_out;
     const TO* base = (const TO*)p.base + (int64_t)sh.rows[t] * p.ld_base;
-    for (int col = n0 + lane * NT; col < n1; col += 64 * NT)
-      store_cols<TO, Vec>(out, col, p.N, p.base ? load_cols<TO, Vec>(base, col, p.N) : make_uint4(0, 0, 0, 0));
+    for (int col = n0 + lane * 4; col < n1; col += 64 * 4)
+      store4<TO, Vec>(out, col, p.N, p.base ? load4<TO, Vec>(base, col, p.N) : make_uint4(0, 0, 0, 0));
   }
 }
 
@@ -558,17 +595,19 @@ __device__ __forceinline__ void up_factor(const UpArgs& p, const Tile& sh, int n
   }
 }
 
+constexpr int kUpCols = 64;  // columns of a wave
+
 // out[row][n] = base[row][n] + sum_j b[n][j] * factor[row][j].
 // The factor's bf16 parts are laid one after another along the contraction:
 // 8-wide chunk number q of a lane's fragments is chunk q % (r / 8) of part
 // q / (r / 8), so ranks 8 and 16 fill one 32-wide matrix-core step with their
-// parts. A wave takes 16 * NT columns: matrix-core tile i has the columns
-// c * NT + i (c its column), so a lane ends with NT consecutive columns, 16
-// bytes, of four rows, and 16 lanes read and write 256 consecutive bytes.
-// What does not depend on the factor is loaded before it is made.
+// parts. A wave takes 64 columns: matrix-core tile i has the columns 4 c + i
+// (c its column), so a lane ends with four consecutive columns of four rows, and
+// 16 lanes read and write 128 (fp32: 256) consecutive bytes of a row. b's 64
+// rows are consecutive in memory and go through the wave's own part of LDS, as
+// in down. What does not depend on the factor is loaded before it is made.
 template <typename TO, int RC, bool Vec, int NSUB>
-__device__ __forceinline__ void up_tile(const UpArgs& p, const Tile& sh, int n, uint16_t* lds) {
-  constexpr int NT = 16 / sizeof(TO);
+__device__ __forceinline__ void up_tile(const UpArgs& p, const Tile& sh, int n, uint16_t* lds, uint4* blds) {
   constexpr int NP = sizeof(TO) == 4 ? 3 : 2;
   constexpr int kChunks = RC / 8;                         // 8-wide chunks of a part
   constexpr int kSteps = (NP * kChunks + 3) / 4;          // 32-wide steps
@@ -577,39 +616,53 @@ __device__ __forceinline__ void up_tile(const UpArgs& p, const Tile& sh, int n, 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
   const uint16_t* b = p.b + (int64_t)sh.adapter * p.N * p.r;
   const int n_end = (int)(blockIdx.y + 1) * p.n_block < p.N ? (int)(blockIdx.y + 1) * p.n_block : p.N;
-  int n0 = blockIdx.y * p.n_block + wave * 16 * NT;
-  bf16x8_t bf[NT][kFrags];
-  uint4 base[4];
-  auto load_b = [&](int col) {
+  int n0 = blockIdx.y * p.n_block + wave * kUpCols;
+  uint4 braw[kChunks], base[4];
+  auto load_b = [&](int first) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const uint16_t* row = b + (int64_t)(col + i < p.N ? col + i : p.N - 1) * p.r;
-#pragma unroll
-      for (int k = 0; k < kFrags; ++k) bf[i][k] = load8<true>(row, ((k * 4 + g) % kChunks) * 8, p.r);
+    for (int i = 0; i < kChunks; ++i) {
+      const int col = first + (i * 64 + lane) / kChunks;
+      braw[i] = load16<uint16_t, true>(b + (int64_t)(col < p.N ? col : p.N - 1) * p.r, (lane % kChunks) * 8, p.r);
     }
   };
   auto load_base = [&](int ts, int col) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      base[q] = p.base ? load_cols<TO, Vec>((const TO*)p.base + (int64_t)sh.rows[ts * kSub + 4 * g + q] * p.ld_base, col,
-                                            p.N)
+      base[q] = p.base ? load4<TO, Vec>((const TO*)p.base + (int64_t)sh.rows[ts * kSub + 4 * g + q] * p.ld_base, col, p.N)
                        : make_uint4(0, 0, 0, 0);
   };
   if (n0 < n_end) {
-    load_b(n0 + c * NT);
-    load_base(0, n0 + c * NT);
+    load_b(n0);
+    load_base(0, n0 + 4 * c);
   }
   up_factor<RC, NP>(p, sh, n, lds);
   __syncthreads();
   while (n0 < n_end) {
-    const int col = n0 + c * NT;
+    const int col = n0 + 4 * c;
+    // row m of b, chunk k at slot k ^ (m / 4): the 16 rows 4 c + i of a fragment in different banks
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      const int m = (i * 64 + lane) / kChunks;
+      blds[m * kChunks + ((lane % kChunks) ^ ((m >> 2) & (kChunks - 1)))] = braw[i];
+    }
+    wave_lds_fence();
+    bf16x8_t bf[4][kFrags];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < kFrags; ++k)
+        bf[i][k] = as_bf16x8(blds[(4 * c + i) * kChunks + (((k * 4 + g) % kChunks) ^ (c & (kChunks - 1)))]);
+    wave_lds_fence();
+    const int next = n0 + kWaves * kUpCols;
+    if (next < n_end) load_b(next);
 #pragma unroll
     for (int ts = 0; ts < NSUB; ++ts) {
-      f32x4_t acc[NT];
-      uint4 in[4] = {base[0], base[1], base[2], base[3]};
+      f32x4_t acc[4];
+      const uint4 in[4] = {base[0], base[1], base[2], base[3]};
       if (ts + 1 < NSUB) load_base(ts + 1, col);
+      else if (next < n_end) load_base(0, next + 4 * c);
 #pragma unroll
-      for (int i = 0; i < NT; ++i) acc[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int i = 0; i < 4; ++i) acc[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int k = 0; k < kSteps; ++k) {
         const int chunk = k * 4 + g;
@@ -618,31 +671,27 @@ __device__ __forceinline__ void up_tile(const UpArgs& p, const Tile& sh, int n, 
             *(const uint4*)(lds + ((q < NP ? q : 0) * kLoraTile + ts * kSub + c) * kPitch + (chunk % kChunks) * 8));
         if (kSteps * 4 > NP * kChunks && q >= NP) hf = as_bf16x8(make_uint4(0, 0, 0, 0));
 #pragma unroll
-        for (int i = 0; i < NT; ++i) acc[i] = mfma16x16x32(hf, bf[i][k % kFrags], acc[i]);
+        for (int i = 0; i < 4; ++i) acc[i] = mfma16x16x32(hf, bf[i][k % kFrags], acc[i]);
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int t = ts * kSub + 4 * g + q;
-        const uint32_t x[4] = {in[q].x, in[q].y, in[q].z, in[q].w};
-        uint32_t d[4];
+        uint4 d = make_uint4(0, 0, 0, 0);
         if constexpr (sizeof(TO) == 4) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) d[i] = __float_as_uint(__uint_as_float(x[i]) + acc[i][q]);
+          d = make_uint4(__float_as_uint(__uint_as_float(in[q].x) + acc[0][q]),
+                         __float_as_uint(__uint_as_float(in[q].y) + acc[1][q]),
+                         __float_as_uint(__uint_as_float(in[q].z) + acc[2][q]),
+                         __float_as_uint(__uint_as_float(in[q].w) + acc[3][q]));
         } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            d[i] = bf16_bits(__uint_as_float(x[i] << 16) + acc[2 * i][q]) |
-                   bf16_bits(__uint_as_float(x[i] & 0xffff0000u) + acc[2 * i + 1][q]) << 16;
+          d.x = bf16_bits(__uint_as_float(in[q].x << 16) + acc[0][q]) |
+                bf16_bits(__uint_as_float(in[q].x & 0xffff0000u) + acc[1][q]) << 16;
+          d.y = bf16_bits(__uint_as_float(in[q].y << 16) + acc[2][q]) |
+                bf16_bits(__uint_as_float(in[q].y & 0xffff0000u) + acc[3][q]) << 16;
         }
-        if (t < n)
-          store_cols<TO, Vec>((TO*)p.out + (int64_t)sh.rows[t] * p.ld_out, col, p.N, make_uint4(d[0], d[1], d[2], d[3]));
+        if (t < n) store4<TO, Vec>((TO*)p.out + (int64_t)sh.rows[t] * p.ld_out, col, p.N, d);
       }
     }
-    n0 += kWaves * 16 * NT;
-    if (n0 < n_end) {
-      load_b(n0 + c * NT);
-      load_base(0, n0 + c * NT);
-    }
+    n0 = next;
   }
 }
 
@@ -651,15 +700,17 @@ __global__ __launch_bounds__(kThreads) void lora_up_kernel(UpArgs p) {
   constexpr int NP = sizeof(TO) == 4 ? 3 : 2;
   __shared__ __align__(16) Tile sh;
   __shared__ __align__(16) uint16_t lds[NP * kLoraTile * (RC + 8)];
+  __shared__ uint4 blds[kWaves][kUpCols * RC / 8];
   const int n = find_tile(p.tile, sh, blockIdx.x);
   if (n == 0) return;
   if (sh.adapter == p.tile.L) {
     copy_rows<TO, Vec>(p, sh, n);
     return;
   }
-  if (n <= 16) up_tile<TO, RC, Vec, 1>(p, sh, n, lds);
-  else if (n <= 32) up_tile<TO, RC, Vec, 2>(p, sh, n, lds);
-  else up_tile<TO, RC, Vec, 4>(p, sh, n, lds);
+  uint4* mine = blds[threadIdx.x >> 6];
+  if (n <= 16) up_tile<TO, RC, Vec, 1>(p, sh, n, lds, mine);
+  else if (n <= 32) up_tile<TO, RC, Vec, 2>(p, sh, n, lds, mine);
+  else up_tile<TO, RC, Vec, 4>(p, sh, n, lds, mine);
 }
 
 // ------------------------------------------------------------------ prep
@@ -675,7 +726,7 @@ struct PrepArgs {
   const float* h;             // [M][r]
   const float* scales;
   int64_t cap;
-  uint16_t* ht;               // [3][r][cap]
+  uint16_t* ht;
 };
 
 // One 64 x 64 block of in [R][C] (C a multiple of 8) to out [C][pitch], rows
@@ -702,12 +753,13 @@ __device__ __forceinline__ void transpose_block(const uint16_t* __restrict__ in,
   }
 }
 
-// The three bf16 parts of scale * (sum of the splits of part) at [part][rank]
-// [position in the grouping], zeros at the tile's padding; dh, if asked for,
-// receives the scaled sums.
+// The three bf16 parts of scale * (sum of the splits of part) as outer's
+// fragments: [32 positions of the grouping][part][16 ranks][lane], lane (g, c)
+// holding positions 8 g .. + 7 of rank c; zeros at the tile's padding. dh, if
+// asked for, receives the scaled sums.
 __device__ __forceinline__ void rank_major(const TileArgs& tile, const Tile& sh, int n, int index, int r,
                                            const float* part, int splits, const float* scales, float* dh, uint16_t* vt,
-                                           int64_t cap, float* lds) {
+                                           float* lds) {
   const int tid = threadIdx.x;
   const float scale = scales ? scales[sh.adapter] : 1.0f;
   const int pitch = r + 4, quads = r / 4;
@@ -727,16 +779,19 @@ __device__ __forceinline__ void rank_major(const TileArgs& tile, const Tile& sh,
     *(float4*)(lds + t * pitch + j) = v;
   }
   __syncthreads();
-  for (int i = tid; i < r * 8; i += kThreads) {
-    const int j = i >> 3, t = (i & 7) * 8;
+  const int ranks = (r + 15) / 16;
+  for (int i = tid; i < 2 * ranks * 64; i += kThreads) {
+    const int lane = i & 63, jt = (i >> 6) % ranks, half = (i >> 6) / ranks;
+    const int j = jt * 16 + (lane & 15), t = half * 32 + (lane >> 4) * 8;
     float f[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = lds[(t + e) * pitch + j];
+    for (int e = 0; e < 8; ++e) f[e] = j < r ? lds[(t + e) * pitch + j] : 0.0f;
     bf16x8_t q[3];
     split_parts<3>(f, q);
 #pragma unroll
     for (int e = 0; e < 3; ++e)
-      *(uint4*)(vt + ((int64_t)e * r + j) * cap + (int64_t)index * kLoraTile + t) = __builtin_bit_cast(uint4, q[e]);
+      *(uint4*)(vt + ((((int64_t)index * 2 + half) * 3 + e) * ranks + jt) * 512 + lane * 8) =
+          __builtin_bit_cast(uint4, q[e]);
   }
 }
 
@@ -762,9 +817,10 @@ __global__ __launch_bounds__(kThreads) void lora_prep_kernel(PrepArgs p) {
     return;
   }
   const int tile = (blockIdx.y - p.tile.L) * gridDim.x + blockIdx.x;
+  if (tile >= p.cap / kLoraTile) return;
   const int n = find_tile(p.tile, sh, tile);
   if (n == 0 || sh.adapter == p.tile.L) return;
-  rank_major(p.tile, sh, n, tile, p.r, p.h, 1, p.scales, nullptr, p.ht, p.cap, lds);
+  rank_major(p.tile, sh, n, tile, p.r, p.h, 1, p.scales, nullptr, p.ht, lds);
 }
 
 // dh: the sum of its splits, scaled, as it is and rank-major.
@@ -774,15 +830,14 @@ struct JoinArgs {
   const float* part;          // [splits][M][r]
   const float* scales;
   float* dh;                  // [M][r]
-  int64_t cap;
-  uint16_t* vt;               // [3][r][cap]
+  uint16_t* vt;
 };
 __global__ __launch_bounds__(kThreads) void lora_join_kernel(JoinArgs p) {
   __shared__ __align__(16) Tile sh;
   __shared__ __align__(16) float lds[kLoraTile * (kLoraMaxRank + 4)];
   const int n = find_tile(p.tile, sh, blockIdx.x);
   if (n == 0 || sh.adapter == p.tile.L) return;
-  rank_major(p.tile, sh, n, blockIdx.x, p.r, p.part, p.splits, p.scales, p.dh, p.vt, p.cap, lds);
+  rank_major(p.tile, sh, n, blockIdx.x, p.r, p.part, p.splits, p.scales, p.dh, p.vt, lds);
 }
 
 // ------------------------------------------------------------------ outer
@@ -790,7 +845,7 @@ struct OuterArgs {
   const void* u;              // [M, W]
   int64_t ldu;
   int W, r, M, L;
-  const uint16_t* vt;         // [3][r][cap]
+  const uint16_t* vt;         // fragments, as rank_major writes them
   int64_t cap;
   const int32_t* sorted;
   const int32_t* block_adapter;
@@ -823,6 +878,7 @@ __global__ __launch_bounds__(kThreads) void lora_outer_kernel(OuterArgs p) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
   const int w0 = blockIdx.x * 128;
   const int j0 = blockIdx.z * 64;
+  const int ranks = (p.r + 15) / 16;
   const int npp = p.offsets[p.L];
   const int p0 = blockIdx.y * p.chunk;
   if (p0 >= npp) return;
@@ -853,10 +909,10 @@ __global__ __launch_bounds__(kThreads) void lora_outer_kernel(OuterArgs p) {
     }
 #pragma unroll
     for (int jt = 0; jt < JT; ++jt) {
-      const int j = j0 + 16 * jt + c < p.r ? j0 + 16 * jt + c : p.r - 1;
+      const int at = j0 / 16 + jt < ranks ? j0 / 16 + jt : ranks - 1;
 #pragma unroll
       for (int q = 0; q < 3; ++q)
-        x.v[jt][q] = as_bf16x8(*(const uint4*)(p.vt + ((int64_t)q * p.r + j) * p.cap + pos + 8 * g));
+        x.v[jt][q] = as_bf16x8(*(const uint4*)(p.vt + (((int64_t)(pos / 32) * 3 + q) * ranks + at) * 512 + lane * 8));
     }
   };
   auto multiply = [&](const Frags& x) {
@@ -998,17 +1054,18 @@ bool vec_ok(const void* p, int64_t ld, bool f32) {
   return !p || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % (f32 ? 4 : 8) == 0);
 }
 
-hipError_t launch_down(const DownArgs& p, bool u_f32, int tiles, hipStream_t stream) {
+hipError_t launch_down(DownArgs p, bool u_f32, int tiles, hipStream_t stream) {
   const bool vec = vec_ok(p.u, p.ldu, u_f32) && p.W % (u_f32 ? 4 : 8) == 0;
+  p.split_steps = (int)ceil_div(ceil_div(p.W, u_f32 ? 32 : 64), p.splits);
   const dim3 grid(tiles, p.splits);
   auto go = [&](auto rt) {
     constexpr int RT = decltype(rt)::value;
     if (u_f32) {
-      if (vec) lora_down_kernel<float, RT, true><<<grid, kDownThreads, 0, stream>>>(p);
-      else lora_down_kernel<float, RT, false><<<grid, kDownThreads, 0, stream>>>(p);
+      if (vec) lora_down_kernel<float, RT, true><<<grid, kThreads, 0, stream>>>(p);
+      else lora_down_kernel<float, RT, false><<<grid, kThreads, 0, stream>>>(p);
     } else {
-      if (vec) lora_down_kernel<uint16_t, RT, true><<<grid, kDownThreads, 0, stream>>>(p);
-      else lora_down_kernel<uint16_t, RT, false><<<grid, kDownThreads, 0, stream>>>(p);
+      if (vec) lora_down_kernel<uint16_t, RT, true><<<grid, kThreads, 0, stream>>>(p);
+      else lora_down_kernel<uint16_t, RT, false><<<grid, kThreads, 0, stream>>>(p);
     }
   };
   if (p.r <= 16) go(std::integral_constant<int, 1>{});
@@ -1021,8 +1078,7 @@ hipError_t launch_down(const DownArgs& p, bool u_f32, int tiles, hipStream_t str
 hipError_t launch_up(UpArgs p, bool out_f32, int tiles, hipStream_t stream) {
   const bool vec = vec_ok(p.base, p.ld_base, out_f32) && vec_ok(p.out, p.ld_out, out_f32) &&
                    p.N % (out_f32 ? 4 : 8) == 0;
-  const int wave_cols = 16 * (out_f32 ? 4 : 8);
-  p.n_block = kWaves * wave_cols;
+  p.n_block = kWaves * kUpCols;
   const dim3 grid((unsigned)tiles, (unsigned)ceil_div(p.N, p.n_block));
   auto go = [&](auto rc) {
     constexpr int RC = decltype(rc)::value;
@@ -1070,13 +1126,12 @@ LoraLayout lora_layout(int64_t M, int64_t L, int64_t K, int64_t N, int64_t r, bo
   // a small batch has no padded lists: at most one tile per list and 64 rows
   o.tiles = (int)(o.small ? (M < M / kLoraTile + lists ? M : M / kLoraTile + lists) : o.cap / kLoraTile);
   // splits of the contraction: enough workgroups for the chip, each wave at
-  // least one 64-column step, and no more than 8 partial sums to add
+  // least one step, and no more than 8 partial sums to add
   const int64_t steps = ceil_div(backward ? N : K, 64);
-  int64_t splits = M > 0 ? ceil_div(256, ceil_div(M, kLoraTile)) : 1;
+  int64_t splits = M > 0 ? ceil_div(512, ceil_div(M, kLoraTile)) : 1;
   if (splits > 8) splits = 8;
-  if (splits > ceil_div(steps, kDownWaves)) splits = ceil_div(steps, kDownWaves);
-  o.split_steps = (int)ceil_div(steps, splits);
-  o.splits = (int)ceil_div(steps, o.split_steps);
+  if (splits > ceil_div(steps, kWaves)) splits = ceil_div(steps, kWaves);
+  o.splits = (int)ceil_div(steps, ceil_div(steps, splits));
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t off = at;
@@ -1094,8 +1149,8 @@ LoraLayout lora_layout(int64_t M, int64_t L, int64_t K, int64_t N, int64_t r, bo
     o.at_off = take(L * K * r * 2);
     o.bt_off = take(L * r * o.n_pad * 2);
     o.dh_off = take(M * r * 4);
-    o.dht_off = take(3 * r * o.cap * 2);
-    o.ht_off = take(3 * r * o.cap * 2);
+    o.dht_off = take(3 * ceil_div(r, 16) * 16 * o.cap * 2);
+    o.ht_off = take(3 * ceil_div(r, 16) * 16 * o.cap * 2);
     // positions per workgroup of the weight gradients: at least 8 r, so that
     // the partial sums are at most a quarter of the rows' bytes, and enough
     // workgroups for the chip
@@ -1142,7 +1197,7 @@ hipError_t launch_lora_forward(const LoraArgs& a, hipStream_t stream) {
   d.tile = t;
   d.u = a.x; d.ldu = a.ldx; d.W = a.K;
   d.v = a.a; d.v_stride = (int64_t)a.r * a.K; d.ldv = a.K; d.r = a.r;
-  d.splits = o.splits; d.split_steps = o.split_steps;
+  d.splits = o.splits;
   d.part = (float*)(a.ws + o.part_off); d.h = a.h;
   UpArgs u{};
   u.tile = t; u.r = a.r; u.N = a.N;
@@ -1179,12 +1234,12 @@ hipError_t launch_lora_backward(const LoraArgs& a, hipStream_t stream) {
     d.tile = t;
     d.u = a.dout; d.ldu = a.ld_dout; d.W = a.N;
     d.v = f.bt; d.v_stride = a.r * o.n_pad; d.ldv = o.n_pad; d.r = a.r;
-    d.splits = o.splits; d.split_steps = o.split_steps;
+    d.splits = o.splits;
     d.part = (float*)(a.ws + o.part_off);
     if ((err = launch_down(d, a.y_f32, o.tiles, stream)) != hipSuccess) return err;
     JoinArgs j{};
     j.tile = t; j.r = a.r; j.splits = o.splits; j.part = d.part; j.scales = a.scales;
-    j.dh = (float*)(a.ws + o.dh_off); j.cap = o.cap; j.vt = (uint16_t*)(a.ws + o.dht_off);
+    j.dh = (float*)(a.ws + o.dh_off); j.vt = (uint16_t*)(a.ws + o.dht_off);
     lora_join_kernel<<<o.tiles, kThreads, 0, stream>>>(j);
     if ((err = hipGetLastError()) != hipSuccess) return err;
     if (a.dx) {

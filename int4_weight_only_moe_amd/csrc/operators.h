@@ -79,11 +79,11 @@ constexpr int kLoraSmallRows = 256;  // rows up to which a forward needs no grou
 struct LoraLayout {
   int64_t cap;                                  // padded rows the grouping may reach
   int tiles;                                    // workgroups' tiles: cap / 64, or a small batch's bound
-  int splits, split_steps;                      // of the contraction (forward K, backward N), in 64-column steps
+  int splits;                                   // of the contraction (forward K, backward N)
   bool small;
   int64_t sorted_off, block_off, offs_off, part_off;
   int64_t at_off, bt_off, n_pad;                // backward: A^T [L, K, r], B^T [L, r, n_pad]
-  int64_t dh_off, dht_off, ht_off;              // backward: dh [M, r]; [3][r][cap] bf16 parts of dh and s*h
+  int64_t dh_off, dht_off, ht_off;              // backward: dh [M, r]; bf16 parts of dh and s*h, rank-major
   int64_t a_slots_off, b_slots_off;             // backward: partial gradients [slots][r * K], [slots][N * r]
   int a_chunk, b_chunk;                         // positions per partial of dA and dB
   int64_t total;
