@@ -490,6 +490,23 @@ __global__ __launch_bounds__(kThreads) void lora_down_kernel(DownArgs p) {
   }
 }
 
+// h: the sum of its splits; 0 for rows without an adapter.
+__global__ __launch_bounds__(kThreads) void lora_sum_kernel(const float* __restrict__ part, int splits, int64_t size,
+                                                            int r, const int32_t* __restrict__ ids, int L,
+                                                            float* __restrict__ h) {
+  const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
+  if (i >= size) return;
+  const int id = ids[i / r];
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+  for (int s = 0; s < splits; ++s) {
+    const float4 x = *(const float4*)(part + s * size + i);
+    v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+  }
+  if (id < 0 || id >= L) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  *(float4*)(h + i) = v;
+}
+
 // ------------------------------------------------------------------ up
 struct UpArgs {
   TileArgs tile;
@@ -617,7 +634,7 @@ __device__ __forceinline__ void up_tile(const UpArgs& p, const Tile& sh, int n, 
   const uint16_t* b = p.b + (int64_t)sh.adapter * p.N * p.r;
   const int n_end = (int)(blockIdx.y + 1) * p.n_block < p.N ? (int)(blockIdx.y + 1) * p.n_block : p.N;
   int n0 = blockIdx.y * p.n_block + wave * kUpCols;
-  uint4 braw[kChunks], base[4];
+  uint4 braw[kChunks], base[NSUB][4];
   auto load_b = [&](int first) {
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
@@ -628,12 +645,13 @@ __device__ __forceinline__ void up_tile(const UpArgs& p, const Tile& sh, int n, 
   auto load_base = [&](int ts, int col) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      base[q] = p.base ? load4<TO, Vec>((const TO*)p.base + (int64_t)sh.rows[ts * kSub + 4 * g + q] * p.ld_base, col, p.N)
+      base[ts][q] = p.base ? load4<TO, Vec>((const TO*)p.base + (int64_t)sh.rows[ts * kSub + 4 * g + q] * p.ld_base, col, p.N)
                        : make_uint4(0, 0, 0, 0);
   };
   if (n0 < n_end) {
     load_b(n0);
-    load_base(0, n0 + 4 * c);
+#pragma unroll
+    for (int ts = 0; ts < NSUB; ++ts) load_base(ts, n0 + 4 * c);
   }
   up_factor<RC, NP>(p, sh, n, lds);
   __syncthreads();
@@ -658,9 +676,8 @@ __device__ __forceinline__ void up_tile(const UpArgs& p, const Tile& sh, int n, 
 #pragma unroll
     for (int ts = 0; ts < NSUB; ++ts) {
       f32x4_t acc[4];
-      const uint4 in[4] = {base[0], base[1], base[2], base[3]};
-      if (ts + 1 < NSUB) load_base(ts + 1, col);
-      else if (next < n_end) load_base(0, next + 4 * c);
+      const uint4 in[4] = {base[ts][0], base[ts][1], base[ts][2], base[ts][3]};
+      if (next < n_end) load_base(ts, next + 4 * c);
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -867,9 +884,9 @@ struct OuterArgs {
 template <typename TU, int JT, bool VecU>
 __global__ __launch_bounds__(kThreads) void lora_outer_kernel(OuterArgs p) {
   constexpr bool kF32 = std::is_same<TU, float>::value;
-  // the next step's loads go out before this one's products where the
-  // registers hold both (fp32 columns take four times a bf16 step's)
-  constexpr bool kAhead = JT == 1 || (!kF32 && (VecU || JT == 2));
+  // the next two steps' loads are in flight during this one's products where
+  // the registers hold them (fp32 columns take four times a bf16 step's)
+  constexpr bool kAhead = !kF32 && VecU;
   constexpr int kVecs = 8 * JT;                         // accumulators of a wave
   constexpr int kRound = kVecs < 16 ? kVecs : 16;       // of them in LDS at a time
   constexpr int kPiece = 1024;                          // positions whose rows are in LDS at a time
@@ -962,20 +979,29 @@ __global__ __launch_bounds__(kThreads) void lora_outer_kernel(OuterArgs p) {
       __syncthreads();
       int pos = piece + 32 * wave;
       if (pos < end) {
-        Frags cur;
-        load(pos, piece, cur);
-        for (pos += 32 * kWaves; pos < end; pos += 32 * kWaves) {
-          if constexpr (kAhead) {
-            Frags next;
-            load(pos, piece, next);
-            multiply(cur);
-            cur = next;
-          } else {
-            multiply(cur);
-            load(pos, piece, cur);
+        constexpr int kStep = 32 * kWaves;
+        if constexpr (kAhead) {
+          Frags f0, f1, f2;
+          load(pos, piece, f0);
+          if (pos + kStep < end) load(pos + kStep, piece, f1);
+          while (true) {
+            if (pos + 2 * kStep < end) load(pos + 2 * kStep, piece, f2);
+            multiply(f0);
+            if ((pos += kStep) >= end) break;
+            if (pos + 2 * kStep < end) load(pos + 2 * kStep, piece, f0);
+            multiply(f1);
+            if ((pos += kStep) >= end) break;
+            if (pos + 2 * kStep < end) load(pos + 2 * kStep, piece, f1);
+            multiply(f2);
+            if ((pos += kStep) >= end) break;
+          }
+        } else {
+          for (; pos < end; pos += kStep) {
+            Frags f;
+            load(pos, piece, f);
+            multiply(f);
           }
         }
-        multiply(cur);
       }
     }
     // join: lane (g, c) has columns 8 c + i, ranks 16 jt + 4 g + q. Four
@@ -1078,7 +1104,11 @@ hipError_t launch_down(DownArgs p, bool u_f32, int tiles, hipStream_t stream) {
 hipError_t launch_up(UpArgs p, bool out_f32, int tiles, hipStream_t stream) {
   const bool vec = vec_ok(p.base, p.ld_base, out_f32) && vec_ok(p.out, p.ld_out, out_f32) &&
                    p.N % (out_f32 ? 4 : 8) == 0;
-  p.n_block = kWaves * kUpCols;
+  // four workgroups a CU, each going on to further columns with its next loads in flight
+  int64_t groups = tiles * ceil_div(p.N, kWaves * kUpCols) / 1024;
+  if (groups < 1) groups = 1;
+  if (groups > 8) groups = 8;
+  p.n_block = (int)groups * kWaves * kUpCols;
   const dim3 grid((unsigned)tiles, (unsigned)ceil_div(p.N, p.n_block));
   auto go = [&](auto rc) {
     constexpr int RC = decltype(rc)::value;
@@ -1143,6 +1173,7 @@ LoraLayout lora_layout(int64_t M, int64_t L, int64_t K, int64_t N, int64_t r, bo
     o.sorted_off = take(o.cap * 4);
     o.block_off = take(o.cap / kLoraTile * 4);
     o.offs_off = take((L + 2) * 4);
+    if (!backward) o.h_off = take(M * r * 4);
   }
   if (backward) {
     o.n_pad = ceil_div(N, 8) * 8;
@@ -1151,14 +1182,15 @@ LoraLayout lora_layout(int64_t M, int64_t L, int64_t K, int64_t N, int64_t r, bo
     o.dh_off = take(M * r * 4);
     o.dht_off = take(3 * ceil_div(r, 16) * 16 * o.cap * 2);
     o.ht_off = take(3 * ceil_div(r, 16) * 16 * o.cap * 2);
-    // positions per workgroup of the weight gradients: at least 8 r, so that
-    // the partial sums are at most a quarter of the rows' bytes, and enough
-    // workgroups for the chip
+    // positions per workgroup of the weight gradients: as many workgroups as
+    // the chip holds at once (ranks above 32: one a CU, else two), so that
+    // partial sums are few; at least one step for each wave
     auto chunk = [&](int64_t W) {
-      int64_t c = M * ceil_div(W, 128) * ceil_div(r, 64) / 512;
-      c = c > 8 * r ? c : 8 * r;
-      c = c > 128 ? c : 128;
-      return ceil_div(c, kLoraTile) * kLoraTile;
+      const int64_t across = ceil_div(W, 128) * ceil_div(r, 64);
+      int64_t cuts = (r > 32 ? 256 : 512) / across;
+      cuts = cuts < 1 ? 1 : cuts;
+      const int64_t c = ceil_div(o.cap, cuts);
+      return ceil_div(c > 128 ? c : 128, kLoraTile) * kLoraTile;
     };
     o.a_chunk = (int)chunk(K);
     o.b_chunk = (int)chunk(N);
@@ -1205,6 +1237,14 @@ hipError_t launch_lora_forward(const LoraArgs& a, hipStream_t stream) {
   u.part = d.part; u.splits = o.splits; u.scales = a.scales; u.h = a.h;
   err = launch_down(d, false, o.tiles, stream);
   if (err != hipSuccess) return err;
+  if (!o.small && o.splits > 1) {  // every workgroup of up would add the same splits again
+    float* h = a.h ? a.h : (float*)(a.ws + o.h_off);
+    const int64_t size = (int64_t)a.M * a.r;
+    lora_sum_kernel<<<(unsigned)ceil_div(size, 4 * kThreads), kThreads, 0, stream>>>(d.part, o.splits, size, a.r, a.ids,
+                                                                                    a.L, h);
+    if ((err = hipGetLastError()) != hipSuccess) return err;
+    u.part = h; u.splits = 1; u.h = nullptr;
+  }
   return launch_up(u, a.y_f32, o.tiles, stream);
 }
 

@@ -81,7 +81,7 @@ struct LoraLayout {
   int tiles;                                    // workgroups' tiles: cap / 64, or a small batch's bound
   int splits;                                   // of the contraction (forward K, backward N)
   bool small;
-  int64_t sorted_off, block_off, offs_off, part_off;
+  int64_t sorted_off, block_off, offs_off, part_off, h_off;
   int64_t at_off, bt_off, n_pad;                // backward: A^T [L, K, r], B^T [L, r, n_pad]
   int64_t dh_off, dht_off, ht_off;              // backward: dh [M, r]; bf16 parts of dh and s*h, rank-major
   int64_t a_slots_off, b_slots_off;             // backward: partial gradients [slots][r * K], [slots][N * r]
