@@ -342,47 +342,60 @@ def moe_mxfp4_layer(*args, **kw) -> None:
 
 
 # ------------------------------------------------------------------ operators beside the layer
-def _shaped(t: torch.Tensor | None, dtype, shape: tuple, what: str, device: torch.device) -> int:
-    """The pointer of a contiguous tensor of this type and shape on this device (None: NULL)."""
-    if t is None:
-        return 0
+def _refuse(t: torch.Tensor, dtype, shape: tuple, what: str, device: torch.device, layout: str):
     if t.device != device:
         raise ValueError(f"{what} must be on {device}, got {t.device}")
     if t.dtype != dtype:
         raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{what} must have shape {shape}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{what} must {layout}")
+
+
+def _shaped(t: torch.Tensor | None, dtype, shape: tuple, what: str, device: torch.device) -> int:
+    """The pointer of a contiguous tensor of this type and shape on this device (None: NULL)."""
+    if t is None:
+        return 0
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device:
+        return t.data_ptr()
+    _refuse(t, dtype, shape, what, device, "be contiguous")
 
 
 def _matrix(t: torch.Tensor | None, dtype, shape: tuple, what: str, device: torch.device) -> tuple:
     """(pointer, row stride) of a matrix whose rows are contiguous (None: NULL)."""
     if t is None:
         return 0, 0
-    if t.device != device:
-        raise ValueError(f"{what} must be on {device}, got {t.device}")
-    if t.dtype != dtype:
-        raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{what} must have shape {shape}, got {tuple(t.shape)}")
-    rows, cols = t.stride()
-    if cols != 1 and shape[1] > 1:
-        raise ValueError(f"{what} must have contiguous rows")
-    if shape[0] <= 1:  # the stride of a single row says nothing
-        rows = -(-shape[1] // 8) * 8
-    return t.data_ptr(), rows
+    if t.dtype is dtype and t.shape == shape and t.device == device:
+        rows, cols = t.stride()
+        if cols == 1 or shape[1] <= 1:
+            # the stride of a single row says nothing
+            return t.data_ptr(), rows if shape[0] > 1 else -(-shape[1] // 8) * 8
+    _refuse(t, dtype, shape, what, device, "have contiguous rows")
+
+
+def _buffer(t: torch.Tensor, what: str, device: torch.device) -> tuple:
+    """(pointer, bytes) of a workspace."""
+    if t.dtype is not torch.uint8 or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous uint8 tensor on {device}")
+    return t.data_ptr(), t.numel()
 
 
 def _on_device(device: torch.device, name: str, stream, *args) -> None:
     """Call an entry point with `device` current, on `stream` or that device's current stream."""
     if device.type != "cuda":
         raise ValueError(f"{name} needs device tensors")
-    if device.index != torch.cuda.current_device():
+    if stream is None:  # the stream's handle without the object that torch.cuda.current_stream makes
+        stream = torch._C._cuda_getCurrentRawStream(device.index)
+    elif isinstance(stream, torch.cuda.Stream):
+        stream = stream.cuda_stream
+    fn = getattr(lib(), name)
+    if device.index == torch.cuda.current_device():
+        status = fn(*args, stream)
+    else:
         with torch.cuda.device(device):
-            return _check(name, getattr(lib(), name)(*args, _stream(stream)))
-    _check(name, getattr(lib(), name)(*args, _stream(stream)))
+            status = fn(*args, stream)
+    if status != MOE_OK:
+        raise MoeError(name, status)
 
 
 def moe_balance_workspace_bytes(M: int, E: int, S: int) -> int:
@@ -414,7 +427,7 @@ def moe_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, expert_counts
                _shaped(prob_sums, torch.float32, (S, E), "prob_sums", dev),
                _shaped(seq_tokens, torch.int32, (S,), "seq_tokens", dev),
                _shaped(loss, torch.float32, (S,), "loss", dev),
-               _shaped(workspace, torch.uint8, tuple(workspace.shape), "workspace", dev), workspace.numel())
+               *_buffer(workspace, "workspace", dev))
 
 
 def moe_balance_loss_backward(logits: torch.Tensor, top_k: int, expert_counts: torch.Tensor,
@@ -461,7 +474,7 @@ def moe_lora_forward(x: torch.Tensor, adapter_ids: torch.Tensor, lora_a: torch.T
                M, L, K, N, r, _shaped(lora_a, bf16, (L, r, K), "lora_a", dev),
                _shaped(lora_b, bf16, (L, N, r), "lora_b", dev), _shaped(scales, f32, (L,), "scales", dev), pb, ldb,
                po, ldo, kind, _shaped(h, f32, (M, r), "h", dev),
-               _shaped(workspace, torch.uint8, tuple(workspace.shape), "workspace", dev), workspace.numel())
+               *_buffer(workspace, "workspace", dev))
 
 
 def moe_lora_backward(grad_out: torch.Tensor, x: torch.Tensor, adapter_ids: torch.Tensor, h: torch.Tensor,
@@ -480,7 +493,7 @@ def moe_lora_backward(grad_out: torch.Tensor, x: torch.Tensor, adapter_ids: torc
                N, r, _shaped(lora_a, bf16, (L, r, K), "lora_a", dev), _shaped(lora_b, bf16, (L, N, r), "lora_b", dev),
                _shaped(scales, f32, (L,), "scales", dev), pb, ldb, pd, ldd,
                _shaped(grad_a, f32, (L, r, K), "grad_a", dev), _shaped(grad_b, f32, (L, N, r), "grad_b", dev),
-               _shaped(workspace, torch.uint8, tuple(workspace.shape), "workspace", dev), workspace.numel())
+               *_buffer(workspace, "workspace", dev))
 
 
 # ------------------------------------------------------------------ measurement helpers
