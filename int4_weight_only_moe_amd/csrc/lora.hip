@@ -13,8 +13,8 @@
 //   down    contracts a wide side with a [r, W] operand (h, dh) in splits of W;
 //   up      adds the splits, expands r values to a wide side and adds the base
 //           (out, dx);
-//   prep    backward: the transposed weights, and s h rank-major;
-//   join    backward: dh, the sum of its splits, as it is and rank-major;
+//   join    backward: dh, the sum of its splits, as it is and rank-major, and
+//           s h rank-major (the transposed weights are made beside the grouping);
 //   outer   sums rows' outer products (dA, dB), reduce joins what was cut.
 // With r <= 128 each of them moves the wide side once and is bound by that
 // traffic, so the products are made exact where that is free: bf16 operands
@@ -95,6 +95,12 @@ __device__ __forceinline__ void load8(const float* __restrict__ row, int w, int 
   }
 }
 
+// Two fp32 values rounded to bf16, the first in the low half.
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)lo, (__bf16)hi});
+}
+
 // Whether every lane of `live` holds the same key as its first one.
 __device__ __forceinline__ bool one_key(int key, uint64_t live) {
   const int first = __builtin_amdgcn_readfirstlane(__shfl(key, (int)__builtin_ctzll(live | (uint64_t(1) << 63)), 64));
@@ -122,24 +128,114 @@ constexpr int kGroupThreads = 1024;
 constexpr int kGroupWaves = kGroupThreads / 64;
 constexpr int kMaxKeys = 1025;  // 1024 adapters and "none"
 
+// Backward: the weights of the adapters that have rows, transposed. Workgroups
+// 1.. of the grouping's launch do it, without waiting for the grouping.
+struct TransposeArgs {
+  const uint16_t* a;        // [L][r][K]
+  const uint16_t* b;        // [L][N][r]
+  int K, N, r;
+  int64_t n_pad;
+  uint16_t* at;             // [L][K][r]
+  uint16_t* bt;             // [L][r][n_pad], zeros from N
+  int a_blocks, b_blocks;   // workgroups per adapter
+};
+
 struct GroupArgs {
   const int32_t* ids;       // [M]
   int M, L;
   int32_t* sorted;          // rows by adapter, each list padded to 64 with M
-  int32_t* block_adapter;   // a tile's adapter, L: rows without one
+  int4* tiles;              // a tile's adapter (L: rows without one), rows, and its list's range of positions
   int32_t* offsets;         // [L + 2]: each list's first position; [L] the first row without an adapter
+  int all_tiles;            // room for: tiles past the last have no rows
 };
+
+// One 64 x 64 block of in [R][C] (C a multiple of 8) to out [C][pitch], rows
+// from R on as zeros up to the pitch.
+__device__ __forceinline__ void transpose_block(const uint16_t* __restrict__ in, int R, int C, int64_t pitch,
+                                                uint16_t* __restrict__ out, int r0, int c0, uint16_t* lds) {
+  constexpr int kPitch = 64 + 8;
+  const int tid = threadIdx.x;
+  if (tid < 64 * 8) {
+    const int i = tid, row = i >> 3, col = (i & 7) * 8;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (r0 + row < R && c0 + col < C) v = *(const uint4*)(in + (int64_t)(r0 + row) * C + c0 + col);
+    *(uint4*)(lds + row * kPitch + col) = v;
+  }
+  __syncthreads();
+  if (tid < 64 * 8) {
+    const int i = tid, col = i >> 3, row = (i & 7) * 8;
+    if (c0 + col >= C || r0 + row >= pitch) return;
+    uint32_t d[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      d[e] = lds[(row + 2 * e) * kPitch + col] | (uint32_t)lds[(row + 2 * e + 1) * kPitch + col] << 16;
+    *(uint4*)(out + (int64_t)(c0 + col) * pitch + r0 + row) = make_uint4(d[0], d[1], d[2], d[3]);
+  }
+}
+
+// Each of these workgroups lists the adapters that have rows, then takes every
+// gridDim.x - 1'th block of their weights.
+__device__ __forceinline__ void transpose_weights(const GroupArgs& g, const TransposeArgs& p, int* room) {
+  int* used = room;                          // [1024]
+  int* list = room + kGroupThreads;          // [1024]
+  int* wave_n = list + kGroupThreads;        // [16]
+  uint16_t* lds = (uint16_t*)(wave_n + 16);  // 64 x 72
+  const int tid = threadIdx.x, wave = tid >> 6;
+  used[tid] = 0;
+  __syncthreads();
+  constexpr int kAhead = 8;
+  for (int f = tid; f < g.M; f += kAhead * kGroupThreads) {
+    int id[kAhead];
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) id[q] = g.ids[f + q * kGroupThreads < g.M ? f + q * kGroupThreads : f];
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q)
+      if (id[q] >= 0 && id[q] < g.L) used[id[q]] = 1;
+  }
+  __syncthreads();
+  const bool mine = used[tid] != 0;
+  const uint64_t live = __ballot(mine);
+  if ((tid & 63) == 0) wave_n[wave] = __builtin_popcountll(live);
+  __syncthreads();
+  int before = bits_below(live), n = 0;
+#pragma unroll
+  for (int w = 0; w < kGroupWaves; ++w) {
+    before += w < wave ? wave_n[w] : 0;
+    n += wave_n[w];
+  }
+  if (mine) list[before] = tid;
+  __syncthreads();
+  const int per = p.a_blocks + p.b_blocks;
+  const int across = (p.K + 63) / 64, down = (int)((p.n_pad + 63) / 64);
+  for (int64_t item = blockIdx.x - 1; item < (int64_t)n * per; item += gridDim.x - 1) {
+    const int l = list[item / per];
+    int i = (int)(item % per);
+    if (i < p.a_blocks) {
+      const int64_t at = (int64_t)l * p.r * p.K;
+      transpose_block(p.a + at, p.r, p.K, p.r, p.at + at, i / across * 64, i % across * 64, lds);
+    } else {
+      i -= p.a_blocks;
+      transpose_block(p.b + (int64_t)l * p.N * p.r, p.N, p.r, p.n_pad, p.bt + l * p.r * p.n_pad, i % down * 64,
+                      i / down * 64, lds);
+    }
+    __syncthreads();
+  }
+}
 
 // Stable grouping by one workgroup: each wave walks a contiguous range of the
 // rows 64 at a time, counts its rows per adapter (one LDS update per distinct
 // adapter of a step, so rows of one adapter in a run cost no more than mixed
 // ones), the counts become each wave's first positions, and a second walk
 // places the rows. The ids are read twice; 8192 rows take 8 steps a wave.
-__global__ __launch_bounds__(kGroupThreads) void lora_group_kernel(GroupArgs p) {
-  __shared__ int cnt[kGroupWaves][kMaxKeys];
-  __shared__ int off[kMaxKeys + 1];
+__global__ __launch_bounds__(kGroupThreads) void lora_group_kernel(GroupArgs p, TransposeArgs weights) {
+  __shared__ __align__(16) int cnt[kGroupWaves][kMaxKeys];
+  __shared__ int off[kMaxKeys + 1], rows_of[kMaxKeys];
   __shared__ int wave_tot[kGroupWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  if (blockIdx.x > 0) {
+    transpose_weights(p, weights, &cnt[0][0]);
+    return;
+  }
   const int keys = p.L + 1;
   const int nbits = 32 - __clz(p.L);
   for (int i = tid; i < keys; i += kGroupThreads)
@@ -196,6 +292,7 @@ __global__ __launch_bounds__(kGroupThreads) void lora_group_kernel(GroupArgs p) 
   // a list's rows, then the padding; the waves' counts become first positions
   auto lay = [&](int key, int first, int count, int room) {
     off[key] = first;
+    rows_of[key] = count;
     p.offsets[key] = first;
     for (int i = first + count; i < first + room; ++i) p.sorted[i] = p.M;
     int run = first;
@@ -217,13 +314,18 @@ __global__ __launch_bounds__(kGroupThreads) void lora_group_kernel(GroupArgs p) 
   }
   __syncthreads();
   const int tiles = off[p.L + 1] / kLoraTile;
-  for (int b = tid; b < tiles; b += kGroupThreads) {
+  for (int b = tid; b < p.all_tiles; b += kGroupThreads) {
+    if (b >= tiles) {
+      p.tiles[b] = make_int4(p.L, 0, 0, 0);
+      continue;
+    }
     int lo = 0, hi = p.L;  // the last list that starts at or before the tile
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (off[mid] <= b * kLoraTile) lo = mid; else hi = mid - 1;
     }
-    p.block_adapter[b] = lo;
+    const int left = off[lo] + rows_of[lo] - b * kLoraTile;
+    p.tiles[b] = make_int4(lo, left < kLoraTile ? left : kLoraTile, off[lo], off[lo + 1]);
   }
   walk([&](int row, int key, int before_me, int total_same) {
     // every lane reads the running position before the first lane advances it
@@ -238,8 +340,7 @@ __global__ __launch_bounds__(kGroupThreads) void lora_group_kernel(GroupArgs p) 
 struct TileArgs {
   const int32_t* ids;            // [M]
   const int32_t* sorted;         // the grouping, or null: a small batch
-  const int32_t* block_adapter;
-  const int32_t* offsets;        // [L + 2]
+  const int4* tiles;
   int M, L;
 };
 struct Tile {
@@ -255,21 +356,14 @@ struct Tile {
 __device__ __forceinline__ int find_tile(const TileArgs& p, Tile& sh, int tile) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   if (p.sorted) {
-    // all loads at once: the lists' buffers have room for every tile of the grid
+    const int4 info = p.tiles[tile];
     const int first = p.sorted[tile * kLoraTile];
     const int row = p.sorted[tile * kLoraTile + lane];
-    const int adapter = p.block_adapter[tile];
-    if (tile * kLoraTile >= p.offsets[p.L + 1]) return 0;
-    if (tid < kLoraTile) {
-      sh.rows[tid] = row < p.M ? row : first;
-      const uint64_t live = __ballot(row < p.M);
-      if (tid == 0) {
-        sh.count = __builtin_popcountll(live);
-        sh.adapter = adapter;
-      }
-    }
+    if (info.y == 0) return 0;
+    if (tid < kLoraTile) sh.rows[tid] = row < p.M ? row : first;
+    if (tid == 0) sh.adapter = info.x;
     __syncthreads();
-    return sh.count;
+    return info.y;
   }
   int key = -1;
   if (tid < p.M) {
@@ -524,22 +618,23 @@ struct UpArgs {
 };
 
 // Four consecutive columns from n of a row, as raw bits (fp32: one word each,
-// bf16: two words in all). Vec: the row is 16-byte aligned and N % 4 == 0.
+// bf16: two words in all); columns past the end hold anything. Vec: the row is 16-byte aligned and N % 4 == 0.
 template <typename TO, bool Vec>
 __device__ __forceinline__ uint4 load4(const TO* row, int n, int N) {
-  uint32_t d[4] = {0, 0, 0, 0};
+  // columns past the end read the row's first ones: a load that is always made
+  // keeps the count of loads in flight known
   if constexpr (Vec) {
-    if (n >= N) return make_uint4(0, 0, 0, 0);
-    if constexpr (sizeof(TO) == 4) return *(const uint4*)(row + n);
-    const uint2 v = *(const uint2*)(row + n);
+    const TO* at = row + (n < N ? n : 0);
+    if constexpr (sizeof(TO) == 4) return *(const uint4*)at;
+    const uint2 v = *(const uint2*)at;
     return make_uint4(v.x, v.y, 0, 0);
   } else {
+    uint32_t d[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (n + i < N) {
-        if constexpr (sizeof(TO) == 4) d[i] = __float_as_uint(row[n + i]);
-        else d[i / 2] |= (uint32_t)row[n + i] << (16 * (i & 1));
-      }
+      const TO x = row[n + i < N ? n + i : 0];
+      if constexpr (sizeof(TO) == 4) d[i] = __float_as_uint(x);
+      else d[i / 2] |= (uint32_t)x << (16 * (i & 1));
     }
     return make_uint4(d[0], d[1], d[2], d[3]);
   }
@@ -562,22 +657,6 @@ __device__ __forceinline__ void store4(TO* row, int n, int N, uint4 v) {
   }
 }
 
-// Rows without an adapter: out = base (nothing to do in place), or zeros.
-template <typename TO, bool Vec>
-__device__ __forceinline__ void copy_rows(const UpArgs& p, const Tile& sh, int n) {
-  if (p.base == p.out) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int n0 = blockIdx.y * p.n_block, n1 = n0 + p.n_block < p.N ? n0 + p.n_block : p.N;
-  for (int t = wave; t < n; t += kWaves) {
-    TO* out = (TO*)p.out + (int64_t)sh.rows[t] * p.ld_out;
-    const TO* base = (const TO*)p.base + (int64_t)sh.rows[t] * p.ld_base;
-    for (int col = n0 + lane * 4; col < n1; col += 64 * 4)
-      store4<TO, Vec>(out, col, p.N, p.base ? load4<TO, Vec>(base, col, p.N) : make_uint4(0, 0, 0, 0));
-  }
-}
-
-constexpr int up_np(bool f32) { return f32 ? 3 : 2; }
-
 // The tile's factor in LDS: the sums of the partial sums, scaled, as bf16 parts.
 template <int RC, int NP>
 __device__ __forceinline__ void up_factor(const UpArgs& p, const Tile& sh, int n, uint16_t* lds) {
@@ -596,7 +675,7 @@ __device__ __forceinline__ void up_factor(const UpArgs& p, const Tile& sh, int n
         const float4 x = *(const float4*)(p.part + s * split_size + at);
         v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
       }
-      if (p.h && blockIdx.y == 0) *(float4*)(p.h + at) = v;
+      if (p.h && blockIdx.x == 0) *(float4*)(p.h + at) = v;
     }
     float f[4] = {v.x * scale, v.y * scale, v.z * scale, v.w * scale};
 #pragma unroll
@@ -623,8 +702,10 @@ constexpr int kUpCols = 64;  // columns of a wave
 // 16 lanes read and write 128 (fp32: 256) consecutive bytes of a row. b's 64
 // rows are consecutive in memory and go through the wave's own part of LDS, as
 // in down. What does not depend on the factor is loaded before it is made.
-template <typename TO, int RC, bool Vec, int NSUB>
-__device__ __forceinline__ void up_tile(const UpArgs& p, const Tile& sh, int n, uint16_t* lds, uint4* blds) {
+// None: rows without an adapter, out = base.
+template <typename TO, int RC, bool Vec, int NSUB, bool None = false>
+__device__ __forceinline__ void up_tile(const UpArgs& p, const Tile& sh, int n, uint16_t* lds, uint4* blds,
+                                        int64_t (*offs)[kLoraTile]) {
   constexpr int NP = sizeof(TO) == 4 ? 3 : 2;
   constexpr int kChunks = RC / 8;                         // 8-wide chunks of a part
   constexpr int kSteps = (NP * kChunks + 3) / 4;          // 32-wide steps
@@ -632,10 +713,21 @@ __device__ __forceinline__ void up_tile(const UpArgs& p, const Tile& sh, int n, 
   constexpr int kPitch = RC + 8;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
   const uint16_t* b = p.b + (int64_t)sh.adapter * p.N * p.r;
-  const int n_end = (int)(blockIdx.y + 1) * p.n_block < p.N ? (int)(blockIdx.y + 1) * p.n_block : p.N;
-  int n0 = blockIdx.y * p.n_block + wave * kUpCols;
+  const int n_end = (int)(blockIdx.x + 1) * p.n_block < p.N ? (int)(blockIdx.x + 1) * p.n_block : p.N;
+  int n0 = blockIdx.x * p.n_block + wave * kUpCols;
   uint4 braw[kChunks], base[NSUB][4];
+  // without a base the loads read out, and their values are dropped
+  const TO* from = p.base ? (const TO*)p.base : (const TO*)p.out;
+  const uint32_t keep = p.base ? 0xffffffffu : 0u;
+  // the rows' offsets once a tile: a 64-bit product for each load and store
+  // took longer than the matrix cores
+  if (threadIdx.x < kLoraTile) {
+    offs[0][threadIdx.x] = sh.rows[threadIdx.x] * (p.base ? p.ld_base : p.ld_out);
+    offs[1][threadIdx.x] = sh.rows[threadIdx.x] * p.ld_out;
+  }
+  __syncthreads();
   auto load_b = [&](int first) {
+    if constexpr (None) return;
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
       const int col = first + (i * 64 + lane) / kChunks;
@@ -645,43 +737,49 @@ __device__ __forceinline__ void up_tile(const UpArgs& p, const Tile& sh, int n, 
   auto load_base = [&](int ts, int col) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      base[ts][q] = p.base ? load4<TO, Vec>((const TO*)p.base + (int64_t)sh.rows[ts * kSub + 4 * g + q] * p.ld_base, col, p.N)
-                       : make_uint4(0, 0, 0, 0);
+      base[ts][q] = load4<TO, Vec>(from + offs[0][ts * kSub + 4 * g + q], col, p.N);
   };
   if (n0 < n_end) {
     load_b(n0);
 #pragma unroll
     for (int ts = 0; ts < NSUB; ++ts) load_base(ts, n0 + 4 * c);
   }
-  up_factor<RC, NP>(p, sh, n, lds);
-  __syncthreads();
-  while (n0 < n_end) {
+  if constexpr (!None) {
+    up_factor<RC, NP>(p, sh, n, lds);
+    __syncthreads();
+  }
+  auto columns = [&](auto more) {  // more: the wave has another group of columns, whose loads go out
     const int col = n0 + 4 * c;
-    // row m of b, chunk k at slot k ^ (m / 4): the 16 rows 4 c + i of a fragment in different banks
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-      const int m = (i * 64 + lane) / kChunks;
-      blds[m * kChunks + ((lane % kChunks) ^ ((m >> 2) & (kChunks - 1)))] = braw[i];
-    }
-    wave_lds_fence();
     bf16x8_t bf[4][kFrags];
+    if constexpr (!None) {
+      // row m of b, chunk k at slot k ^ (m / 4): the 16 rows 4 c + i of a fragment in different banks
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < kChunks; ++i) {
+        const int m = (i * 64 + lane) / kChunks;
+        blds[m * kChunks + ((lane % kChunks) ^ ((m >> 2) & (kChunks - 1)))] = braw[i];
+      }
+      wave_lds_fence();
 #pragma unroll
-      for (int k = 0; k < kFrags; ++k)
-        bf[i][k] = as_bf16x8(blds[(4 * c + i) * kChunks + (((k * 4 + g) % kChunks) ^ (c & (kChunks - 1)))]);
-    wave_lds_fence();
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int k = 0; k < kFrags; ++k)
+          bf[i][k] = as_bf16x8(blds[(4 * c + i) * kChunks + (((k * 4 + g) % kChunks) ^ (c & (kChunks - 1)))]);
+      wave_lds_fence();
+    }
     const int next = n0 + kWaves * kUpCols;
-    if (next < n_end) load_b(next);
+    if constexpr (decltype(more)::value) load_b(next);
 #pragma unroll
     for (int ts = 0; ts < NSUB; ++ts) {
       f32x4_t acc[4];
-      const uint4 in[4] = {base[ts][0], base[ts][1], base[ts][2], base[ts][3]};
-      if (next < n_end) load_base(ts, next + 4 * c);
+      uint4 in[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        in[q] = make_uint4(base[ts][q].x & keep, base[ts][q].y & keep, base[ts][q].z & keep, base[ts][q].w & keep);
+      if constexpr (decltype(more)::value) load_base(ts, next + 4 * c);
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int k = 0; k < kSteps; ++k) {
+      for (int k = 0; k < (None ? 0 : kSteps); ++k) {
         const int chunk = k * 4 + g;
         const int q = chunk / kChunks;
         bf16x8_t hf = as_bf16x8(
@@ -693,83 +791,45 @@ __device__ __forceinline__ void up_tile(const UpArgs& p, const Tile& sh, int n, 
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int t = ts * kSub + 4 * g + q;
-        uint4 d = make_uint4(0, 0, 0, 0);
-        if constexpr (sizeof(TO) == 4) {
+        uint4 d = in[q];
+        if constexpr (None) {
+        } else if constexpr (sizeof(TO) == 4) {
           d = make_uint4(__float_as_uint(__uint_as_float(in[q].x) + acc[0][q]),
                          __float_as_uint(__uint_as_float(in[q].y) + acc[1][q]),
                          __float_as_uint(__uint_as_float(in[q].z) + acc[2][q]),
                          __float_as_uint(__uint_as_float(in[q].w) + acc[3][q]));
         } else {
-          d.x = bf16_bits(__uint_as_float(in[q].x << 16) + acc[0][q]) |
-                bf16_bits(__uint_as_float(in[q].x & 0xffff0000u) + acc[1][q]) << 16;
-          d.y = bf16_bits(__uint_as_float(in[q].y << 16) + acc[2][q]) |
-                bf16_bits(__uint_as_float(in[q].y & 0xffff0000u) + acc[3][q]) << 16;
+          d.x = bf16_pair(__uint_as_float(in[q].x << 16) + acc[0][q], __uint_as_float(in[q].x & 0xffff0000u) + acc[1][q]);
+          d.y = bf16_pair(__uint_as_float(in[q].y << 16) + acc[2][q], __uint_as_float(in[q].y & 0xffff0000u) + acc[3][q]);
         }
-        if (t < n) store4<TO, Vec>((TO*)p.out + (int64_t)sh.rows[t] * p.ld_out, col, p.N, d);
+        if (t < n) store4<TO, Vec>((TO*)p.out + offs[1][t], col, p.N, d);
       }
     }
     n0 = next;
-  }
+  };
+  while (n0 + kWaves * kUpCols < n_end) columns(std::true_type{});
+  if (n0 < n_end) columns(std::false_type{});
 }
 
 template <typename TO, int RC, bool Vec>
-__global__ __launch_bounds__(kThreads) void lora_up_kernel(UpArgs p) {
+__global__ __launch_bounds__(kThreads, RC <= 64 ? 3 : 1) void lora_up_kernel(UpArgs p) {
   constexpr int NP = sizeof(TO) == 4 ? 3 : 2;
   __shared__ __align__(16) Tile sh;
   __shared__ __align__(16) uint16_t lds[NP * kLoraTile * (RC + 8)];
   __shared__ uint4 blds[kWaves][kUpCols * RC / 8];
-  const int n = find_tile(p.tile, sh, blockIdx.x);
+  const int n = find_tile(p.tile, sh, blockIdx.y);
   if (n == 0) return;
-  if (sh.adapter == p.tile.L) {
-    copy_rows<TO, Vec>(p, sh, n);
-    return;
-  }
+  const bool none = sh.adapter == p.tile.L;
+  if (none && p.base == p.out) return;  // in place
+  __shared__ __align__(16) int64_t offs[2][kLoraTile];
   uint4* mine = blds[threadIdx.x >> 6];
-  if (n <= 16) up_tile<TO, RC, Vec, 1>(p, sh, n, lds, mine);
-  else if (n <= 32) up_tile<TO, RC, Vec, 2>(p, sh, n, lds, mine);
-  else up_tile<TO, RC, Vec, 4>(p, sh, n, lds, mine);
+  if (none) up_tile<TO, RC, Vec, 4, true>(p, sh, n, lds, mine, offs);
+  else if (n <= 16) up_tile<TO, RC, Vec, 1>(p, sh, n, lds, mine, offs);
+  else if (n <= 32) up_tile<TO, RC, Vec, 2>(p, sh, n, lds, mine, offs);
+  else up_tile<TO, RC, Vec, 4>(p, sh, n, lds, mine, offs);
 }
 
-// ------------------------------------------------------------------ prep
-struct PrepArgs {
-  TileArgs tile;
-  const uint16_t* a;          // [L][r][K]
-  const uint16_t* b;          // [L][N][r]
-  int K, N, r;
-  int64_t n_pad;
-  uint16_t* at;               // [L][K][r], or null
-  uint16_t* bt;               // [L][r][n_pad], zeros from N
-  int a_blocks, b_blocks;     // workgroups per adapter
-  const float* h;             // [M][r]
-  const float* scales;
-  int64_t cap;
-  uint16_t* ht;
-};
-
-// One 64 x 64 block of in [R][C] (C a multiple of 8) to out [C][pitch], rows
-// from R on as zeros up to the pitch.
-__device__ __forceinline__ void transpose_block(const uint16_t* __restrict__ in, int R, int C, int64_t pitch,
-                                                uint16_t* __restrict__ out, int r0, int c0, uint16_t* lds) {
-  constexpr int kPitch = 64 + 8;
-  const int tid = threadIdx.x;
-  for (int i = tid; i < 64 * 8; i += kThreads) {
-    const int row = i >> 3, col = (i & 7) * 8;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (r0 + row < R && c0 + col < C) v = *(const uint4*)(in + (int64_t)(r0 + row) * C + c0 + col);
-    *(uint4*)(lds + row * kPitch + col) = v;
-  }
-  __syncthreads();
-  for (int i = tid; i < 64 * 8; i += kThreads) {
-    const int col = i >> 3, row = (i & 7) * 8;
-    if (c0 + col >= C || r0 + row >= pitch) continue;
-    uint32_t d[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      d[e] = lds[(row + 2 * e) * kPitch + col] | (uint32_t)lds[(row + 2 * e + 1) * kPitch + col] << 16;
-    *(uint4*)(out + (int64_t)(c0 + col) * pitch + r0 + row) = make_uint4(d[0], d[1], d[2], d[3]);
-  }
-}
-
+// ------------------------------------------------------------------ join
 // The three bf16 parts of scale * (sum of the splits of part) as outer's
 // fragments: [32 positions of the grouping][part][16 ranks][lane], lane (g, c)
 // holding positions 8 g .. + 7 of rank c; zeros at the tile's padding. dh, if
@@ -812,66 +872,48 @@ __device__ __forceinline__ void rank_major(const TileArgs& tile, const Tile& sh,
   }
 }
 
-// blockIdx.y: an adapter, whose weights are transposed if it has rows in the
-// batch; past the adapters: tiles, whose h is laid out rank-major.
-__global__ __launch_bounds__(kThreads) void lora_prep_kernel(PrepArgs p) {
-  __shared__ __align__(16) Tile sh;
-  __shared__ __align__(16) float lds[kLoraTile * (kLoraMaxRank + 4)];
-  const int tid = threadIdx.x;
-  if ((int)blockIdx.y < p.tile.L) {
-    const int l = blockIdx.y;
-    if (p.tile.offsets[l] == p.tile.offsets[l + 1]) return;
-    int i = blockIdx.x;
-    if (i < p.a_blocks) {
-      const int across = (p.K + 63) / 64;
-      const int64_t at = (int64_t)l * p.r * p.K;
-      transpose_block(p.a + at, p.r, p.K, p.r, p.at + at, i / across * 64, i % across * 64, (uint16_t*)lds);
-    } else if ((i -= p.a_blocks) < p.b_blocks) {
-      const int down = (int)((p.n_pad + 63) / 64);
-      transpose_block(p.b + (int64_t)l * p.N * p.r, p.N, p.r, p.n_pad, p.bt + l * p.r * p.n_pad, i % down * 64,
-                      i / down * 64, (uint16_t*)lds);
-    }
-    return;
-  }
-  const int tile = (blockIdx.y - p.tile.L) * gridDim.x + blockIdx.x;
-  if (tile >= p.cap / kLoraTile) return;
-  const int n = find_tile(p.tile, sh, tile);
-  if (n == 0 || sh.adapter == p.tile.L) return;
-  rank_major(p.tile, sh, n, tile, p.r, p.h, 1, p.scales, nullptr, p.ht, lds);
-}
-
-// dh: the sum of its splits, scaled, as it is and rank-major.
+// dh: the sum of its splits, scaled, as it is and rank-major (blockIdx.y = 0);
+// s h rank-major (1).
 struct JoinArgs {
   TileArgs tile;
   int r, splits;
   const float* part;          // [splits][M][r]
   const float* scales;
   float* dh;                  // [M][r]
-  uint16_t* vt;
+  uint16_t* dht;
+  const float* h;             // [M][r]
+  uint16_t* ht;
 };
 __global__ __launch_bounds__(kThreads) void lora_join_kernel(JoinArgs p) {
   __shared__ __align__(16) Tile sh;
   __shared__ __align__(16) float lds[kLoraTile * (kLoraMaxRank + 4)];
   const int n = find_tile(p.tile, sh, blockIdx.x);
   if (n == 0 || sh.adapter == p.tile.L) return;
-  rank_major(p.tile, sh, n, blockIdx.x, p.r, p.part, p.splits, p.scales, p.dh, p.vt, lds);
+  if (blockIdx.y == 0) rank_major(p.tile, sh, n, blockIdx.x, p.r, p.part, p.splits, p.scales, p.dh, p.dht, lds);
+  else rank_major(p.tile, sh, n, blockIdx.x, p.r, p.h, 1, p.scales, nullptr, p.ht, lds);
 }
 
 // ------------------------------------------------------------------ outer
-struct OuterArgs {
+struct OuterSide {
   const void* u;              // [M, W]
   int64_t ldu;
-  int W, r, M, L;
+  int W;
   const uint16_t* vt;         // fragments, as rank_major writes them
-  int64_t cap;
-  const int32_t* sorted;
-  const int32_t* block_adapter;
-  const int32_t* offsets;     // [L + 2]
   float* out;                 // [L][r][W], or [L][W][r] (rank_minor)
   float* slots;               // [2 * chunks] of the same shape
   int chunk;                  // positions per workgroup, a multiple of 64
-  bool rank_minor;
+  int chunks;
 };
+struct OuterArgs {
+  int r, M, L;
+  int64_t cap;
+  const int32_t* sorted;
+  const int4* tiles;
+  OuterSide a, b;             // dA (x, bf16), dB (the output side, either type)
+  int a_blocks;               // workgroups of dA, before those of dB
+};
+
+constexpr int kPiece = 1024;  // positions whose rows are in LDS at a time
 
 // sum over an adapter's rows of u[row][w] * v[row][j], for 128 columns and up
 // to 64 ranks a workgroup. A step takes 32 positions: lane (g, c) loads 8
@@ -881,25 +923,24 @@ struct OuterArgs {
 // the adapters' lengths, so the work is even; sums of an adapter within one
 // chunk go to the output, those of one that crosses the chunk's start or end to
 // slots 2 c or 2 c + 1, which the reduce kernel adds in order.
-template <typename TU, int JT, bool VecU>
-__global__ __launch_bounds__(kThreads) void lora_outer_kernel(OuterArgs p) {
+template <typename TU, int JT, bool VecU, bool RankMinor>
+__device__ __forceinline__ void outer_block(const OuterArgs& p, const OuterSide& side, int block,
+                                            f32x4_t (*joined)[8 * JT < 16 ? 8 * JT : 16][64], int64_t* offs) {
   constexpr bool kF32 = std::is_same<TU, float>::value;
   // the next two steps' loads are in flight during this one's products where
   // the registers hold them (fp32 columns take four times a bf16 step's)
   constexpr bool kAhead = !kF32 && VecU;
   constexpr int kVecs = 8 * JT;                         // accumulators of a wave
   constexpr int kRound = kVecs < 16 ? kVecs : 16;       // of them in LDS at a time
-  constexpr int kPiece = 1024;                          // positions whose rows are in LDS at a time
-  __shared__ f32x4_t joined[kWaves][kRound][64];
-  __shared__ __align__(16) int rows_lds[kPiece];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
-  const int w0 = blockIdx.x * 128;
-  const int j0 = blockIdx.z * 64;
+  // the column blocks of a chunk are neighbours: together they read whole rows
+  const int across = (side.W + 127) / 128;
+  const int w0 = block % across * 128;
+  const int chunk = block / across % side.chunks;
+  const int j0 = block / across / side.chunks * 64;
   const int ranks = (p.r + 15) / 16;
-  const int npp = p.offsets[p.L];
-  const int p0 = blockIdx.y * p.chunk;
-  if (p0 >= npp) return;
-  const int p1 = p0 + p.chunk < npp ? p0 + p.chunk : npp;
+  const int p0 = chunk * side.chunk;
+  const int p1 = p0 + side.chunk < p.cap ? p0 + side.chunk : (int)p.cap;
   f32x4_t acc[8][JT];
 
   struct Frags {
@@ -908,20 +949,14 @@ __global__ __launch_bounds__(kThreads) void lora_outer_kernel(OuterArgs p) {
     bf16x8_t v[JT][3];
   };
   auto load = [&](int pos, int piece, Frags& x) {
-    const int4 ra = *(const int4*)(rows_lds + pos - piece + 8 * g);
-    const int4 rb = *(const int4*)(rows_lds + pos - piece + 8 * g + 4);
-    const int rows[8] = {ra.x, ra.y, ra.z, ra.w, rb.x, rb.y, rb.z, rb.w};
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
-      const bool live = rows[t] < p.M;
-      const TU* row = (const TU*)p.u + (int64_t)(live ? rows[t] : 0) * p.ldu;
+      const TU* row = (const TU*)side.u + offs[pos - piece + 8 * g + t];
       if constexpr (kF32) {
-        load8<VecU>((const float*)row, w0 + 8 * c, p.W, x.f[t]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x.f[t][i] = live ? x.f[t][i] : 0.0f;
+        load8<VecU>((const float*)row, w0 + 8 * c, side.W, x.f[t]);
       } else {
-        const uint4 v = __builtin_bit_cast(uint4, load8<VecU>((const uint16_t*)row, w0 + 8 * c, p.W));
-        x.d[t][0] = live ? v.x : 0; x.d[t][1] = live ? v.y : 0; x.d[t][2] = live ? v.z : 0; x.d[t][3] = live ? v.w : 0;
+        const uint4 v = load16<uint16_t, VecU>((const uint16_t*)row, w0 + 8 * c, side.W);
+        x.d[t][0] = v.x; x.d[t][1] = v.y; x.d[t][2] = v.z; x.d[t][3] = v.w;
       }
     }
 #pragma unroll
@@ -929,7 +964,7 @@ __global__ __launch_bounds__(kThreads) void lora_outer_kernel(OuterArgs p) {
       const int at = j0 / 16 + jt < ranks ? j0 / 16 + jt : ranks - 1;
 #pragma unroll
       for (int q = 0; q < 3; ++q)
-        x.v[jt][q] = as_bf16x8(*(const uint4*)(p.vt + (((int64_t)(pos / 32) * 3 + q) * ranks + at) * 512 + lane * 8));
+        x.v[jt][q] = as_bf16x8(*(const uint4*)(side.vt + (((int64_t)(pos / 32) * 3 + q) * ranks + at) * 512 + lane * 8));
     }
   };
   auto multiply = [&](const Frags& x) {
@@ -964,8 +999,11 @@ __global__ __launch_bounds__(kThreads) void lora_outer_kernel(OuterArgs p) {
   };
 
   for (int s0 = p0; s0 < p1;) {
-    const int adapter = p.block_adapter[s0 / kLoraTile];
-    const int o0 = p.offsets[adapter], o1 = p.offsets[adapter + 1];
+    // an adapter's positions in the chunk; the last list (rows without an
+    // adapter) and the room behind it have nothing
+    const int4 info = p.tiles[s0 / kLoraTile];
+    if (info.y == 0 || info.x == p.L) return;
+    const int adapter = info.x, o0 = info.z, o1 = info.w;
     const int s1 = o1 < p1 ? o1 : p1;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -974,26 +1012,47 @@ __global__ __launch_bounds__(kThreads) void lora_outer_kernel(OuterArgs p) {
     for (int piece = s0; piece < s1; piece += kPiece) {
       const int end = piece + kPiece < s1 ? piece + kPiece : s1;
       __syncthreads();
-      for (int i = threadIdx.x * 4; i < end - piece; i += kThreads * 4)
-        *(int4*)(rows_lds + i) = *(const int4*)(p.sorted + piece + i);
+      // padding repeats its tile's first row, whose factors there are 0: what
+      // is not finite in that row is in this adapter's sums anyway
+      for (int i = threadIdx.x; i < end - piece; i += kThreads) {
+        const int row = p.sorted[piece + i], first = p.sorted[(piece + i) / kLoraTile * kLoraTile];
+        offs[i] = (row < p.M ? row : first) * side.ldu;
+      }
       __syncthreads();
       int pos = piece + 32 * wave;
       if (pos < end) {
         constexpr int kStep = 32 * kWaves;
         if constexpr (kAhead) {
+          // triples of steps, each step's loads in flight during the two before
+          // it; no load hangs on a condition, so each wait is for its own step
           Frags f0, f1, f2;
-          load(pos, piece, f0);
-          if (pos + kStep < end) load(pos + kStep, piece, f1);
-          while (true) {
-            if (pos + 2 * kStep < end) load(pos + 2 * kStep, piece, f2);
+          const int triples = (end - pos + kStep - 1) / kStep / 3;
+          if (triples > 0) {
+            load(pos, piece, f0);
+            load(pos + kStep, piece, f1);
+            load(pos + 2 * kStep, piece, f2);
+            for (int i = 1; i < triples; ++i) {
+              pos += 3 * kStep;
+              multiply(f0);
+              load(pos, piece, f0);
+              multiply(f1);
+              load(pos + kStep, piece, f1);
+              multiply(f2);
+              load(pos + 2 * kStep, piece, f2);
+            }
             multiply(f0);
-            if ((pos += kStep) >= end) break;
-            if (pos + 2 * kStep < end) load(pos + 2 * kStep, piece, f0);
             multiply(f1);
-            if ((pos += kStep) >= end) break;
-            if (pos + 2 * kStep < end) load(pos + 2 * kStep, piece, f1);
             multiply(f2);
-            if ((pos += kStep) >= end) break;
+            pos += 3 * kStep;
+          }
+          if (pos + kStep < end) {
+            load(pos, piece, f0);
+            load(pos + kStep, piece, f1);
+            multiply(f0);
+            multiply(f1);
+          } else if (pos < end) {
+            load(pos, piece, f0);
+            multiply(f0);
           }
         } else {
           for (; pos < end; pos += kStep) {
@@ -1006,9 +1065,9 @@ __global__ __launch_bounds__(kThreads) void lora_outer_kernel(OuterArgs p) {
     }
     // join: lane (g, c) has columns 8 c + i, ranks 16 jt + 4 g + q. Four
     // accumulators (half of i, one jt) go to one wave.
-    const int64_t size = (int64_t)p.r * p.W;
-    float* out = (o0 >= p0 && o1 <= p0 + p.chunk) ? p.out + adapter * size
-                                                  : p.slots + (2 * (int64_t)blockIdx.y + (o0 < p0 ? 0 : 1)) * size;
+    const int64_t size = (int64_t)p.r * side.W;
+    float* out = (o0 >= p0 && o1 <= p0 + side.chunk) ? side.out + adapter * size
+                                                     : side.slots + (2 * (int64_t)chunk + (o0 < p0 ? 0 : 1)) * size;
 #pragma unroll
     for (int r0 = 0; r0 < kVecs; r0 += kRound) {
 #pragma unroll
@@ -1024,15 +1083,15 @@ __global__ __launch_bounds__(kThreads) void lora_outer_kernel(OuterArgs p) {
         }
         const int w = w0 + 8 * c + v % 8, j = j0 + 16 * ((r0 + v) / 8) + 4 * g;
         if (j < p.r) {
-          if (p.rank_minor) {
+          if constexpr (RankMinor) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              if (w + i < p.W) *(f32x4_t*)(out + (int64_t)(w + i) * p.r + j) = sum[i];
+              if (w + i < side.W) *(f32x4_t*)(out + (int64_t)(w + i) * p.r + j) = sum[i];
           } else {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              float* at = out + (int64_t)(j + q) * p.W + w;
-              if (w < p.W) *(f32x4_t*)at = f32x4_t{sum[0][q], sum[1][q], sum[2][q], sum[3][q]};
+              float* at = out + (int64_t)(j + q) * side.W + w;
+              if (w < side.W) *(f32x4_t*)at = f32x4_t{sum[0][q], sum[1][q], sum[2][q], sum[3][q]};
             }
           }
         }
@@ -1041,6 +1100,14 @@ __global__ __launch_bounds__(kThreads) void lora_outer_kernel(OuterArgs p) {
     }
     s0 = s1;
   }
+}
+
+template <typename TU, int JT, bool VecU>
+__global__ __launch_bounds__(kThreads) void lora_outer_kernel(OuterArgs p) {
+  __shared__ f32x4_t joined[kWaves][8 * JT < 16 ? 8 * JT : 16][64];
+  __shared__ __align__(16) int64_t offs[kPiece];
+  if ((int)blockIdx.x < p.a_blocks) outer_block<uint16_t, JT, true, false>(p, p.a, blockIdx.x, joined, offs);
+  else outer_block<TU, JT, VecU, true>(p, p.b, blockIdx.x - p.a_blocks, joined, offs);
 }
 
 // Adapters that cross chunks: their slots, in order; adapters without rows:
@@ -1104,12 +1171,15 @@ hipError_t launch_down(DownArgs p, bool u_f32, int tiles, hipStream_t stream) {
 hipError_t launch_up(UpArgs p, bool out_f32, int tiles, hipStream_t stream) {
   const bool vec = vec_ok(p.base, p.ld_base, out_f32) && vec_ok(p.out, p.ld_out, out_f32) &&
                    p.N % (out_f32 ? 4 : 8) == 0;
-  // four workgroups a CU, each going on to further columns with its next loads in flight
-  int64_t groups = tiles * ceil_div(p.N, kWaves * kUpCols) / 1024;
-  if (groups < 1) groups = 1;
-  if (groups > 8) groups = 8;
-  p.n_block = (int)groups * kWaves * kUpCols;
-  const dim3 grid((unsigned)tiles, (unsigned)ceil_div(p.N, p.n_block));
+  // as many workgroups as the chip holds at once (by their registers and LDS),
+  // each going on to further columns with its next loads in flight; the column
+  // blocks of a tile are neighbours, so that together they read whole rows
+  // (rank 16, [1999, 7168]: 24 us with the tiles as neighbours, 15 so)
+  const int64_t cols = ceil_div(p.N, kWaves * kUpCols);
+  int64_t across = 256 * (p.r <= 64 ? 3 : 1) / tiles;
+  across = across < 1 ? 1 : (across > cols ? cols : across);
+  p.n_block = (int)(ceil_div(cols, across) * kWaves * kUpCols);
+  const dim3 grid((unsigned)ceil_div(p.N, p.n_block), (unsigned)tiles);
   auto go = [&](auto rc) {
     constexpr int RC = decltype(rc)::value;
     if (out_f32) {
@@ -1128,15 +1198,20 @@ hipError_t launch_up(UpArgs p, bool out_f32, int tiles, hipStream_t stream) {
   return hipGetLastError();
 }
 
-hipError_t launch_outer(const OuterArgs& p, bool u_f32, hipStream_t stream) {
-  const bool vec = vec_ok(p.u, p.ldu, u_f32) && p.W % (u_f32 ? 4 : 8) == 0;
-  const dim3 grid((unsigned)ceil_div(p.W, 128), (unsigned)ceil_div(p.cap, p.chunk), (unsigned)ceil_div(p.r, 64));
+hipError_t launch_outer(OuterArgs p, bool b_f32, hipStream_t stream) {
+  const bool vec = vec_ok(p.b.u, p.b.ldu, b_f32) && p.b.W % (b_f32 ? 4 : 8) == 0;
+  const int64_t ranks = ceil_div(p.r, 64);
+  p.a.chunks = (int)ceil_div(p.cap, p.a.chunk);
+  p.b.chunks = (int)ceil_div(p.cap, p.b.chunk);
+  const int64_t a_blocks = ceil_div(p.a.W, 128) * p.a.chunks * ranks;
+  const int64_t blocks = a_blocks + ceil_div(p.b.W, 128) * p.b.chunks * ranks;
+  p.a_blocks = (int)a_blocks;
   auto go = [&](auto jt) {
     constexpr int JT = decltype(jt)::value;
-    if (u_f32 && vec) lora_outer_kernel<float, JT, true><<<grid, kThreads, 0, stream>>>(p);
-    else if (u_f32) lora_outer_kernel<float, JT, false><<<grid, kThreads, 0, stream>>>(p);
-    else if (vec) lora_outer_kernel<uint16_t, JT, true><<<grid, kThreads, 0, stream>>>(p);
-    else lora_outer_kernel<uint16_t, JT, false><<<grid, kThreads, 0, stream>>>(p);
+    if (b_f32 && vec) lora_outer_kernel<float, JT, true><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
+    else if (b_f32) lora_outer_kernel<float, JT, false><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
+    else if (vec) lora_outer_kernel<uint16_t, JT, true><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
+    else lora_outer_kernel<uint16_t, JT, false><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
   };
   if (p.r <= 16) go(std::integral_constant<int, 1>{});
   else if (p.r <= 32) go(std::integral_constant<int, 2>{});
@@ -1158,7 +1233,10 @@ LoraLayout lora_layout(int64_t M, int64_t L, int64_t K, int64_t N, int64_t r, bo
   // splits of the contraction: enough workgroups for the chip, each wave at
   // least one step, and no more than 8 partial sums to add
   const int64_t steps = ceil_div(backward ? N : K, 64);
-  int64_t splits = M > 0 ? ceil_div(512, ceil_div(M, kLoraTile)) : 1;
+  // (the tiles of a batch are M / 64 and part of one for each adapter with rows)
+  const int64_t full = ceil_div(M, kLoraTile);
+  int64_t splits = M > 0 ? 512 / (full + (L - 1 < full ? L - 1 : full) / 4) : 1;
+  if (splits < 1) splits = 1;
   if (splits > 8) splits = 8;
   if (splits > ceil_div(steps, kWaves)) splits = ceil_div(steps, kWaves);
   o.splits = (int)ceil_div(steps, ceil_div(steps, splits));
@@ -1171,7 +1249,7 @@ LoraLayout lora_layout(int64_t M, int64_t L, int64_t K, int64_t N, int64_t r, bo
   o.part_off = take(o.splits * M * r * 4);
   if (!o.small) {
     o.sorted_off = take(o.cap * 4);
-    o.block_off = take(o.cap / kLoraTile * 4);
+    o.block_off = take(o.cap / kLoraTile * 16);
     o.offs_off = take((L + 2) * 4);
     if (!backward) o.h_off = take(M * r * 4);
   }
@@ -1204,17 +1282,21 @@ LoraLayout lora_layout(int64_t M, int64_t L, int64_t K, int64_t N, int64_t r, bo
 namespace {
 
 // The grouping (none for a small batch) and the arguments that name it.
-hipError_t group_rows(const LoraArgs& a, const LoraLayout& o, TileArgs& t, hipStream_t stream) {
+hipError_t group_rows(const LoraArgs& a, const LoraLayout& o, const TransposeArgs& weights, TileArgs& t,
+                      hipStream_t stream) {
   t = TileArgs{};
   t.ids = a.ids; t.M = a.M; t.L = a.L;
   if (o.small) return hipSuccess;
   GroupArgs g{};
   g.ids = a.ids; g.M = a.M; g.L = a.L;
   g.sorted = (int32_t*)(a.ws + o.sorted_off);
-  g.block_adapter = (int32_t*)(a.ws + o.block_off);
+  g.tiles = (int4*)(a.ws + o.block_off);
   g.offsets = (int32_t*)(a.ws + o.offs_off);
-  t.sorted = g.sorted; t.block_adapter = g.block_adapter; t.offsets = g.offsets;
-  lora_group_kernel<<<1, kGroupThreads, 0, stream>>>(g);
+  g.all_tiles = o.tiles;
+  t.sorted = g.sorted; t.tiles = g.tiles;
+  int64_t more = a.M > 0 ? (a.M < a.L ? a.M : a.L) * (int64_t)(weights.a_blocks + weights.b_blocks) : 0;
+  if (more > 511) more = 511;  // with the grouping, two workgroups a CU
+  lora_group_kernel<<<(unsigned)(1 + more), kGroupThreads, 0, stream>>>(g, weights);
   return hipGetLastError();
 }
 
@@ -1223,7 +1305,7 @@ hipError_t group_rows(const LoraArgs& a, const LoraLayout& o, TileArgs& t, hipSt
 hipError_t launch_lora_forward(const LoraArgs& a, hipStream_t stream) {
   const LoraLayout o = lora_layout(a.M, a.L, a.K, a.N, a.r, false);
   TileArgs t;
-  hipError_t err = group_rows(a, o, t, stream);
+  hipError_t err = group_rows(a, o, TransposeArgs{}, t, stream);
   if (err != hipSuccess) return err;
   DownArgs d{};
   d.tile = t;
@@ -1250,26 +1332,22 @@ hipError_t launch_lora_forward(const LoraArgs& a, hipStream_t stream) {
 
 hipError_t launch_lora_backward(const LoraArgs& a, hipStream_t stream) {
   const LoraLayout o = lora_layout(a.M, a.L, a.K, a.N, a.r, true);
+  TransposeArgs f{};
+  f.a = a.a; f.b = a.b; f.K = a.K; f.N = a.N; f.r = a.r; f.n_pad = o.n_pad;
+  f.at = (uint16_t*)(a.ws + o.at_off); f.bt = (uint16_t*)(a.ws + o.bt_off);
+  const int64_t ranks = ceil_div(a.r, 64);
+  f.a_blocks = a.dx ? (int)(ranks * ceil_div(a.K, 64)) : 0;
+  f.b_blocks = (int)(ranks * ceil_div(o.n_pad, 64));
   TileArgs t;
-  hipError_t err = group_rows(a, o, t, stream);
+  hipError_t err = group_rows(a, o, f, t, stream);
   if (err != hipSuccess) return err;
   ReduceArgs red{};
-  red.offsets = t.offsets;
+  red.offsets = (const int32_t*)(a.ws + o.offs_off);
   red.size[0] = (int64_t)a.r * a.K; red.size[1] = (int64_t)a.r * a.N;
   red.chunk[0] = o.a_chunk; red.chunk[1] = o.b_chunk;
   red.slots[0] = (float*)(a.ws + o.a_slots_off); red.slots[1] = (float*)(a.ws + o.b_slots_off);
   red.out[0] = a.da; red.out[1] = a.db;
   if (a.M > 0) {
-    PrepArgs f{};
-    f.tile = t; f.a = a.a; f.b = a.b; f.K = a.K; f.N = a.N; f.r = a.r; f.n_pad = o.n_pad;
-    f.at = (uint16_t*)(a.ws + o.at_off); f.bt = (uint16_t*)(a.ws + o.bt_off);
-    const int64_t ranks = ceil_div(a.r, 64);
-    f.a_blocks = a.dx ? (int)(ranks * ceil_div(a.K, 64)) : 0;
-    f.b_blocks = (int)(ranks * ceil_div(o.n_pad, 64));
-    f.h = a.h; f.scales = a.scales; f.cap = o.cap; f.ht = (uint16_t*)(a.ws + o.ht_off);
-    const int64_t across = f.a_blocks + f.b_blocks;
-    lora_prep_kernel<<<dim3((unsigned)across, (unsigned)(a.L + ceil_div(o.tiles, across))), kThreads, 0, stream>>>(f);
-    if ((err = hipGetLastError()) != hipSuccess) return err;
     DownArgs d{};
     d.tile = t;
     d.u = a.dout; d.ldu = a.ld_dout; d.W = a.N;
@@ -1279,8 +1357,9 @@ hipError_t launch_lora_backward(const LoraArgs& a, hipStream_t stream) {
     if ((err = launch_down(d, a.y_f32, o.tiles, stream)) != hipSuccess) return err;
     JoinArgs j{};
     j.tile = t; j.r = a.r; j.splits = o.splits; j.part = d.part; j.scales = a.scales;
-    j.dh = (float*)(a.ws + o.dh_off); j.vt = (uint16_t*)(a.ws + o.dht_off);
-    lora_join_kernel<<<o.tiles, kThreads, 0, stream>>>(j);
+    j.dh = (float*)(a.ws + o.dh_off); j.dht = (uint16_t*)(a.ws + o.dht_off);
+    j.h = a.h; j.ht = (uint16_t*)(a.ws + o.ht_off);
+    lora_join_kernel<<<dim3(o.tiles, 2), kThreads, 0, stream>>>(j);
     if ((err = hipGetLastError()) != hipSuccess) return err;
     if (a.dx) {
       UpArgs u{};
@@ -1289,13 +1368,11 @@ hipError_t launch_lora_backward(const LoraArgs& a, hipStream_t stream) {
       if ((err = launch_up(u, false, o.tiles, stream)) != hipSuccess) return err;
     }
     OuterArgs w{};
-    w.r = a.r; w.M = a.M; w.L = a.L; w.cap = o.cap;
-    w.sorted = t.sorted; w.block_adapter = t.block_adapter; w.offsets = t.offsets;
-    w.u = a.x; w.ldu = a.ldx; w.W = a.K; w.vt = j.vt; w.out = a.da;
-    w.slots = (float*)(a.ws + o.a_slots_off); w.chunk = o.a_chunk;
-    if ((err = launch_outer(w, false, stream)) != hipSuccess) return err;
-    w.u = a.dout; w.ldu = a.ld_dout; w.W = a.N; w.vt = f.ht; w.out = a.db; w.rank_minor = true;
-    w.slots = (float*)(a.ws + o.b_slots_off); w.chunk = o.b_chunk;
+    w.r = a.r; w.M = a.M; w.L = a.L; w.cap = o.cap; w.sorted = t.sorted; w.tiles = t.tiles;
+    w.a.u = a.x; w.a.ldu = a.ldx; w.a.W = a.K; w.a.vt = j.dht; w.a.out = a.da;
+    w.a.slots = (float*)(a.ws + o.a_slots_off); w.a.chunk = o.a_chunk;
+    w.b.u = a.dout; w.b.ldu = a.ld_dout; w.b.W = a.N; w.b.vt = j.ht; w.b.out = a.db;
+    w.b.slots = (float*)(a.ws + o.b_slots_off); w.b.chunk = o.b_chunk;
     if ((err = launch_outer(w, a.y_f32, stream)) != hipSuccess) return err;
   }
   const int64_t widest = red.size[0] > red.size[1] ? red.size[0] : red.size[1];
