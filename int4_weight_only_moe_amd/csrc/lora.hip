@@ -56,45 +56,6 @@ __device__ __forceinline__ void split_parts(const float (&v)[8], bf16x8_t (&part
   }
 }
 
-// Eight consecutive elements from column w of a row of W elements, zeros past
-// the row's end. Vec: the row is 16-byte aligned and W % 8 == 0 (bf16) or
-// W % 4 == 0 (fp32).
-template <bool Vec>
-__device__ __forceinline__ bf16x8_t load8(const uint16_t* __restrict__ row, int w, int W) {
-  if constexpr (Vec) {
-    uint4 v = *(const uint4*)(row + (w < W ? w : 0));
-    if (w >= W) v = make_uint4(0, 0, 0, 0);
-    return as_bf16x8(v);
-  } else {
-    uint32_t e[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t x = row[w + i < W ? w + i : 0];
-      e[i] = w + i < W ? x : 0u;
-    }
-    return as_bf16x8(make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16));
-  }
-}
-template <bool Vec>
-__device__ __forceinline__ void load8(const float* __restrict__ row, int w, int W, float (&v)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; i += 4) {
-    if constexpr (Vec) {
-      const float4 x = *(const float4*)(row + (w + i < W ? w + i : 0));
-      v[i] = w + i < W ? x.x : 0.0f;
-      v[i + 1] = w + i < W ? x.y : 0.0f;
-      v[i + 2] = w + i < W ? x.z : 0.0f;
-      v[i + 3] = w + i < W ? x.w : 0.0f;
-    } else {
-#pragma unroll
-      for (int q = i; q < i + 4; ++q) {
-        const float x = row[w + q < W ? w + q : 0];
-        v[q] = w + q < W ? x : 0.0f;
-      }
-    }
-  }
-}
-
 // Two fp32 values rounded to bf16, the first in the low half.
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
@@ -407,21 +368,37 @@ __device__ __forceinline__ int find_tile(const TileArgs& p, Tile& sh, int tile) 
   return n;
 }
 
-// 16 bytes of a row of W elements from element w, zeros past its end. Vec: the
-// row is 16-byte aligned and W a multiple of 16 bytes' elements.
-template <typename T, bool Vec>
+// All ones or zeros, in a register whose value the compiler cannot trace: it
+// turns a load whose value is dropped for some lanes into a branch around the
+// load, and after one of those waits no longer for the loads that it needs but
+// for all of them.
+__device__ __forceinline__ uint32_t lane_mask(bool keep) {
+  uint32_t m = keep ? 0xffffffffu : 0u;
+  asm("" : "+v"(m));
+  return m;
+}
+
+// 16 bytes of a row of W elements from element w. Past the row's end: zeros
+// (Zero), or anything. Vec: the row is 16-byte aligned and W a multiple of 16
+// bytes' elements.
+template <typename T, bool Vec, bool Zero = true>
 __device__ __forceinline__ uint4 load16(const T* __restrict__ row, int w, int W) {
   constexpr int kN = 16 / sizeof(T);
   if constexpr (Vec) {
-    const uint4 v = *(const uint4*)(row + (w < W ? w : 0));
-    return w < W ? v : make_uint4(0, 0, 0, 0);
+    uint4 v = *(const uint4*)(row + (w < W ? w : 0));
+    if constexpr (Zero) {
+      const uint32_t m = lane_mask(w < W);
+      v.x &= m; v.y &= m; v.z &= m; v.w &= m;
+    }
+    return v;
   } else {
     uint32_t d[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       const T x = row[w + i < W ? w + i : 0];
-      if constexpr (sizeof(T) == 4) d[i] = w + i < W ? __float_as_uint(x) : 0u;
-      else d[i / 2] |= (w + i < W ? (uint32_t)x : 0u) << (16 * (i & 1));
+      const uint32_t m = Zero ? lane_mask(w + i < W) : 0xffffffffu;
+      if constexpr (sizeof(T) == 4) d[i] = __float_as_uint(x) & m;
+      else d[i / 2] |= ((uint32_t)x & m) << (16 * (i & 1));
     }
     return make_uint4(d[0], d[1], d[2], d[3]);
   }
@@ -922,22 +899,24 @@ constexpr int kPiece = 1024;  // positions whose rows are in LDS at a time
 // turn and join their sums in LDS. The positions are cut into chunks whatever
 // the adapters' lengths, so the work is even; sums of an adapter within one
 // chunk go to the output, those of one that crosses the chunk's start or end to
-// slots 2 c or 2 c + 1, which the reduce kernel adds in order.
-template <typename TU, int JT, bool VecU, bool RankMinor>
+// slots 2 c or 2 c + 1, which the reduce kernel adds in order. Ranks above 64
+// are further workgroups, eight apart: on the same XCD, whose L2 has the columns.
+template <typename TU, int JT, int H, bool VecU, bool RankMinor>
 __device__ __forceinline__ void outer_block(const OuterArgs& p, const OuterSide& side, int block,
-                                            f32x4_t (*joined)[8 * JT < 16 ? 8 * JT : 16][64], int64_t* offs) {
+                                            f32x4_t (*joined)[8 * JT][64], int64_t* offs) {
   constexpr bool kF32 = std::is_same<TU, float>::value;
-  // the next two steps' loads are in flight during this one's products where
-  // the registers hold them (fp32 columns take four times a bf16 step's)
-  constexpr bool kAhead = !kF32 && VecU;
   constexpr int kVecs = 8 * JT;                         // accumulators of a wave
-  constexpr int kRound = kVecs < 16 ? kVecs : 16;       // of them in LDS at a time
+  constexpr int kTurns = kWaves / H;                    // waves that take turns at the positions
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
   // the column blocks of a chunk are neighbours: together they read whole rows
   const int across = (side.W + 127) / 128;
-  const int w0 = block % across * 128;
-  const int chunk = block / across % side.chunks;
-  const int j0 = block / across / side.chunks * 64;
+  const int zs = (p.r + 16 * JT * H - 1) / (16 * JT * H);
+  const int at = block % 8 * ((across * side.chunks + 7) / 8) + block / 8 / zs;
+  const int w0 = at % across * 128;
+  const int chunk = at / across;
+  if (chunk >= side.chunks || block / 8 / zs >= (across * side.chunks + 7) / 8) return;
+  const int turn = wave / H;
+  const int j0 = (block / 8 % zs * H + wave % H) * 16 * JT;
   const int ranks = (p.r + 15) / 16;
   const int p0 = chunk * side.chunk;
   const int p1 = p0 + side.chunk < p.cap ? p0 + side.chunk : (int)p.cap;
@@ -953,9 +932,14 @@ __device__ __forceinline__ void outer_block(const OuterArgs& p, const OuterSide&
     for (int t = 0; t < 8; ++t) {
       const TU* row = (const TU*)side.u + offs[pos - piece + 8 * g + t];
       if constexpr (kF32) {
-        load8<VecU>((const float*)row, w0 + 8 * c, side.W, x.f[t]);
+        const uint4 lo = load16<float, VecU, false>((const float*)row, w0 + 8 * c, side.W);
+        const uint4 hi = load16<float, VecU, false>((const float*)row, w0 + 8 * c + 4, side.W);
+        x.f[t][0] = __uint_as_float(lo.x); x.f[t][1] = __uint_as_float(lo.y);
+        x.f[t][2] = __uint_as_float(lo.z); x.f[t][3] = __uint_as_float(lo.w);
+        x.f[t][4] = __uint_as_float(hi.x); x.f[t][5] = __uint_as_float(hi.y);
+        x.f[t][6] = __uint_as_float(hi.z); x.f[t][7] = __uint_as_float(hi.w);
       } else {
-        const uint4 v = load16<uint16_t, VecU>((const uint16_t*)row, w0 + 8 * c, side.W);
+        const uint4 v = load16<uint16_t, VecU, false>((const uint16_t*)row, w0 + 8 * c, side.W);
         x.d[t][0] = v.x; x.d[t][1] = v.y; x.d[t][2] = v.z; x.d[t][3] = v.w;
       }
     }
@@ -1019,41 +1003,28 @@ __device__ __forceinline__ void outer_block(const OuterArgs& p, const OuterSide&
         offs[i] = (row < p.M ? row : first) * side.ldu;
       }
       __syncthreads();
-      int pos = piece + 32 * wave;
+      int pos = piece + 32 * turn;
       if (pos < end) {
-        constexpr int kStep = 32 * kWaves;
-        if constexpr (kAhead) {
-          // triples of steps, each step's loads in flight during the two before
-          // it; no load hangs on a condition, so each wait is for its own step
-          Frags f0, f1, f2;
-          const int triples = (end - pos + kStep - 1) / kStep / 3;
-          if (triples > 0) {
-            load(pos, piece, f0);
+        constexpr int kStep = 32 * kTurns;
+        if constexpr (!kF32) {
+          // The next step's loads are in flight during this one's products. No
+          // load of the loop hangs on a condition, so each wait is for its own
+          // step, and the barriers keep the compiler from mixing the steps.
+          Frags f0, f1;
+          load(pos, piece, f0);
+          for (; pos + 2 * kStep < end; pos += 2 * kStep) {
             load(pos + kStep, piece, f1);
-            load(pos + 2 * kStep, piece, f2);
-            for (int i = 1; i < triples; ++i) {
-              pos += 3 * kStep;
-              multiply(f0);
-              load(pos, piece, f0);
-              multiply(f1);
-              load(pos + kStep, piece, f1);
-              multiply(f2);
-              load(pos + 2 * kStep, piece, f2);
-            }
+            __builtin_amdgcn_sched_barrier(0);
             multiply(f0);
+            __builtin_amdgcn_sched_barrier(0);
+            load(pos + 2 * kStep, piece, f0);
+            __builtin_amdgcn_sched_barrier(0);
             multiply(f1);
-            multiply(f2);
-            pos += 3 * kStep;
+            __builtin_amdgcn_sched_barrier(0);
           }
-          if (pos + kStep < end) {
-            load(pos, piece, f0);
-            load(pos + kStep, piece, f1);
-            multiply(f0);
-            multiply(f1);
-          } else if (pos < end) {
-            load(pos, piece, f0);
-            multiply(f0);
-          }
+          if (pos + kStep < end) load(pos + kStep, piece, f1);
+          multiply(f0);
+          if (pos + kStep < end) multiply(f1);
         } else {
           for (; pos < end; pos += kStep) {
             Frags f;
@@ -1069,45 +1040,42 @@ __device__ __forceinline__ void outer_block(const OuterArgs& p, const OuterSide&
     float* out = (o0 >= p0 && o1 <= p0 + side.chunk) ? side.out + adapter * size
                                                      : side.slots + (2 * (int64_t)chunk + (o0 < p0 ? 0 : 1)) * size;
 #pragma unroll
-    for (int r0 = 0; r0 < kVecs; r0 += kRound) {
+    for (int v = 0; v < kVecs; ++v) joined[wave][v][lane] = acc[v % 8][v / 8];
+    __syncthreads();
+    for (int v = turn * 4; v < kVecs; v += kTurns * 4) {
+      f32x4_t sum[4];
 #pragma unroll
-      for (int v = 0; v < kRound; ++v) joined[wave][v][lane] = acc[(r0 + v) % 8][(r0 + v) / 8];
-      __syncthreads();
-      for (int v = wave * 4; v < kRound; v += kWaves * 4) {
-        f32x4_t sum[4];
+      for (int i = 0; i < 4; ++i) {
+        sum[i] = joined[wave % H][v + i][lane];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          sum[i] = joined[0][v + i][lane];
+        for (int w = 1; w < kTurns; ++w) sum[i] += joined[w * H + wave % H][v + i][lane];
+      }
+      const int w = w0 + 8 * c + v % 8, j = j0 + 16 * (v / 8) + 4 * g;
+      if (j < p.r) {
+        if constexpr (RankMinor) {
 #pragma unroll
-          for (int w = 1; w < kWaves; ++w) sum[i] += joined[w][v + i][lane];
-        }
-        const int w = w0 + 8 * c + v % 8, j = j0 + 16 * ((r0 + v) / 8) + 4 * g;
-        if (j < p.r) {
-          if constexpr (RankMinor) {
+          for (int i = 0; i < 4; ++i)
+            if (w + i < side.W) *(f32x4_t*)(out + (int64_t)(w + i) * p.r + j) = sum[i];
+        } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (w + i < side.W) *(f32x4_t*)(out + (int64_t)(w + i) * p.r + j) = sum[i];
-          } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              float* at = out + (int64_t)(j + q) * side.W + w;
-              if (w < side.W) *(f32x4_t*)at = f32x4_t{sum[0][q], sum[1][q], sum[2][q], sum[3][q]};
-            }
+          for (int q = 0; q < 4; ++q) {
+            float* to = out + (int64_t)(j + q) * side.W + w;
+            if (w < side.W) *(f32x4_t*)to = f32x4_t{sum[0][q], sum[1][q], sum[2][q], sum[3][q]};
           }
         }
       }
-      __syncthreads();
     }
+    __syncthreads();
     s0 = s1;
   }
 }
 
-template <typename TU, int JT, bool VecU>
-__global__ __launch_bounds__(kThreads) void lora_outer_kernel(OuterArgs p) {
-  __shared__ f32x4_t joined[kWaves][8 * JT < 16 ? 8 * JT : 16][64];
+template <typename TU, int JT, int H, bool VecU>
+__global__ __launch_bounds__(kThreads, 2) void lora_outer_kernel(OuterArgs p) {
+  __shared__ f32x4_t joined[kWaves][8 * JT][64];
   __shared__ __align__(16) int64_t offs[kPiece];
-  if ((int)blockIdx.x < p.a_blocks) outer_block<uint16_t, JT, true, false>(p, p.a, blockIdx.x, joined, offs);
-  else outer_block<TU, JT, VecU, true>(p, p.b, blockIdx.x - p.a_blocks, joined, offs);
+  if ((int)blockIdx.x < p.a_blocks) outer_block<uint16_t, JT, H, true, false>(p, p.a, blockIdx.x, joined, offs);
+  else outer_block<TU, JT, H, VecU, true>(p, p.b, blockIdx.x - p.a_blocks, joined, offs);
 }
 
 // Adapters that cross chunks: their slots, in order; adapters without rows:
@@ -1200,22 +1168,24 @@ hipError_t launch_up(UpArgs p, bool out_f32, int tiles, hipStream_t stream) {
 
 hipError_t launch_outer(OuterArgs p, bool b_f32, hipStream_t stream) {
   const bool vec = vec_ok(p.b.u, p.b.ldu, b_f32) && p.b.W % (b_f32 ? 4 : 8) == 0;
-  const int64_t ranks = ceil_div(p.r, 64);
+  const int64_t zs = ceil_div(p.r, 64);
   p.a.chunks = (int)ceil_div(p.cap, p.a.chunk);
   p.b.chunks = (int)ceil_div(p.cap, p.b.chunk);
-  const int64_t a_blocks = ceil_div(p.a.W, 128) * p.a.chunks * ranks;
-  const int64_t blocks = a_blocks + ceil_div(p.b.W, 128) * p.b.chunks * ranks;
+  const int64_t a_blocks = ceil_div(ceil_div(p.a.W, 128) * p.a.chunks, 8) * 8 * zs;
+  const int64_t blocks = a_blocks + ceil_div(ceil_div(p.b.W, 128) * p.b.chunks, 8) * 8 * zs;
   p.a_blocks = (int)a_blocks;
-  auto go = [&](auto jt) {
-    constexpr int JT = decltype(jt)::value;
-    if (b_f32 && vec) lora_outer_kernel<float, JT, true><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
-    else if (b_f32) lora_outer_kernel<float, JT, false><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
-    else if (vec) lora_outer_kernel<uint16_t, JT, true><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
-    else lora_outer_kernel<uint16_t, JT, false><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
+  auto go = [&](auto jt, auto h) {
+    constexpr int JT = decltype(jt)::value, H = decltype(h)::value;
+    if (b_f32 && vec) lora_outer_kernel<float, JT, H, true><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
+    else if (b_f32) lora_outer_kernel<float, JT, H, false><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
+    else if (vec) lora_outer_kernel<uint16_t, JT, H, true><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
+    else lora_outer_kernel<uint16_t, JT, H, false><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
   };
-  if (p.r <= 16) go(std::integral_constant<int, 1>{});
-  else if (p.r <= 32) go(std::integral_constant<int, 2>{});
-  else go(std::integral_constant<int, 4>{});
+  using One = std::integral_constant<int, 1>;
+  using Two = std::integral_constant<int, 2>;
+  if (p.r <= 16) go(One{}, One{});
+  else if (p.r <= 32) go(Two{}, One{});
+  else go(Two{}, Two{});
   return hipGetLastError();
 }
 
@@ -1261,11 +1231,11 @@ LoraLayout lora_layout(int64_t M, int64_t L, int64_t K, int64_t N, int64_t r, bo
     o.dht_off = take(3 * ceil_div(r, 16) * 16 * o.cap * 2);
     o.ht_off = take(3 * ceil_div(r, 16) * 16 * o.cap * 2);
     // positions per workgroup of the weight gradients: as many workgroups as
-    // the chip holds at once (ranks above 32: one a CU, else two), so that
-    // partial sums are few; at least one step for each wave
+    // the chip holds at once, two a CU, so that partial sums are few; at least
+    // one step for each wave
     auto chunk = [&](int64_t W) {
       const int64_t across = ceil_div(W, 128) * ceil_div(r, 64);
-      int64_t cuts = (r > 32 ? 256 : 512) / across;
+      int64_t cuts = 512 / across;
       cuts = cuts < 1 ? 1 : cuts;
       const int64_t c = ceil_div(o.cap, cuts);
       return ceil_div(c > 128 ? c : 128, kLoraTile) * kLoraTile;
