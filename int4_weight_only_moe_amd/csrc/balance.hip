@@ -157,7 +157,8 @@ constexpr int kSumRows = kSumThreads / 16;  // rows of a forward pass at 16 lane
 template <int Lanes, int NV, bool Vec>
 __global__ __launch_bounds__(kSumThreads) void balance_rows_kernel(BalanceArgs a, int chunk_rows, float* psums,
                                                                    int32_t* pcounts, int32_t* ptokens,
-                                                                   int32_t* tickets) {
+                                                                   int32_t* tickets, bool only) {
+  __shared__ double parts[kSumWaves];
   __shared__ int cnt[kMaxExperts];
   __shared__ __align__(16) float sums[kSumWaves][4 * Lanes * NV];
   __shared__ int live_rows;
@@ -180,16 +181,19 @@ __global__ __launch_bounds__(kSumThreads) void balance_rows_kernel(BalanceArgs a
   const int first_id = (unsigned)tid < chunk_n ? chunk_ids[tid] : -1;
   const bool first_live = (unsigned)tid < chunk_n && (!a.valid || a.valid[r0 + (unsigned)tid / (unsigned)k]);
   // the finalize kernel's tickets start at zero
-  for (int s = blockIdx.x * kSumThreads + tid; s < a.S; s += gridDim.x * kSumThreads) tickets[s] = 0;
-  if (r0 >= r1) return;
-  Sequence seq = sequence_of(a, r0);
+  if (!only)
+    for (int s = blockIdx.x * kSumThreads + tid; s < a.S; s += gridDim.x * kSumThreads) tickets[s] = 0;
+  if (r0 >= r1 && !only) return;
+  Sequence seq = only ? Sequence{0, a.offsets ? clamp_row(a.offsets[0], a.M) : 0,
+                                 a.offsets ? clamp_row(a.offsets[1], a.M) : a.M}
+                      : sequence_of(a, r0);
   bool fetched = true;  // v holds row r0 + group if that is in this sequence
   for (; seq.s < a.S; ++seq.s, seq.lo = seq.hi, seq.hi = seq.s < a.S ? a.offsets[seq.s + 1] : 0) {
     const int s = seq.s;
-    if (seq.lo >= r1) break;
+    if (seq.lo >= r1 && !only) break;
     const int lo = seq.lo > r0 ? seq.lo : r0;
     const int hi = seq.hi < r1 ? seq.hi : r1;
-    if (lo >= hi) continue;
+    if (lo >= hi && !only) continue;
     if (tid < E) cnt[tid] = 0;
     if (tid == 0) live_rows = 0;
     __syncthreads();
@@ -226,10 +230,32 @@ __global__ __launch_bounds__(kSumThreads) void balance_rows_kernel(BalanceArgs a
     }
     __syncthreads();
     const int64_t slot = (int64_t)blockIdx.x + s;
+    float sum = 0.0f;
     if (tid < E) {
-      float sum = 0.0f;
 #pragma unroll
       for (int w = 0; w < kSumWaves; ++w) sum += sums[w][tid];
+    }
+    if (only) {  // all of the sequence is here
+      double part = tid < E ? (double)sum * (double)cnt[tid] : 0.0;
+#pragma unroll
+      for (int d = 32; d; d >>= 1) part += __shfl_xor(part, d, 64);
+      if ((tid & 63) == 0) parts[wave] = part;
+      if (tid < E) {
+        a.prob_sums[(int64_t)s * E + tid] = sum;
+        a.counts[(int64_t)s * E + tid] = cnt[tid];
+      }
+      __syncthreads();
+      if (tid == 0) {
+        double loss = 0.0;
+        for (int w = 0; w < kSumWaves; ++w) loss += parts[w];
+        const double T = live_rows;
+        a.tokens[s] = live_rows;
+        a.loss[s] = live_rows ? (float)(loss * (double)E / ((double)k * T * T)) : 0.0f;
+      }
+      __syncthreads();
+      continue;
+    }
+    if (tid < E) {
       psums[slot * E + tid] = sum;
       pcounts[slot * E + tid] = cnt[tid];
     }
@@ -237,6 +263,10 @@ __global__ __launch_bounds__(kSumThreads) void balance_rows_kernel(BalanceArgs a
     __syncthreads();
   }
 }
+
+// Batches that one workgroup sums alone, with no second launch: 128 rows are two
+// passes, which cost less than a launch.
+bool one_workgroup(int64_t M, int64_t S) { return M <= 2 * kSumRows && S <= 64; }
 
 // Sums a sequence's slots for 64 experts at a time, in a fixed order and in
 // fp64, and the loss. With several workgroups a sequence (gridDim.x > 1) each
@@ -457,16 +487,17 @@ BalanceLayout balance_layout(int64_t M, int64_t E, int64_t S) {
 
 hipError_t launch_balance_loss(const BalanceArgs& a, hipStream_t stream) {
   const BalanceLayout L = balance_layout(a.M, a.E, a.S);
-  const int rows = balance_chunk_rows(a.M);
+  const bool only = one_workgroup(a.M, a.S);
+  const int rows = only ? 2 * kSumRows : balance_chunk_rows(a.M);
   float* psums = (float*)(a.ws + L.sums_off);
   int32_t* pcounts = (int32_t*)(a.ws + L.counts_off);
   int32_t* ptokens = (int32_t*)(a.ws + L.tokens_off);
   int32_t* tickets = (int32_t*)(a.ws + L.ticket_off);
   hipError_t err = by_width(a, [&](auto lanes, auto nv, auto vec) {
     balance_rows_kernel<decltype(lanes)::value, decltype(nv)::value, decltype(vec)::value>
-        <<<(unsigned)L.chunks, kSumThreads, 0, stream>>>(a, rows, psums, pcounts, ptokens, tickets);
+        <<<only ? 1u : (unsigned)L.chunks, kSumThreads, 0, stream>>>(a, rows, psums, pcounts, ptokens, tickets, only);
   });
-  if (err != hipSuccess) return err;
+  if (err != hipSuccess || only) return err;
   // few sequences: one workgroup per 64 experts of each
   const unsigned groups = a.S >= 32 ? 1u : (unsigned)ceil_div(a.E, 64);
   balance_finalize_kernel<<<dim3(groups, (unsigned)a.S), kFinThreads, 0, stream>>>(

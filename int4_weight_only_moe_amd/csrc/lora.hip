@@ -187,8 +187,8 @@ __device__ __forceinline__ void transpose_weights(const GroupArgs& g, const Tran
 // rows 64 at a time, counts its rows per adapter (one LDS update per distinct
 // adapter of a step, so rows of one adapter in a run cost no more than mixed
 // ones), the counts become each wave's first positions, and a second walk
-// places the rows. The ids are read twice; 8192 rows take 8 steps a wave.
-__global__ __launch_bounds__(kGroupThreads) void lora_group_kernel(GroupArgs p, TransposeArgs weights) {
+// places the rows. Up to 8192 rows are read once.
+__global__ __launch_bounds__(kGroupThreads, 8) void lora_group_kernel(GroupArgs p, TransposeArgs weights) {
   __shared__ __align__(16) int cnt[kGroupWaves][kMaxKeys];
   __shared__ int off[kMaxKeys + 1], rows_of[kMaxKeys];
   __shared__ int wave_tot[kGroupWaves];
@@ -206,28 +206,30 @@ __global__ __launch_bounds__(kGroupThreads) void lora_group_kernel(GroupArgs p, 
   const int seg = ((p.M + kGroupWaves - 1) / kGroupWaves + 63) / 64 * 64;
   const int f0 = wave * seg < p.M ? wave * seg : p.M;
   const int f1 = f0 + seg < p.M ? f0 + seg : p.M;
-  constexpr int kAhead = 8;  // ids a lane loads at once
-  auto walk = [&](auto step) {
-    for (int fb = f0; fb < f1; fb += 64 * kAhead) {
-      int key[kAhead];
+  // 512 rows of the wave's range: each lane's keys, and its rank among the equal
+  // keys of its step (low half) with their number
+  constexpr int kSteps = 8;
+  int key[kSteps], place[kSteps];
+  auto walk = [&](int fb) {
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int f = fb + 64 * i + lane;
-        const int id = p.ids[f < f1 ? f : f1 - 1];
-        key[i] = id >= 0 && id < p.L ? id : p.L;
-      }
+    for (int i = 0; i < kSteps; ++i) {
+      const int f = fb + 64 * i + lane;
+      const int id = p.ids[f < f1 ? f : f1 - 1];
+      key[i] = id >= 0 && id < p.L ? id : p.L;
+    }
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        if (fb + 64 * i >= f1) break;
-        const uint64_t live = __ballot(fb + 64 * i + lane < f1);
-        const uint64_t same = same_key(key[i], nbits, live);
-        if (fb + 64 * i + lane < f1) step(fb + 64 * i + lane, key[i], bits_below(same), __builtin_popcountll(same));
-      }
+    for (int i = 0; i < kSteps; ++i) {
+      if (fb + 64 * i >= f1) break;
+      const uint64_t same = same_key(key[i], nbits, __ballot(fb + 64 * i + lane < f1));
+      place[i] = bits_below(same) | __builtin_popcountll(same) << 16;
     }
   };
-  walk([&](int, int key, int before, int total) {
-    if (before == 0) cnt[wave][key] += total;
-  });
+  for (int fb = f0; fb < f1; fb += 64 * kSteps) {
+    walk(fb);
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i)
+      if (fb + 64 * i + lane < f1 && (place[i] & 0xffff) == 0) cnt[wave][key[i]] += place[i] >> 16;
+  }
   __syncthreads();
   // exclusive scan of the adapters' padded counts, one adapter a thread
   int total = 0;
@@ -288,13 +290,18 @@ __global__ __launch_bounds__(kGroupThreads) void lora_group_kernel(GroupArgs p, 
     const int left = off[lo] + rows_of[lo] - b * kLoraTile;
     p.tiles[b] = make_int4(lo, left < kLoraTile ? left : kLoraTile, off[lo], off[lo + 1]);
   }
-  walk([&](int row, int key, int before_me, int total_same) {
-    // every lane reads the running position before the first lane advances it
-    // (one wave: its LDS operations complete in order)
-    const int base = cnt[wave][key];
-    p.sorted[base + before_me] = row;
-    if (before_me == 0) cnt[wave][key] = base + total_same;
-  });
+  for (int fb = f0; fb < f1; fb += 64 * kSteps) {
+    if (seg > 64 * kSteps) walk(fb);  // else the one batch is still there
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      if (fb + 64 * i + lane >= f1) continue;
+      // every lane reads the running position before the first lane advances it
+      // (one wave: its LDS operations complete in order)
+      const int base = cnt[wave][key[i]];
+      p.sorted[base + (place[i] & 0xffff)] = fb + 64 * i + lane;
+      if ((place[i] & 0xffff) == 0) cnt[wave][key[i]] = base + (place[i] >> 16);
+    }
+  }
 }
 
 // ------------------------------------------------------------------ a workgroup's tile
@@ -908,13 +915,14 @@ __device__ __forceinline__ void outer_block(const OuterArgs& p, const OuterSide&
   constexpr int kVecs = 8 * JT;                         // accumulators of a wave
   constexpr int kTurns = kWaves / H;                    // waves that take turns at the positions
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
-  // the column blocks of a chunk are neighbours: together they read whole rows
-  const int across = (side.W + 127) / 128;
+  // XCD x (workgroups x, x + 8, ...) takes an eighth of the column blocks, those
+  // of a chunk one after another: together the XCDs read whole rows
+  const int across = (side.W + 127) / 128, part = (across + 7) / 8;
   const int zs = (p.r + 16 * JT * H - 1) / (16 * JT * H);
-  const int at = block % 8 * ((across * side.chunks + 7) / 8) + block / 8 / zs;
-  const int w0 = at % across * 128;
-  const int chunk = at / across;
-  if (chunk >= side.chunks || block / 8 / zs >= (across * side.chunks + 7) / 8) return;
+  const int at = block / 8 / zs;
+  const int w0 = (block % 8 * part + at % part) * 128;
+  const int chunk = at / part;
+  if (w0 >= side.W) return;
   const int turn = wave / H;
   const int j0 = (block / 8 % zs * H + wave % H) * 16 * JT;
   const int ranks = (p.r + 15) / 16;
@@ -1171,8 +1179,8 @@ hipError_t launch_outer(OuterArgs p, bool b_f32, hipStream_t stream) {
   const int64_t zs = ceil_div(p.r, 64);
   p.a.chunks = (int)ceil_div(p.cap, p.a.chunk);
   p.b.chunks = (int)ceil_div(p.cap, p.b.chunk);
-  const int64_t a_blocks = ceil_div(ceil_div(p.a.W, 128) * p.a.chunks, 8) * 8 * zs;
-  const int64_t blocks = a_blocks + ceil_div(ceil_div(p.b.W, 128) * p.b.chunks, 8) * 8 * zs;
+  const int64_t a_blocks = ceil_div(ceil_div(p.a.W, 128), 8) * 8 * p.a.chunks * zs;
+  const int64_t blocks = a_blocks + ceil_div(ceil_div(p.b.W, 128), 8) * 8 * p.b.chunks * zs;
   p.a_blocks = (int)a_blocks;
   auto go = [&](auto jt, auto h) {
     constexpr int JT = decltype(jt)::value, H = decltype(h)::value;
@@ -1289,7 +1297,10 @@ hipError_t launch_lora_forward(const LoraArgs& a, hipStream_t stream) {
   u.part = d.part; u.splits = o.splits; u.scales = a.scales; u.h = a.h;
   err = launch_down(d, false, o.tiles, stream);
   if (err != hipSuccess) return err;
-  if (!o.small && o.splits > 1) {  // every workgroup of up would add the same splits again
+  // up's workgroups each add their tile's splits again; where that is more than
+  // the rest of what they read (64 rows of a few hundred columns), a launch of
+  // its own does it once (4096 rows of rank 64: 5 + 31 us instead of 61)
+  if (o.splits * a.r > 128 && !o.small) {
     float* h = a.h ? a.h : (float*)(a.ws + o.h_off);
     const int64_t size = (int64_t)a.M * a.r;
     lora_sum_kernel<<<(unsigned)ceil_div(size, 4 * kThreads), kThreads, 0, stream>>>(d.part, o.splits, size, a.r, a.ids,
