@@ -378,7 +378,8 @@ int moe_mxfp4_layer(const float* logits, const uint16_t* x_bf16, int32_t M, int3
  *               (T), loss fp32 [S]: out, all of it written. With M = 0 too:
  *               zeros.
  *   workspace   >= moe_balance_workspace_bytes(M, E, S) bytes, 16-byte
- *               aligned; contents on entry do not matter.
+ *               aligned; contents on entry do not matter. One for a larger M
+ *               or S serves smaller ones.
  * The backward call takes expert_counts and seq_tokens as the forward wrote
  * them. A data-parallel job may sum expert_counts, prob_sums and seq_tokens
  * over its ranks before it uses them. Results are identical on every call.
@@ -422,8 +423,12 @@ int moe_balance_loss_backward(const float* logits, int32_t M, int32_t E, int32_t
  *   dx_base, dx bf16 [M, K], as base and out; dx may be NULL (then dx_base is).
  *   grad_a, grad_b fp32 [L, rank, K], [L, N, rank]: every element written.
  *               With M = 0 too: zeros.
- *   workspace   >= moe_lora_workspace_bytes(M, L, K, N, rank, backward) bytes.
- * out and dx are accumulated in fp32 and rounded once; h and dh stay fp32.
+ *   workspace   >= moe_lora_workspace_bytes(M, L, K, N, rank, backward) bytes;
+ *               contents on entry do not matter. One for a larger M serves
+ *               smaller ones, a backward call's serves the forward call.
+ * out and dx are accumulated in fp32 and rounded once; h and dh stay fp32. A
+ * row that is not finite (or whose adapter is not) makes its own row of the
+ * results not finite, and its adapter's gradients.
  * Results are identical on every call.
  * x, a, b, dx_base, dx, h, grad_a, grad_b and workspace are 16-byte aligned,
  * ldx, ld_dx_base and ld_dx multiples of 8; base, out and grad_out need their

@@ -475,7 +475,9 @@ BalanceLayout balance_layout(int64_t M, int64_t E, int64_t S) {
   BalanceLayout L;
   L.chunks = ceil_div(M, balance_chunk_rows(M));
   if (L.chunks < 1) L.chunks = 1;
-  L.slots = L.chunks + S;
+  // room for what any smaller batch takes too
+  const int64_t most = ceil_div(M, kSumRows);
+  L.slots = (most < 1 ? 1 : most > 256 ? 256 : most) + S;
   L.sums_off = 0;
   L.counts_off = align256(L.slots * E * 4);
   L.tokens_off = L.counts_off + align256(L.slots * E * 4);

@@ -599,6 +599,7 @@ struct UpArgs {
   void* out;                  // [M, N]
   int64_t ld_out;
   int n_block;                // columns per workgroup
+  int across;                 // workgroups per tile
 };
 
 // Four consecutive columns from n of a row, as raw bits (fp32: one word each,
@@ -659,7 +660,7 @@ __device__ __forceinline__ void up_factor(const UpArgs& p, const Tile& sh, int n
         const float4 x = *(const float4*)(p.part + s * split_size + at);
         v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
       }
-      if (p.h && blockIdx.x == 0) *(float4*)(p.h + at) = v;
+      if (p.h && blockIdx.x % p.across == 0) *(float4*)(p.h + at) = v;
     }
     float f[4] = {v.x * scale, v.y * scale, v.z * scale, v.w * scale};
 #pragma unroll
@@ -697,8 +698,9 @@ __device__ __forceinline__ void up_tile(const UpArgs& p, const Tile& sh, int n, 
   constexpr int kPitch = RC + 8;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
   const uint16_t* b = p.b + (int64_t)sh.adapter * p.N * p.r;
-  const int n_end = (int)(blockIdx.x + 1) * p.n_block < p.N ? (int)(blockIdx.x + 1) * p.n_block : p.N;
-  int n0 = blockIdx.x * p.n_block + wave * kUpCols;
+  const int first = blockIdx.x % p.across * p.n_block;
+  const int n_end = first + p.n_block < p.N ? first + p.n_block : p.N;
+  int n0 = first + wave * kUpCols;
   uint4 braw[kChunks], base[NSUB][4];
   // without a base the loads read out, and their values are dropped
   const TO* from = p.base ? (const TO*)p.base : (const TO*)p.out;
@@ -710,11 +712,11 @@ __device__ __forceinline__ void up_tile(const UpArgs& p, const Tile& sh, int n, 
     offs[1][threadIdx.x] = sh.rows[threadIdx.x] * p.ld_out;
   }
   __syncthreads();
-  auto load_b = [&](int first) {
+  auto load_b = [&](int col0) {
     if constexpr (None) return;
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
-      const int col = first + (i * 64 + lane) / kChunks;
+      const int col = col0 + (i * 64 + lane) / kChunks;
       braw[i] = load16<uint16_t, true>(b + (int64_t)(col < p.N ? col : p.N - 1) * p.r, (lane % kChunks) * 8, p.r);
     }
   };
@@ -801,7 +803,7 @@ __global__ __launch_bounds__(kThreads, RC <= 64 ? 3 : 1) void lora_up_kernel(UpA
   __shared__ __align__(16) Tile sh;
   __shared__ __align__(16) uint16_t lds[NP * kLoraTile * (RC + 8)];
   __shared__ uint4 blds[kWaves][kUpCols * RC / 8];
-  const int n = find_tile(p.tile, sh, blockIdx.y);
+  const int n = find_tile(p.tile, sh, blockIdx.x / p.across);
   if (n == 0) return;
   const bool none = sh.adapter == p.tile.L;
   if (none && p.base == p.out) return;  // in place
@@ -1155,7 +1157,8 @@ hipError_t launch_up(UpArgs p, bool out_f32, int tiles, hipStream_t stream) {
   int64_t across = 256 * (p.r <= 64 ? 3 : 1) / tiles;
   across = across < 1 ? 1 : (across > cols ? cols : across);
   p.n_block = (int)(ceil_div(cols, across) * kWaves * kUpCols);
-  const dim3 grid((unsigned)ceil_div(p.N, p.n_block), (unsigned)tiles);
+  p.across = (int)ceil_div(p.N, p.n_block);
+  const unsigned grid = (unsigned)(p.across * (int64_t)tiles);
   auto go = [&](auto rc) {
     constexpr int RC = decltype(rc)::value;
     if (out_f32) {
@@ -1224,7 +1227,9 @@ LoraLayout lora_layout(int64_t M, int64_t L, int64_t K, int64_t N, int64_t r, bo
     at += align256(bytes);
     return off;
   };
-  o.part_off = take(o.splits * M * r * 4);
+  // room for what any smaller batch takes too: splits * M <= 512 * 64 unless splits = 1
+  const int64_t part_rows = 8 * M < 512 * kLoraTile ? 8 * M : 512 * kLoraTile;
+  o.part_off = take((M > part_rows ? M : part_rows) * r * 4);
   if (!o.small) {
     o.sorted_off = take(o.cap * 4);
     o.block_off = take(o.cap / kLoraTile * 16);
@@ -1241,17 +1246,17 @@ LoraLayout lora_layout(int64_t M, int64_t L, int64_t K, int64_t N, int64_t r, bo
     // positions per workgroup of the weight gradients: as many workgroups as
     // the chip holds at once, two a CU, so that partial sums are few; at least
     // one step for each wave
-    auto chunk = [&](int64_t W) {
+    auto slots = [&](int64_t W, int& chunk) {
       const int64_t across = ceil_div(W, 128) * ceil_div(r, 64);
       int64_t cuts = 512 / across;
       cuts = cuts < 1 ? 1 : cuts;
       const int64_t c = ceil_div(o.cap, cuts);
-      return ceil_div(c > 128 ? c : 128, kLoraTile) * kLoraTile;
+      chunk = (int)(ceil_div(c > 128 ? c : 128, kLoraTile) * kLoraTile);
+      const int64_t most = ceil_div(o.cap, 128);
+      return take(2 * (most < cuts ? most : cuts) * r * W * 4);
     };
-    o.a_chunk = (int)chunk(K);
-    o.b_chunk = (int)chunk(N);
-    o.a_slots_off = take(2 * ceil_div(o.cap, o.a_chunk) * r * K * 4);
-    o.b_slots_off = take(2 * ceil_div(o.cap, o.b_chunk) * r * N * 4);
+    o.a_slots_off = slots(K, o.a_chunk);
+    o.b_slots_off = slots(N, o.b_chunk);
   }
   o.total = at;
   return o;

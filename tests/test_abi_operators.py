@@ -81,6 +81,19 @@ def test_lora_backward_validation():
     assert moe.moe_lora_workspace_bytes(0, 2, 64, 48, 8, True) > 0
 
 
+def test_workspaces_grow_with_the_batch():
+    """A workspace for more rows serves fewer, and a backward call's the forward call."""
+    for L, K, N, r in ((1, 7168, 7168, 64), (1024, 64, 1, 8), (8, 8, 5000, 128), (64, 2048, 384, 24)):
+        before = {0: 0, 1: 0}
+        for M in [*range(0, 300), *range(300, 20000, 97), 100000, 1 << 22, 1 << 24]:
+            need = {back: moe.moe_lora_workspace_bytes(M, L, K, N, r, back) for back in (0, 1)}
+            assert need[1] >= need[0] and need[0] >= before[0] and need[1] >= before[1], M
+            before = need
+    for E in (1, 384, 1024):
+        sizes = [moe.moe_balance_workspace_bytes(M, E, 5) for M in [*range(0, 3000, 7), *range(3000, 100000, 613)]]
+        assert sizes == sorted(sizes)
+
+
 @pytest.fixture(scope="module")
 def checker():
     import torch

@@ -219,3 +219,13 @@ def test_balance_wrapper_refusals():
     with pytest.raises(moe.MoeError) as e:
         moe.balance_loss(lg, ids, small)
     assert e.value.status == moe.MOE_ERR_WORKSPACE
+
+
+def test_balance_many_short_sequences_and_one_workgroup():
+    """Up to 128 rows and 64 sequences one workgroup does it all; around that limit the same results."""
+    for M, S in ((128, 64), (128, 65), (129, 3), (5, 64), (2000, 1999)):
+        rng = np.random.default_rng(M + S)
+        logits, ids, _, valid = make(M, 48, 4, 1, True, 200 + M)
+        off = np.concatenate([[0], np.sort(rng.integers(0, M + 1, S - 1)), [M]]).astype(np.int32)
+        bufs, ref = check(logits, ids, off, valid, 48, 4, S)
+        check_backward(logits, off, valid, 48, 4, S, ref["counts"], ref["tokens"])

@@ -304,3 +304,48 @@ def test_lora_wrapper_refusals():
         with pytest.raises(moe.MoeError) as e:
             call()
         assert e.value.status == status
+
+
+def test_lora_many_rows():
+    """More tiles than a grid's second dimension holds (M / 64 > 65535)."""
+    M, L, K, N, r = 4_300_000, 2, 8, 8, 8
+    rng = np.random.default_rng(3)
+    x = torch.randn((M, K), device="cuda").to(torch.bfloat16)
+    a = bf16(rng.standard_normal((L, r, K))).cuda()
+    b = bf16(rng.standard_normal((L, N, r))).cuda()
+    gids = torch.randint(-1, L, (M,), device="cuda", dtype=torch.int32)
+    h = torch.empty((M, r), device="cuda")
+    base = torch.zeros((M, N), device="cuda")
+    out = moe.lora_forward(x, gids, a, b, base=base, h=h)
+    dx, da, db = moe.lora_backward(out, x, gids, h, a, b)
+    rows = torch.cat([torch.arange(1000), torch.arange(M - 1000, M)]).cuda()
+    c = Case(2000, L, K, N, r, True, "mixed")  # the bounds of a small case with these rows
+    c.x, c.a, c.b, c.ids, c.scales = x[rows].cpu(), a.cpu(), b.cpu(), gids[rows].cpu().numpy(), torch.ones(L)
+    want, wh, err, herr = forward_bounds(c, np.zeros((2000, N)))
+    within(out[rows], want, err, "out")
+    within(h[rows], wh, herr, "h")
+    for i in range(L):  # the sums over all rows, in fp64 on the device
+        m = gids == i
+        hs = h[m].double()
+        wb = out[m].double().t() @ hs
+        mag = out[m].double().abs().t() @ hs.abs()
+        assert ((db[i].double() - wb).abs() <= mag * (roundings(M, 6) + 2.0 ** -23)).all()
+        assert torch.isfinite(da[i]).all()
+    assert torch.isfinite(dx.float()).all()
+
+
+def test_lora_reused_workspace():
+    """One workspace of the largest batch, backward, serves smaller ones and forward calls."""
+    L, K, N, r = 5, 136, 96, 24
+    ws = torch.empty(moe.moe_lora_workspace_bytes(3000, L, K, N, r, True), dtype=torch.uint8, device="cuda")
+    for M in (3000, 1, 257, 900, 64):
+        c = Case(M, L, K, N, r, False, "mixed", seed=60)
+        d = {n: getattr(c, n).cuda() for n in ("x", "a", "b", "scales", "base", "dout")}
+        gids = torch.from_numpy(c.ids).cuda()
+        h, h2 = torch.empty((M, r), device="cuda"), torch.empty((M, r), device="cuda")
+        one = moe.lora_forward(d["x"], gids, d["a"], d["b"], d["scales"], base=d["base"], h=h, workspace=ws)
+        two = moe.lora_forward(d["x"], gids, d["a"], d["b"], d["scales"], base=d["base"], h=h2)
+        assert torch.equal(one, two) and torch.equal(h, h2)
+        g1 = moe.lora_backward(d["dout"], d["x"], gids, h, d["a"], d["b"], d["scales"], workspace=ws)
+        g2 = moe.lora_backward(d["dout"], d["x"], gids, h, d["a"], d["b"], d["scales"])
+        assert all(torch.equal(p, q) for p, q in zip(g1, g2))
