@@ -816,22 +816,21 @@ __global__ __launch_bounds__(kThreads, RC <= 64 ? 3 : 1) void lora_up_kernel(UpA
 }
 
 // ------------------------------------------------------------------ join
-// The three bf16 parts of scale * (sum of the splits of part) as outer's
-// fragments: [32 positions of the grouping][part][16 ranks][lane], lane (g, c)
-// holding positions 8 g .. + 7 of rank c; zeros at the tile's padding. dh, if
-// asked for, receives the scaled sums.
-__device__ __forceinline__ void rank_major(const TileArgs& tile, const Tile& sh, int n, int index, int r,
+// Of 16 ranks from j0: the three bf16 parts of scale * (sum of the splits of
+// part) as outer's fragments, [32 positions of the grouping][part][16 ranks]
+// [lane], lane (g, c) holding positions 8 g .. + 7 of rank c; zeros at the tile's
+// padding. dh, if asked for, receives the scaled sums.
+__device__ __forceinline__ void rank_major(const TileArgs& tile, const Tile& sh, int n, int index, int r, int j0,
                                            const float* part, int splits, const float* scales, float* dh, uint16_t* vt,
-                                           float* lds) {
+                                           float (*lds)[20]) {
   const int tid = threadIdx.x;
   const float scale = scales ? scales[sh.adapter] : 1.0f;
-  const int pitch = r + 4, quads = r / 4;
-  for (int i = tid; i < kLoraTile * quads; i += kThreads) {
-    const int t = i / quads, j = i % quads * 4;
+  {
+    const int t = tid / 4, j = j0 + tid % 4 * 4;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (t < n) {
+    if (t < n && j < r) {
       const int64_t at = (int64_t)sh.rows[t] * r + j;
-#pragma unroll 4
+#pragma unroll 8
       for (int s = 0; s < splits; ++s) {
         const float4 x = *(const float4*)(part + (int64_t)s * tile.M * r + at);
         v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
@@ -839,27 +838,26 @@ __device__ __forceinline__ void rank_major(const TileArgs& tile, const Tile& sh,
       v = make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
       if (dh) *(float4*)(dh + at) = v;
     }
-    *(float4*)(lds + t * pitch + j) = v;
+    *(float4*)&lds[t][tid % 4 * 4] = v;
   }
   __syncthreads();
+  if (tid >= 128) return;
+  const int lane = tid & 63, half = tid >> 6;
+  const int t = half * 32 + (lane >> 4) * 8;
+  float f[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] = lds[t + e][lane & 15];
+  bf16x8_t q[3];
+  split_parts<3>(f, q);
   const int ranks = (r + 15) / 16;
-  for (int i = tid; i < 2 * ranks * 64; i += kThreads) {
-    const int lane = i & 63, jt = (i >> 6) % ranks, half = (i >> 6) / ranks;
-    const int j = jt * 16 + (lane & 15), t = half * 32 + (lane >> 4) * 8;
-    float f[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = j < r ? lds[(t + e) * pitch + j] : 0.0f;
-    bf16x8_t q[3];
-    split_parts<3>(f, q);
-#pragma unroll
-    for (int e = 0; e < 3; ++e)
-      *(uint4*)(vt + ((((int64_t)index * 2 + half) * 3 + e) * ranks + jt) * 512 + lane * 8) =
-          __builtin_bit_cast(uint4, q[e]);
-  }
+  for (int e = 0; e < 3; ++e)
+    *(uint4*)(vt + ((((int64_t)index * 2 + half) * 3 + e) * ranks + j0 / 16) * 512 + lane * 8) =
+        __builtin_bit_cast(uint4, q[e]);
 }
 
-// dh: the sum of its splits, scaled, as it is and rank-major (blockIdx.y = 0);
-// s h rank-major (1).
+// dh: the sum of its splits, scaled, as it is and rank-major (even blockIdx.y);
+// s h rank-major (odd). blockIdx.y / 2: 16 ranks.
 struct JoinArgs {
   TileArgs tile;
   int r, splits;
@@ -872,11 +870,12 @@ struct JoinArgs {
 };
 __global__ __launch_bounds__(kThreads) void lora_join_kernel(JoinArgs p) {
   __shared__ __align__(16) Tile sh;
-  __shared__ __align__(16) float lds[kLoraTile * (kLoraMaxRank + 4)];
+  __shared__ __align__(16) float lds[kLoraTile][20];
   const int n = find_tile(p.tile, sh, blockIdx.x);
   if (n == 0 || sh.adapter == p.tile.L) return;
-  if (blockIdx.y == 0) rank_major(p.tile, sh, n, blockIdx.x, p.r, p.part, p.splits, p.scales, p.dh, p.dht, lds);
-  else rank_major(p.tile, sh, n, blockIdx.x, p.r, p.h, 1, p.scales, nullptr, p.ht, lds);
+  const int j0 = blockIdx.y / 2 * 16;
+  if (blockIdx.y % 2 == 0) rank_major(p.tile, sh, n, blockIdx.x, p.r, j0, p.part, p.splits, p.scales, p.dh, p.dht, lds);
+  else rank_major(p.tile, sh, n, blockIdx.x, p.r, j0, p.h, 1, p.scales, nullptr, p.ht, lds);
 }
 
 // ------------------------------------------------------------------ outer
@@ -1345,7 +1344,7 @@ hipError_t launch_lora_backward(const LoraArgs& a, hipStream_t stream) {
     j.tile = t; j.r = a.r; j.splits = o.splits; j.part = d.part; j.scales = a.scales;
     j.dh = (float*)(a.ws + o.dh_off); j.dht = (uint16_t*)(a.ws + o.dht_off);
     j.h = a.h; j.ht = (uint16_t*)(a.ws + o.ht_off);
-    lora_join_kernel<<<dim3(o.tiles, 2), kThreads, 0, stream>>>(j);
+    lora_join_kernel<<<dim3(o.tiles, 2 * (unsigned)ceil_div(a.r, 16)), kThreads, 0, stream>>>(j);
     if ((err = hipGetLastError()) != hipSuccess) return err;
     if (a.dx) {
       UpArgs u{};
