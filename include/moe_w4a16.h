@@ -372,8 +372,8 @@ int moe_mxfp4_layer(const float* logits, const uint16_t* x_bf16, int32_t M, int3
  *               [seq_offsets[s], seq_offsets[s + 1]); NULL (S = 1 only): all
  *               rows. Rows of no sequence are not read, and their rows of
  *               grad_logits are left as they were.
- *   row_valid   uint8 [M] or NULL: rows with 0 (padding) are not counted and
- *               their logits are not read; their rows of grad_logits are 0.
+ *   row_valid   uint8 [M] or NULL: rows with 0 (padding) are not counted, what
+ *               their logits hold is not used; their rows of grad_logits are 0.
  *   expert_counts int32 [S, E], prob_sums fp32 [S, E], seq_tokens int32 [S]
  *               (T), loss fp32 [S]: out, all of it written. With M = 0 too:
  *               zeros.

@@ -78,8 +78,9 @@ __device__ __forceinline__ void load_row(const float* __restrict__ row, int E, i
 // Values become exp(v - max) and the result is what makes them probabilities,
 // 1 / their sum. A row of nothing but -inf has none: 0. A NaN or +inf gives NaN.
 // exp(v - m) = 2^(v log2(e) - m log2(e)) in one fused step: the rounding of
-// m log2(e) is the same factor for the whole row and goes out with the sum.
-// Where that product could overflow (|m| >= 2^100) the difference is taken first.
+// m log2(e), at most 2^-4 for |m| < 2^20, is the same factor for the whole row
+// and goes out with the sum. A larger |m| would make that factor large (it
+// overflows from 2^30 on): there the difference is taken first.
 template <int Lanes, int N>
 __device__ __forceinline__ float exp_row(float (&v)[N]) {
   constexpr float kLog2e = 1.4426950408889634f;
@@ -88,7 +89,7 @@ __device__ __forceinline__ float exp_row(float (&v)[N]) {
   for (int i = 1; i < N; ++i) m = fmaxf(m, v[i]);
   m = row_max<Lanes>(m);
   m = m == -INFINITY ? 0.0f : m;
-  const bool far = fabsf(m) >= 0x1p100f;
+  const bool far = fabsf(m) >= 0x1p20f;
   if (__any(far)) {
     const float first = far ? m : 0.0f;
 #pragma unroll
@@ -192,8 +193,9 @@ __global__ __launch_bounds__(kSumThreads) void balance_rows_kernel(BalanceArgs a
     const int s = seq.s;
     if (seq.lo >= r1 && !only) break;
     const int lo = seq.lo > r0 ? seq.lo : r0;
-    const int hi = seq.hi < r1 ? seq.hi : r1;
+    int hi = seq.hi < r1 ? seq.hi : r1;
     if (lo >= hi && !only) continue;
+    hi = hi < lo ? lo : hi;
     if (tid < E) cnt[tid] = 0;
     if (tid == 0) live_rows = 0;
     __syncthreads();

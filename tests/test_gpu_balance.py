@@ -229,3 +229,44 @@ def test_balance_many_short_sequences_and_one_workgroup():
         off = np.concatenate([[0], np.sort(rng.integers(0, M + 1, S - 1)), [M]]).astype(np.int32)
         bufs, ref = check(logits, ids, off, valid, 48, 4, S)
         check_backward(logits, off, valid, 48, 4, S, ref["counts"], ref["tokens"])
+
+
+def test_balance_large_logits():
+    """Rows of every magnitude, each of values a few steps of its type apart:
+    a row that a mask has moved as a whole keeps its probabilities. Values more
+    than 104 below the maximum are below 2^-126; the others differ by at most
+    104, which is what the tolerance counts for a difference."""
+    E, k = 24, 2
+    tops = [3e6, -3e6, 1e9, -1e9, 1e10, -1e10, 1.7e12, -1e15, 1e20, -1e25, 1e29, -1e30, 1.2e30, -1.3e30, 1e31, 3e38,
+            np.finfo(np.float32).min]
+    rng = np.random.default_rng(12)
+    logits = np.zeros((len(tops), E), np.float32)
+    for i, top in enumerate(tops):
+        steps = rng.integers(0, 3, E)
+        v = np.full(E, top, np.float32)
+        for _ in range(2):
+            v = np.where(steps > 0, np.nextafter(v, np.float32(0)), v)
+            steps -= 1
+        logits[i] = v
+    logits[4, 5:] = 0.25  # 1e10 against ordinary values
+    logits[5, 7] = 0.25
+    S = len(tops)
+    off = np.arange(S + 1, dtype=np.int32)
+    ids = np.stack([rng.permutation(E)[:k] for _ in range(S)]).astype(np.int32)
+    ref = oracle.balance(logits, ids, off, None)
+    n = 104 + 6 + 4 + 4
+    for repeat in (1, 20):  # one workgroup, and the chunks' path
+        lg, iv, ov = np.repeat(logits, repeat, 0), np.repeat(ids, repeat, 0), off * repeat
+        bufs = moe.alloc_balance_buffers(S * repeat, E, S)
+        moe.balance_loss(dev(lg), dev(iv), bufs, seq_offsets=dev(ov))
+        np.testing.assert_allclose(bufs.prob_sums.cpu().numpy(), ref["probs"] * repeat, rtol=(n + 10) * U,
+                                   atol=repeat * 2.0 ** -126)
+        np.testing.assert_allclose(bufs.loss.cpu().numpy(), ref["loss"], rtol=(n + 11) * U, atol=2.0 ** -120)
+    gl = np.ones(S, np.float32)
+    want = oracle.balance_backward(logits, k, ref["counts"], ref["tokens"], gl, off, None)
+    got = moe.balance_loss_backward(dev(logits), k, dev(ref["counts"].astype(np.int32)),
+                                    dev(ref["tokens"].astype(np.int32)), dev(gl), seq_offsets=dev(off))
+    p = ref["probs"]
+    bound = E / k * p * (ref["counts"] + (ref["counts"] * p).sum(1, keepdims=True))
+    err = np.abs(got.cpu().numpy() - want)
+    assert (err <= (2 * n + 4 + 4 + 10) * U * bound + 2.0 ** -120).all()
