@@ -34,6 +34,8 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kSub = 16;  // rows of a matrix-core tile
 
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+
 __device__ __forceinline__ uint32_t bf16_bits(float v) {
   return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)v);
 }
@@ -603,16 +605,17 @@ struct UpArgs {
 };
 
 // Four consecutive columns from n of a row, as raw bits (fp32: one word each,
-// bf16: two words in all); columns past the end hold anything. Vec: the row is 16-byte aligned and N % 4 == 0.
-template <typename TO, bool Vec>
+// bf16: two words in all); columns past the end hold anything. Vec: the row is
+// 16-byte aligned and N % 4 == 0. Past: around the caches.
+template <typename TO, bool Vec, bool Past>
 __device__ __forceinline__ uint4 load4(const TO* row, int n, int N) {
   // columns past the end read the row's first ones: a load that is always made
   // keeps the count of loads in flight known
   if constexpr (Vec) {
     const TO* at = row + (n < N ? n : 0);
     if constexpr (sizeof(TO) == 4) return *(const uint4*)at;
-    const uint2 v = *(const uint2*)at;
-    return make_uint4(v.x, v.y, 0, 0);
+    const u32x2_t v = Past ? __builtin_nontemporal_load((const u32x2_t*)at) : *(const u32x2_t*)at;
+    return make_uint4(v[0], v[1], 0, 0);
   } else {
     uint32_t d[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -624,12 +627,13 @@ __device__ __forceinline__ uint4 load4(const TO* row, int n, int N) {
     return make_uint4(d[0], d[1], d[2], d[3]);
   }
 }
-template <typename TO, bool Vec>
+template <typename TO, bool Vec, bool Past>
 __device__ __forceinline__ void store4(TO* row, int n, int N, uint4 v) {
   if constexpr (Vec) {
     if (n >= N) return;
     if constexpr (sizeof(TO) == 4) *(uint4*)(row + n) = v;
-    else *(uint2*)(row + n) = make_uint2(v.x, v.y);
+    else if constexpr (Past) __builtin_nontemporal_store(u32x2_t{v.x, v.y}, (u32x2_t*)(row + n));
+    else *(u32x2_t*)(row + n) = u32x2_t{v.x, v.y};
   } else {
     const uint32_t d[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -688,7 +692,7 @@ constexpr int kUpCols = 64;  // columns of a wave
 // rows are consecutive in memory and go through the wave's own part of LDS, as
 // in down. What does not depend on the factor is loaded before it is made.
 // None: rows without an adapter, out = base.
-template <typename TO, int RC, bool Vec, int NSUB, bool None = false>
+template <typename TO, int RC, bool Vec, bool Past, int NSUB, bool None = false>
 __device__ __forceinline__ void up_tile(const UpArgs& p, const Tile& sh, int n, uint16_t* lds, uint4* blds,
                                         int64_t (*offs)[kLoraTile]) {
   constexpr int NP = sizeof(TO) == 4 ? 3 : 2;
@@ -723,7 +727,7 @@ __device__ __forceinline__ void up_tile(const UpArgs& p, const Tile& sh, int n, 
   auto load_base = [&](int ts, int col) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      base[ts][q] = load4<TO, Vec>(from + offs[0][ts * kSub + 4 * g + q], col, p.N);
+      base[ts][q] = load4<TO, Vec, Past>(from + offs[0][ts * kSub + 4 * g + q], col, p.N);
   };
   if (n0 < n_end) {
     load_b(n0);
@@ -788,7 +792,7 @@ __device__ __forceinline__ void up_tile(const UpArgs& p, const Tile& sh, int n, 
           d.x = bf16_pair(__uint_as_float(in[q].x << 16) + acc[0][q], __uint_as_float(in[q].x & 0xffff0000u) + acc[1][q]);
           d.y = bf16_pair(__uint_as_float(in[q].y << 16) + acc[2][q], __uint_as_float(in[q].y & 0xffff0000u) + acc[3][q]);
         }
-        if (t < n) store4<TO, Vec>((TO*)p.out + offs[1][t], col, p.N, d);
+        if (t < n) store4<TO, Vec, Past>((TO*)p.out + offs[1][t], col, p.N, d);
       }
     }
     n0 = next;
@@ -797,7 +801,7 @@ __device__ __forceinline__ void up_tile(const UpArgs& p, const Tile& sh, int n, 
   if (n0 < n_end) columns(std::false_type{});
 }
 
-template <typename TO, int RC, bool Vec>
+template <typename TO, int RC, bool Vec, bool Past>
 __global__ __launch_bounds__(kThreads, RC <= 64 ? 3 : 1) void lora_up_kernel(UpArgs p) {
   constexpr int NP = sizeof(TO) == 4 ? 3 : 2;
   __shared__ __align__(16) Tile sh;
@@ -809,10 +813,10 @@ __global__ __launch_bounds__(kThreads, RC <= 64 ? 3 : 1) void lora_up_kernel(UpA
   if (none && p.base == p.out) return;  // in place
   __shared__ __align__(16) int64_t offs[2][kLoraTile];
   uint4* mine = blds[threadIdx.x >> 6];
-  if (none) up_tile<TO, RC, Vec, 4, true>(p, sh, n, lds, mine, offs);
-  else if (n <= 16) up_tile<TO, RC, Vec, 1>(p, sh, n, lds, mine, offs);
-  else if (n <= 32) up_tile<TO, RC, Vec, 2>(p, sh, n, lds, mine, offs);
-  else up_tile<TO, RC, Vec, 4>(p, sh, n, lds, mine, offs);
+  if (none) up_tile<TO, RC, Vec, Past, 4, true>(p, sh, n, lds, mine, offs);
+  else if (n <= 16) up_tile<TO, RC, Vec, Past, 1>(p, sh, n, lds, mine, offs);
+  else if (n <= 32) up_tile<TO, RC, Vec, Past, 2>(p, sh, n, lds, mine, offs);
+  else up_tile<TO, RC, Vec, Past, 4>(p, sh, n, lds, mine, offs);
 }
 
 // ------------------------------------------------------------------ join
@@ -895,7 +899,7 @@ struct OuterArgs {
   const int32_t* sorted;
   const int4* tiles;
   OuterSide a, b;             // dA (x, bf16), dB (the output side, either type)
-  int a_blocks;               // workgroups of dA, before those of dB
+  int b_blocks;               // workgroups of dB, before those of dA
 };
 
 constexpr int kPiece = 1024;  // positions whose rows are in LDS at a time
@@ -1083,8 +1087,8 @@ template <typename TU, int JT, int H, bool VecU>
 __global__ __launch_bounds__(kThreads, 2) void lora_outer_kernel(OuterArgs p) {
   __shared__ f32x4_t joined[kWaves][8 * JT][64];
   __shared__ __align__(16) int64_t offs[kPiece];
-  if ((int)blockIdx.x < p.a_blocks) outer_block<uint16_t, JT, H, true, false>(p, p.a, blockIdx.x, joined, offs);
-  else outer_block<TU, JT, H, VecU, true>(p, p.b, blockIdx.x - p.a_blocks, joined, offs);
+  if ((int)blockIdx.x < p.b_blocks) outer_block<TU, JT, H, VecU, true>(p, p.b, blockIdx.x, joined, offs);
+  else outer_block<uint16_t, JT, H, true, false>(p, p.a, blockIdx.x - p.b_blocks, joined, offs);
 }
 
 // Adapters that cross chunks: their slots, in order; adapters without rows:
@@ -1145,7 +1149,8 @@ hipError_t launch_down(DownArgs p, bool u_f32, int tiles, hipStream_t stream) {
   return hipGetLastError();
 }
 
-hipError_t launch_up(UpArgs p, bool out_f32, int tiles, hipStream_t stream) {
+// past: base and out need not stay in the caches (bf16).
+hipError_t launch_up(UpArgs p, bool out_f32, bool past, int tiles, hipStream_t stream) {
   const bool vec = vec_ok(p.base, p.ld_base, out_f32) && vec_ok(p.out, p.ld_out, out_f32) &&
                    p.N % (out_f32 ? 4 : 8) == 0;
   // as many workgroups as the chip holds at once (by their registers and LDS),
@@ -1161,11 +1166,12 @@ hipError_t launch_up(UpArgs p, bool out_f32, int tiles, hipStream_t stream) {
   auto go = [&](auto rc) {
     constexpr int RC = decltype(rc)::value;
     if (out_f32) {
-      if (vec) lora_up_kernel<float, RC, true><<<grid, kThreads, 0, stream>>>(p);
-      else lora_up_kernel<float, RC, false><<<grid, kThreads, 0, stream>>>(p);
+      if (vec) lora_up_kernel<float, RC, true, false><<<grid, kThreads, 0, stream>>>(p);
+      else lora_up_kernel<float, RC, false, false><<<grid, kThreads, 0, stream>>>(p);
     } else {
-      if (vec) lora_up_kernel<uint16_t, RC, true><<<grid, kThreads, 0, stream>>>(p);
-      else lora_up_kernel<uint16_t, RC, false><<<grid, kThreads, 0, stream>>>(p);
+      if (vec && past) lora_up_kernel<uint16_t, RC, true, true><<<grid, kThreads, 0, stream>>>(p);
+      else if (vec) lora_up_kernel<uint16_t, RC, true, false><<<grid, kThreads, 0, stream>>>(p);
+      else lora_up_kernel<uint16_t, RC, false, false><<<grid, kThreads, 0, stream>>>(p);
     }
   };
   if (p.r <= 8) go(std::integral_constant<int, 8>{});
@@ -1181,9 +1187,9 @@ hipError_t launch_outer(OuterArgs p, bool b_f32, hipStream_t stream) {
   const int64_t zs = ceil_div(p.r, 64);
   p.a.chunks = (int)ceil_div(p.cap, p.a.chunk);
   p.b.chunks = (int)ceil_div(p.cap, p.b.chunk);
-  const int64_t a_blocks = ceil_div(ceil_div(p.a.W, 128), 8) * 8 * p.a.chunks * zs;
-  const int64_t blocks = a_blocks + ceil_div(ceil_div(p.b.W, 128), 8) * 8 * p.b.chunks * zs;
-  p.a_blocks = (int)a_blocks;
+  const int64_t b_blocks = ceil_div(ceil_div(p.b.W, 128), 8) * 8 * p.b.chunks * zs;
+  const int64_t blocks = b_blocks + ceil_div(ceil_div(p.a.W, 128), 8) * 8 * p.a.chunks * zs;
+  p.b_blocks = (int)b_blocks;
   auto go = [&](auto jt, auto h) {
     constexpr int JT = decltype(jt)::value, H = decltype(h)::value;
     if (b_f32 && vec) lora_outer_kernel<float, JT, H, true><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
@@ -1312,7 +1318,7 @@ hipError_t launch_lora_forward(const LoraArgs& a, hipStream_t stream) {
     if ((err = hipGetLastError()) != hipSuccess) return err;
     u.part = h; u.splits = 1; u.h = nullptr;
   }
-  return launch_up(u, a.y_f32, o.tiles, stream);
+  return launch_up(u, a.y_f32, false, o.tiles, stream);
 }
 
 hipError_t launch_lora_backward(const LoraArgs& a, hipStream_t stream) {
@@ -1346,12 +1352,6 @@ hipError_t launch_lora_backward(const LoraArgs& a, hipStream_t stream) {
     j.h = a.h; j.ht = (uint16_t*)(a.ws + o.ht_off);
     lora_join_kernel<<<dim3(o.tiles, 2 * (unsigned)ceil_div(a.r, 16)), kThreads, 0, stream>>>(j);
     if ((err = hipGetLastError()) != hipSuccess) return err;
-    if (a.dx) {
-      UpArgs u{};
-      u.tile = t; u.r = a.r; u.N = a.K; u.part = j.dh; u.splits = 1;
-      u.b = f.at; u.base = a.dx_base; u.ld_base = a.ld_dx_base; u.out = a.dx; u.ld_out = a.ld_dx;
-      if ((err = launch_up(u, false, o.tiles, stream)) != hipSuccess) return err;
-    }
     OuterArgs w{};
     w.r = a.r; w.M = a.M; w.L = a.L; w.cap = o.cap; w.sorted = t.sorted; w.tiles = t.tiles;
     w.a.u = a.x; w.a.ldu = a.ldx; w.a.W = a.K; w.a.vt = j.dht; w.a.out = a.da;
@@ -1359,6 +1359,17 @@ hipError_t launch_lora_backward(const LoraArgs& a, hipStream_t stream) {
     w.b.u = a.dout; w.b.ldu = a.ld_dout; w.b.W = a.N; w.b.vt = j.ht; w.b.out = a.db;
     w.b.slots = (float*)(a.ws + o.b_slots_off); w.b.chunk = o.b_chunk;
     if ((err = launch_outer(w, a.y_f32, stream)) != hipSuccess) return err;
+    if (a.dx) {
+      // last, so that outer finds grad_out where down left it, in the 256 MB cache
+      // (8192 rows of [7168] twice, rank 64: outer 81 us after dx, 71 before it).
+      // A call that moves more than the cache holds keeps dx and its base out of
+      // it: their write-back fell into the next kernels (193 us in all, 185 so).
+      const bool past = 6 * (int64_t)a.M * a.K + (a.y_f32 ? 4 : 2) * (int64_t)a.M * a.N > (int64_t(256) << 20);
+      UpArgs u{};
+      u.tile = t; u.r = a.r; u.N = a.K; u.part = j.dh; u.splits = 1;
+      u.b = f.at; u.base = a.dx_base; u.ld_base = a.ld_dx_base; u.out = a.dx; u.ld_out = a.ld_dx;
+      if ((err = launch_up(u, false, past, o.tiles, stream)) != hipSuccess) return err;
+    }
   }
   const int64_t widest = red.size[0] > red.size[1] ? red.size[0] : red.size[1];
   int64_t blocks = ceil_div(widest, 4 * kThreads);
