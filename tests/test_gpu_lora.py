@@ -349,3 +349,31 @@ def test_lora_reused_workspace():
         g1 = moe.lora_backward(d["dout"], d["x"], gids, h, d["a"], d["b"], d["scales"], workspace=ws)
         g2 = moe.lora_backward(d["dout"], d["x"], gids, h, d["a"], d["b"], d["scales"])
         assert all(torch.equal(p, q) for p, q in zip(g1, g2))
+
+
+def test_lora_backward_larger_than_the_cache():
+    """Ten times the rows of one case, with more than 256 MB to move: the same
+    dx for each repetition (with a base, in place, and without one), ten times
+    the weight gradients."""
+    M, L, K, N, r, times = 230, 3, 20480, 72, 16, 10
+    assert times * M * (6 * K + 2 * N) > 2**28 > M * (6 * K + 2 * N)
+    c = Case(M, L, K, N, r, False, "mixed", seed=61)
+    gids, a, b, s = torch.from_numpy(c.ids).cuda(), c.a.cuda(), c.b.cuda(), c.scales.cuda()
+    x, dout, dxb = c.x.cuda(), c.dout.cuda(), c.dx_base.cuda()
+    h = torch.empty((M, r), device="cuda")
+    moe.lora_forward(x, gids, a, b, s, h=h)
+    dx, da, db, edx, eda, edb = backward_bounds(c, h.double().cpu().numpy(), c.dx_base.double().numpy())
+    many = [t.repeat(times, *[1] * (t.dim() - 1)) for t in (dout, x, gids, h, dxb)]
+    got = moe.lora_backward(*many[:4], a, b, s, dx_base=many[4])
+    for i in range(times):
+        within(got[0][i * M:(i + 1) * M], dx, edx, "dx")
+    # eda and edb hold roundings(M, 3) of the terms' magnitudes; the longer sums take the difference more
+    more = (roundings(times * M, 3) - roundings(M, 3)) / roundings(M, 3)
+    within(got[1], times * da, times * eda * (1 + more), "da")
+    within(got[2], times * db, times * edb * (1 + more), "db")
+    place = many[4].clone()
+    moe.lora_backward(*many[:4], a, b, s, dx_base=place, grads=(place, *[torch.empty_like(t) for t in got[1:]]))
+    assert torch.equal(place, got[0])
+    bare = moe.lora_backward(*many[:4], a, b, s)
+    zero = moe.lora_backward(*many[:4], a, b, s, dx_base=torch.zeros_like(place))
+    assert torch.equal(bare[0], zero[0])
