@@ -4,9 +4,11 @@ The layer of "The Throughput Lever: Quantifying the MoE GEMM and Mapping the
 Road to B300" (section "Phase 3: The INT4 Marlin MoE Throughput Lever"):
 top-k routing, per-expert grouping padded to the tile size, FC1 gate/up with
 SiLU*mul and FC2 with the routing-weighted sum, as HIP kernels for gfx950
-behind the C ABI of include/moe_w4a16.h. This package is the Python binding
-(ctypes; PyTorch only provides device memory and streams) plus two helpers
-that allocate the buffers a layer call needs.
+behind the C ABI of include/moe_w4a16.h, and beside it the router's balance
+loss with its gradient (balance_loss, balance_loss_backward) and low-rank
+adapters of many requests, forward and backward (lora_forward, lora_backward).
+This package is the Python binding (ctypes; PyTorch only provides device memory
+and streams) plus helpers that allocate the buffers a call needs.
 """
 from __future__ import annotations
 

@@ -155,6 +155,8 @@ constexpr int kSumRows = kSumThreads / 16;  // rows of a forward pass at 16 lane
 // that 64 rows are in flight at once: with 4 waves and the next row prefetched
 // [16384, 384] took 13.8 us, bound by the loads' latency. The first row and the
 // first choices of the chunk are loaded before the sequence is looked up.
+// [16384, 384] with offsets and padding 13.1 us (25 MB: one pass, bound by the
+// latencies of that and of the join), [32768, 1024] 31 us (4.4 TB/s).
 template <int Lanes, int NV, bool Vec>
 __global__ __launch_bounds__(kSumThreads) void balance_rows_kernel(BalanceArgs a, int chunk_rows, float* psums,
                                                                    int32_t* pcounts, int32_t* ptokens,
@@ -273,7 +275,8 @@ bool one_workgroup(int64_t M, int64_t S) { return M <= 2 * kSumRows && S <= 64; 
 // Sums a sequence's slots for 64 experts at a time, in a fixed order and in
 // fp64, and the loss. With several workgroups a sequence (gridDim.x > 1) each
 // leaves its part of the loss, and the last one to finish (the ticket) adds
-// the parts in order.
+// the parts in order. Bound by latency: 5.6 us for 4 sequences of 384 experts,
+// 7.0 for one of 1024 in 256 chunks.
 constexpr int kFinThreads = 1024;
 __global__ __launch_bounds__(kFinThreads) void balance_finalize_kernel(BalanceArgs a, int chunk_rows,
                                                                        const float* psums, const int32_t* pcounts,
@@ -348,7 +351,7 @@ __global__ __launch_bounds__(kFinThreads) void balance_finalize_kernel(BalanceAr
     // only, which the whole device performs in one place: a part is there once
     // the old value has come back, and the ticket is drawn after that (it adds
     // what came back, masked to nothing, to the one it draws). A fence would
-    // write the L2 back: 2 us here.
+    // write the L2 back: 7.6 us instead of 5.6.
     unsigned long long* mine = (unsigned long long*)ploss + (int64_t)s * 16;
     int drawn = 0;
     if (lane == 0) {
@@ -372,6 +375,8 @@ __global__ __launch_bounds__(kFinThreads) void balance_finalize_kernel(BalanceAr
 
 // A row's lanes take every kRows-th row of a chunk, the next row in flight
 // while they compute one. They hold the counts of its current sequence.
+// [16384, 384]: 12.6 us for 50 MB read and written (4.0 TB/s; a copy of as much
+// takes 9.3 at the rate of a large one).
 template <int Lanes, int NV, bool Vec>
 __global__ __launch_bounds__(kThreads) void balance_backward_kernel(BalanceArgs a, int chunk_rows) {
   constexpr int kRows = kThreads / Lanes;

@@ -17,7 +17,9 @@
 //           s h rank-major (the transposed weights are made beside the grouping);
 //   outer   sums rows' outer products (dA, dB), reduce joins what was cut.
 // With r <= 128 each of them moves the wide side once and is bound by that
-// traffic, so the products are made exact where that is free: bf16 operands
+// traffic (a copy reaches 5.2 TB/s read and written, a read 7), a small call by
+// the launches (3.6 us each), so the products are made exact where that is
+// free: bf16 operands
 // multiply exactly into fp32, and an fp32 factor (h, dh, an fp32 side) enters
 // as bf16 parts of 8 bits each, three (24 bits: all of fp32) where the result
 // is fp32, two (16 bits, 2^-17 relative against the 2^-8 of the result's own
@@ -189,7 +191,9 @@ __device__ __forceinline__ void transpose_weights(const GroupArgs& g, const Tran
 // rows 64 at a time, counts its rows per adapter (one LDS update per distinct
 // adapter of a step, so rows of one adapter in a run cost no more than mixed
 // ones), the counts become each wave's first positions, and a second walk
-// places the rows. Up to 8192 rows are read once.
+// places the rows. Up to 8192 rows are read once. Bound by the latency of its
+// passes: 6.4 us for 8192 rows, with the weights' transposition beside it (rank
+// 64, [7168] both sides) too.
 __global__ __launch_bounds__(kGroupThreads, 8) void lora_group_kernel(GroupArgs p, TransposeArgs weights) {
   __shared__ __align__(16) int cnt[kGroupWaves][kMaxKeys];
   __shared__ int off[kMaxKeys + 1], rows_of[kMaxKeys];
@@ -447,13 +451,15 @@ struct DownShape {
 // A wave's sums over its steps of v[j][w] * u[row][w], left in its LDS as
 // [row][rank] with the 16-byte chunks of a row exchanged by row.
 // The matrix core wants lane (g, c) to hold 8 columns of row c, but a load
-// instruction runs at full rate only where neighbouring lanes read
-// neighbouring bytes (16 bytes a row and lane ran at a quarter of it: 40 us
-// against 27 for x [8192, 7168] alone, ranks 64). So eight lanes read a row's
-// 128 bytes, and the step goes through the wave's own part of LDS (no other
-// wave takes part, so no barrier), chunks exchanged by row so that the 16 rows
-// of a fragment lie in different banks. The next step's loads are in flight
-// while this one is multiplied.
+// instruction runs at full rate only where neighbouring lanes read neighbouring
+// bytes (with 16 bytes a row and lane the kernel took 40 us instead of 32 for
+// [8192, 7168], rank 64). So eight lanes read a row's 128 bytes, and the step
+// goes through the wave's own part of LDS (no other wave takes part, so no
+// barrier), chunks exchanged by row so that the 16 rows of a fragment lie in
+// different banks. The next step's loads are in flight while this one is
+// multiplied. Bound by the reading of u, beside which as many bytes of v come
+// from L2: [8192, 7168] bf16, rank 64, 31.6 us (3.7 TB/s of u), six adapters'
+// [4096, 7168] 25 us; one row 4.9 us, little more than a launch.
 template <typename TU, int RT, bool VecU, int NSUB>
 __device__ __forceinline__ void down_tile(const DownArgs& p, const Tile& sh, uint4* lds) {
   constexpr bool kF32 = std::is_same<TU, float>::value;
@@ -570,7 +576,8 @@ __global__ __launch_bounds__(kThreads) void lora_down_kernel(DownArgs p) {
   }
 }
 
-// h: the sum of its splits; 0 for rows without an adapter.
+// h: the sum of its splits; 0 for rows without an adapter. 5 us for 7 splits of
+// [4096, 64].
 __global__ __launch_bounds__(kThreads) void lora_sum_kernel(const float* __restrict__ part, int splits, int64_t size,
                                                             int r, const int32_t* __restrict__ ids, int L,
                                                             float* __restrict__ h) {
@@ -692,6 +699,10 @@ constexpr int kUpCols = 64;  // columns of a wave
 // rows are consecutive in memory and go through the wave's own part of LDS, as
 // in down. What does not depend on the factor is loaded before it is made.
 // None: rows without an adapter, out = base.
+// Bound by reading the base and writing out, beside which b comes from L2:
+// [8192, 7168] bf16 of rank 64 58 us (4.1 TB/s, where copying in the same
+// pattern takes 35 to 42), [4096, 7168] 31 us, rank 16 [1999, 7168] 15 us; two
+// workgroups a CU instead of three took 38 us for the second.
 template <typename TO, int RC, bool Vec, bool Past, int NSUB, bool None = false>
 __device__ __forceinline__ void up_tile(const UpArgs& p, const Tile& sh, int n, uint16_t* lds, uint4* blds,
                                         int64_t (*offs)[kLoraTile]) {
@@ -861,7 +872,10 @@ __device__ __forceinline__ void rank_major(const TileArgs& tile, const Tile& sh,
 }
 
 // dh: the sum of its splits, scaled, as it is and rank-major (even blockIdx.y);
-// s h rank-major (odd). blockIdx.y / 2: 16 ranks.
+// s h rank-major (odd). blockIdx.y / 2: 16 ranks. outer would otherwise make the
+// parts once for each 128 columns. Bound by latency: 7.1 us for 8192 rows of
+// rank 64, 3.5 to 4 for 1000 to 2000 of ranks up to 32 (with all ranks in one
+// workgroup 8.4 and 4.9).
 struct JoinArgs {
   TileArgs tile;
   int r, splits;
@@ -913,6 +927,11 @@ constexpr int kPiece = 1024;  // positions whose rows are in LDS at a time
 // chunk go to the output, those of one that crosses the chunk's start or end to
 // slots 2 c or 2 c + 1, which the reduce kernel adds in order. Ranks above 64
 // are further workgroups, eight apart: on the same XCD, whose L2 has the columns.
+// Bound by the reading of both sides: x and grad_out of [8192, 7168], rank 64,
+// 68 us (3.5 TB/s); [1999, 7168] and [1999, 2048] of rank 16 12 us. One wave or
+// two a SIMD, loads one to three steps ahead and 32 ranks a wave or 64 were all
+// within 15 % of each other. An fp32 side enters as three parts, of whose
+// products with the factor's three the six above 2^-24 are taken.
 template <typename TU, int JT, int H, bool VecU, bool RankMinor>
 __device__ __forceinline__ void outer_block(const OuterArgs& p, const OuterSide& side, int block,
                                             f32x4_t (*joined)[8 * JT][64], int64_t* offs) {
@@ -1092,7 +1111,8 @@ __global__ __launch_bounds__(kThreads, 2) void lora_outer_kernel(OuterArgs p) {
 }
 
 // Adapters that cross chunks: their slots, in order; adapters without rows:
-// zeros. blockIdx.z: dA, dB.
+// zeros. blockIdx.z: dA, dB. 8 us for one adapter of rank 64 and [7168] both
+// sides in 9 chunks (33 MB of partial sums, which the caches still hold).
 struct ReduceArgs {
   const int32_t* offsets;
   int64_t size[2];
@@ -1216,8 +1236,10 @@ LoraLayout lora_layout(int64_t M, int64_t L, int64_t K, int64_t N, int64_t r, bo
   o.cap = ceil_div(M + lists * (kLoraTile - 1), kLoraTile) * kLoraTile;
   // a small batch has no padded lists: at most one tile per list and 64 rows
   o.tiles = (int)(o.small ? (M < M / kLoraTile + lists ? M : M / kLoraTile + lists) : o.cap / kLoraTile);
-  // splits of the contraction: enough workgroups for the chip, each wave at
-  // least one step, and no more than 8 partial sums to add
+  // splits of the contraction: as many workgroups as the chip holds at once, two
+  // a CU (8192 rows of rank 64: 256 workgroups 43 us, 384 35, 512 31, 700 40, 1024
+  // 37), each wave at least one step, and no more than 8 partial sums to add (16:
+  // 64 rows of rank 16 11 us instead of 8)
   const int64_t steps = ceil_div(backward ? N : K, 64);
   // (the tiles of a batch are M / 64 and part of one for each adapter with rows)
   const int64_t full = ceil_div(M, kLoraTile);
