@@ -516,8 +516,10 @@ hipError_t launch_balance_loss(const BalanceArgs& a, hipStream_t stream) {
 
 hipError_t launch_balance_backward(const BalanceArgs& a, hipStream_t stream) {
   // two passes a workgroup, so that the counts are read for more than one row
-  // and the second row is in flight, once that leaves two workgroups a CU
-  const int rows = kPassRows * (a.M >= 1024 * kPassRows ? 2 : 1);
+  // and the second row is in flight, once that leaves two workgroups a CU; more
+  // from 2^24 rows on (a grid has fewer than 2^32 threads)
+  const int passes = a.M >= 1024 * kPassRows ? 2 * (int)ceil_div(a.M, int64_t(1) << 24) : 1;
+  const int rows = kPassRows * passes;
   return by_width(a, [&](auto lanes, auto nv, auto vec) {
     balance_backward_kernel<decltype(lanes)::value, decltype(nv)::value, decltype(vec)::value>
         <<<(unsigned)ceil_div(a.M, rows), kThreads, 0, stream>>>(a, rows);

@@ -271,3 +271,29 @@ def test_balance_large_logits():
     bound = E / k * p * (ref["counts"] + (ref["counts"] * p).sum(1, keepdims=True))
     err = np.abs(got.cpu().numpy() - want)
     assert (err <= (2 * n + 4 + 4 + 10) * U * bound + 2.0 ** -120).all()
+
+
+def test_balance_most_rows():
+    """More rows than a grid of one thread for 8 of them could have threads (2^29)."""
+    M, E, k = 2**29 + 777, 2, 1
+    logits = torch.randn((M, E), device="cuda")
+    ids = torch.zeros((M, k), dtype=torch.int32, device="cuda")
+    ids[:M // 3] = 1
+    bufs = moe.balance_loss(logits, ids, moe.alloc_balance_buffers(M, E))
+    assert bufs.seq_tokens.tolist() == [M] and bufs.expert_counts.tolist() == [[M - M // 3, M // 3]]
+    gl = torch.full((1,), float(M), device="cuda")
+    grad = torch.full_like(logits, 7.0)
+    moe.balance_loss_backward(logits, k, bufs.expert_counts, bufs.seq_tokens, gl, grad_logits=grad)
+    counts = bufs.expert_counts.cpu().numpy()
+    for lo in (0, M // 2, M - 1000):
+        row = logits[lo:lo + 1000].double().cpu().numpy()
+        p = np.exp(row - row.max(1, keepdims=True))
+        p /= p.sum(1, keepdims=True)
+        w = float(M) * E / (k * float(M) ** 2)
+        want = w * p * (counts - (counts * p).sum(1, keepdims=True))
+        # c, T and E / (k T) are rounded to fp32 too: four roundings more than the small cases
+        n = 2 * row_roundings(row, E) + 4 + 4 + 10 + 4
+        bound = w * p * (counts + (counts * p).sum(1, keepdims=True))
+        assert (np.abs(grad[lo:lo + 1000].cpu().numpy() - want) <= n * U * bound).all()
+    step = 1 << 24
+    assert all(bool((grad[i:i + step] != 7.0).all()) for i in range(0, M, step))
