@@ -135,15 +135,31 @@ __device__ __forceinline__ Sequence sequence_of(const BalanceArgs& a, int t) {
 
 __device__ __forceinline__ int clamp_row(int v, int M) { return v < 0 ? 0 : (v > M ? M : v); }
 
-// Sum over the wave's rows (lanes l, l + Lanes, ...).
-template <int Lanes>
-__device__ __forceinline__ float across_rows(float v) {
-  if constexpr (Lanes == 16) {
-    const auto h = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = __uint_as_float(h[0]) + __uint_as_float(h[1]);
+// Sums of a wave's rows (lanes l, l + Lanes, ...) to out[expert]. Each exchange
+// takes two values and leaves one of them summed in either half of the lanes, a
+// quarter of the work of summing each value into every lane (the kernel
+// 11.5 us instead of 12.8 for [16384, 384], 27 instead of 31 for [32768, 1024]).
+__device__ __forceinline__ float half_sums32(float a, float b) {  // lanes 0..31: a's, 32..63: b's
+  const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  return __uint_as_float(h[0]) + __uint_as_float(h[1]);
+}
+__device__ __forceinline__ float half_sums16(float a, float b) {  // even 16 lanes: a's, odd 16: b's
+  const auto h = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  return __uint_as_float(h[0]) + __uint_as_float(h[1]);
+}
+template <int Lanes, int NV>
+__device__ __forceinline__ void join_rows(const float (&v)[4 * NV], float* out) {
+  const int lane = threadIdx.x & 63, l = lane % Lanes;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    if constexpr (Lanes == 16) {
+      const int q = (lane >> 5) + 2 * ((lane >> 4) & 1);
+      out[64 * j + 4 * l + q] = half_sums16(half_sums32(v[4 * j], v[4 * j + 1]), half_sums32(v[4 * j + 2], v[4 * j + 3]));
+    } else {
+      *(float2*)(out + 128 * j + 4 * l + 2 * (lane >> 5)) =
+          make_float2(half_sums32(v[4 * j], v[4 * j + 2]), half_sums32(v[4 * j + 1], v[4 * j + 3]));
+    }
   }
-  const auto g = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return __uint_as_float(g[0]) + __uint_as_float(g[1]);
 }
 
 constexpr int kSumThreads = 1024;
@@ -155,8 +171,9 @@ constexpr int kSumRows = kSumThreads / 16;  // rows of a forward pass at 16 lane
 // that 64 rows are in flight at once: with 4 waves and the next row prefetched
 // [16384, 384] took 13.8 us, bound by the loads' latency. The first row and the
 // first choices of the chunk are loaded before the sequence is looked up.
-// [16384, 384] with offsets and padding 13.1 us (25 MB: one pass, bound by the
-// latencies of that and of the join), [32768, 1024] 31 us (4.4 TB/s).
+// [16384, 384] with offsets and padding 11.5 us (25 MB: one pass, bound by the
+// latencies of that and of the join; 9.7 without exponentials, counts, join and
+// stores), [32768, 1024] 27 us (4.9 TB/s).
 template <int Lanes, int NV, bool Vec>
 __global__ __launch_bounds__(kSumThreads) void balance_rows_kernel(BalanceArgs a, int chunk_rows, float* psums,
                                                                    int32_t* pcounts, int32_t* ptokens,
@@ -224,14 +241,7 @@ __global__ __launch_bounds__(kSumThreads) void balance_rows_kernel(BalanceArgs a
     fetched = false;
     if (l == 0 && rows) atomicAdd(&live_rows, rows);
     // the wave's rows, then the waves
-#pragma unroll
-    for (int i = 0; i < 4 * NV; ++i) acc[i] = across_rows<Lanes>(acc[i]);
-    if ((tid & 63) < Lanes) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-        *(float4*)&sums[wave][4 * Lanes * j + 4 * l] =
-            make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
-    }
+    join_rows<Lanes, NV>(acc, sums[wave]);
     __syncthreads();
     const int64_t slot = (int64_t)blockIdx.x + s;
     float sum = 0.0f;
