@@ -72,7 +72,7 @@ enum {
     MOE_ERR_INVALID_ARG = -1, /* null pointer, negative size, misaligned pointer */
     MOE_ERR_UNSUPPORTED = -2, /* a size outside the limits above */
     MOE_ERR_CAPACITY = -3,    /* cap smaller than moe_route_align_capacity() */
-    MOE_ERR_WORKSPACE = -4,   /* workspace smaller than moe_w4a16_workspace_bytes() */
+    MOE_ERR_WORKSPACE = -4,   /* workspace smaller than the call's ..._workspace_bytes() */
     MOE_ERR_HIP = -5,         /* a HIP launch failed */
     MOE_ERR_SCRATCH = -6      /* batch too large for moe_w4a16_layer_noalloc's static scratch */
 };
