@@ -19,11 +19,8 @@
 // With r <= 128 each of them moves the wide side once and is bound by that
 // traffic (a copy reaches 5.2 TB/s read and written, a read 7), a small call by
 // the launches (3.6 us each), so the products are made exact where that is
-// free: bf16 operands
-// multiply exactly into fp32, and an fp32 factor (h, dh, an fp32 side) enters
-// as bf16 parts of 8 bits each, three (24 bits: all of fp32) where the result
-// is fp32, two (16 bits, 2^-17 relative against the 2^-8 of the result's own
-// rounding) where it is bf16.
+// free: bf16 operands multiply exactly into fp32, and an fp32 factor (h, dh, an
+// fp32 side) enters as three bf16 parts of 8 bits each, all 24 bits of fp32.
 #include <type_traits>
 
 #include "device_common.h"
@@ -43,8 +40,15 @@ __device__ __forceinline__ uint32_t bf16_bits(float v) {
 }
 __device__ __forceinline__ float bf16_value(uint32_t bits) { return __uint_as_float(bits << 16); }
 
+// Two fp32 values rounded to bf16, the first in the low half.
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)lo, (__bf16)hi});
+}
+
 // Eight fp32 values as NP bf16 parts, v = parts[0] + parts[1] + ...: each part
-// is the rounding of what the parts before it leave.
+// is the rounding of what the parts before it leave. Values are converted in pairs
+// and taken apart again: one by one the compiler converts each of them twice.
 template <int NP>
 __device__ __forceinline__ void split_parts(const float (&v)[8], bf16x8_t (&parts)[NP]) {
   float rest[8];
@@ -52,18 +56,15 @@ __device__ __forceinline__ void split_parts(const float (&v)[8], bf16x8_t (&part
   for (int i = 0; i < 8; ++i) rest[i] = v[i];
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
+    uint32_t d[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      parts[p][i] = (__bf16)rest[i];
-      rest[i] -= (float)parts[p][i];
+    for (int i = 0; i < 4; ++i) {
+      d[i] = bf16_pair(rest[2 * i], rest[2 * i + 1]);
+      rest[2 * i] -= bf16_value(d[i]);
+      rest[2 * i + 1] -= __uint_as_float(d[i] & 0xffff0000u);
     }
+    parts[p] = as_bf16x8(make_uint4(d[0], d[1], d[2], d[3]));
   }
-}
-
-// Two fp32 values rounded to bf16, the first in the low half.
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)lo, (__bf16)hi});
 }
 
 // Whether every lane of `live` holds the same key as its first one.
@@ -653,10 +654,24 @@ __device__ __forceinline__ void store4(TO* row, int n, int N, uint4 v) {
   }
 }
 
-// The tile's factor in LDS: the sums of the partial sums, scaled, as bf16 parts.
-template <int RC, int NP>
+// LDS of a workgroup: the factor as three bf16 parts, and a wave's 64 rows of b.
+// For bf16 results of ranks 33 to 64 b goes through LDS in two turns, half of its
+// ranks each, so that a CU holds three workgroups: rank 64, [7168] columns of 8192
+// rows 65 us and of 4096 rows 33.5, in one turn with two workgroups 72.5 and 32.4.
+// Up to rank 32 three fit either way, above 64 one does, and with fp32 results the
+// registers hold two.
+template <typename TO, int RC>
+struct UpShape {
+  static constexpr int kParts = 3;
+  static constexpr int kPitch = RC + 8;                                // of the factor's rows
+  static constexpr int kTurns = RC == 64 && sizeof(TO) == 2 ? 2 : 1;
+  static constexpr int kSeg = RC / 8 / kTurns;                         // 8-wide chunks of a row in a turn
+};
+
+// The tile's factor: the sums of the partial sums, scaled.
+template <typename TO, int RC>
 __device__ __forceinline__ void up_factor(const UpArgs& p, const Tile& sh, int n, uint16_t* lds) {
-  constexpr int kPitch = RC + 8;
+  using Shape = UpShape<TO, RC>;
   const int tid = threadIdx.x;
   const int rows = (n + kSub - 1) / kSub * kSub;
   const float scale = p.scales ? p.scales[sh.adapter] : 1.0f;
@@ -675,14 +690,14 @@ __device__ __forceinline__ void up_factor(const UpArgs& p, const Tile& sh, int n
     }
     float f[4] = {v.x * scale, v.y * scale, v.z * scale, v.w * scale};
 #pragma unroll
-    for (int q = 0; q < NP; ++q) {
+    for (int q = 0; q < Shape::kParts; ++q) {
       uint32_t bits[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         bits[e] = bf16_bits(f[e]);
         f[e] -= bf16_value(bits[e]);
       }
-      *(uint2*)(lds + (q * kLoraTile + t) * kPitch + j) = make_uint2(bits[0] | bits[1] << 16, bits[2] | bits[3] << 16);
+      *(uint2*)(lds + (q * kLoraTile + t) * Shape::kPitch + j) = make_uint2(bits[0] | bits[1] << 16, bits[2] | bits[3] << 16);
     }
   }
 }
@@ -699,18 +714,18 @@ constexpr int kUpCols = 64;  // columns of a wave
 // rows are consecutive in memory and go through the wave's own part of LDS, as
 // in down. What does not depend on the factor is loaded before it is made.
 // None: rows without an adapter, out = base.
-// Bound by reading the base and writing out, beside which b comes from L2:
-// [8192, 7168] bf16 of rank 64 58 us (4.1 TB/s, where copying in the same
-// pattern takes 35 to 42), [4096, 7168] 31 us, rank 16 [1999, 7168] 15 us; two
-// workgroups a CU instead of three took 38 us for the second.
+// Bound by reading the base and writing out, beside which b comes from L2 and the
+// matrix cores run: [8192, 7168] bf16 of rank 64 65 us (3.6 TB/s; 60.5 with a factor
+// of two parts, 16 bits, whose loss shows in a bf16 result that cancels), [4096,
+// 7168] 33.5 us, rank 16 [1999, 7168] 16 us.
 template <typename TO, int RC, bool Vec, bool Past, int NSUB, bool None = false>
 __device__ __forceinline__ void up_tile(const UpArgs& p, const Tile& sh, int n, uint16_t* lds, uint4* blds,
                                         int64_t (*offs)[kLoraTile]) {
-  constexpr int NP = sizeof(TO) == 4 ? 3 : 2;
+  using Shape = UpShape<TO, RC>;
+  constexpr int NP = Shape::kParts, kPitch = Shape::kPitch, kSeg = Shape::kSeg;
   constexpr int kChunks = RC / 8;                         // 8-wide chunks of a part
   constexpr int kSteps = (NP * kChunks + 3) / 4;          // 32-wide steps
   constexpr int kFrags = kChunks >= 4 ? kChunks / 4 : 1;  // different steps of b
-  constexpr int kPitch = RC + 8;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
   const uint16_t* b = p.b + (int64_t)sh.adapter * p.N * p.r;
   const int first = blockIdx.x % p.across * p.n_block;
@@ -731,8 +746,9 @@ __device__ __forceinline__ void up_tile(const UpArgs& p, const Tile& sh, int n, 
     if constexpr (None) return;
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
-      const int col = col0 + (i * 64 + lane) / kChunks;
-      braw[i] = load16<uint16_t, true>(b + (int64_t)(col < p.N ? col : p.N - 1) * p.r, (lane % kChunks) * 8, p.r);
+      const int col = col0 + (i % kSeg * 64 + lane) / kSeg;
+      braw[i] = load16<uint16_t, true>(b + (int64_t)(col < p.N ? col : p.N - 1) * p.r, (i / kSeg * kSeg + lane % kSeg) * 8,
+                                       p.r);
     }
   };
   auto load_base = [&](int ts, int col) {
@@ -746,26 +762,32 @@ __device__ __forceinline__ void up_tile(const UpArgs& p, const Tile& sh, int n, 
     for (int ts = 0; ts < NSUB; ++ts) load_base(ts, n0 + 4 * c);
   }
   if constexpr (!None) {
-    up_factor<RC, NP>(p, sh, n, lds);
+    up_factor<TO, RC>(p, sh, n, lds);
     __syncthreads();
   }
   auto columns = [&](auto more) {  // more: the wave has another group of columns, whose loads go out
     const int col = n0 + 4 * c;
     bf16x8_t bf[4][kFrags];
     if constexpr (!None) {
-      // row m of b, chunk k at slot k ^ (m / 4): the 16 rows 4 c + i of a fragment in different banks
+      // the 16 rows 4 c + i of a fragment in different banks: row m, chunk k at slot
+      // k ^ (m / 4), or in two turns the rows of a fragment together, and chunks
+      // exchanged by four rows of it
+      auto at = [](int m, int k) {
+        if constexpr (Shape::kTurns == 1) return m * kSeg + (k ^ ((m >> 2) & (kSeg - 1)));
+        else return ((m & 3) * 16 + ((m >> 2) ^ (m & 3))) * kSeg + (k ^ (m >> 4));
+      };
 #pragma unroll
-      for (int i = 0; i < kChunks; ++i) {
-        const int m = (i * 64 + lane) / kChunks;
-        blds[m * kChunks + ((lane % kChunks) ^ ((m >> 2) & (kChunks - 1)))] = braw[i];
+      for (int turn = 0; turn < Shape::kTurns; ++turn) {
+#pragma unroll
+        for (int i = 0; i < kSeg; ++i) blds[at((i * 64 + lane) / kSeg, lane % kSeg)] = braw[turn * kSeg + i];
+        wave_lds_fence();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int k = 0; k < kFrags / Shape::kTurns; ++k)
+            bf[i][turn * kFrags / Shape::kTurns + k] = as_bf16x8(blds[at(4 * c + i, (k * 4 + g) % kSeg)]);
+        wave_lds_fence();
       }
-      wave_lds_fence();
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int k = 0; k < kFrags; ++k)
-          bf[i][k] = as_bf16x8(blds[(4 * c + i) * kChunks + (((k * 4 + g) % kChunks) ^ (c & (kChunks - 1)))]);
-      wave_lds_fence();
     }
     const int next = n0 + kWaves * kUpCols;
     if constexpr (decltype(more)::value) load_b(next);
@@ -814,10 +836,9 @@ __device__ __forceinline__ void up_tile(const UpArgs& p, const Tile& sh, int n, 
 
 template <typename TO, int RC, bool Vec, bool Past>
 __global__ __launch_bounds__(kThreads, RC <= 64 ? 3 : 1) void lora_up_kernel(UpArgs p) {
-  constexpr int NP = sizeof(TO) == 4 ? 3 : 2;
   __shared__ __align__(16) Tile sh;
-  __shared__ __align__(16) uint16_t lds[NP * kLoraTile * (RC + 8)];
-  __shared__ uint4 blds[kWaves][kUpCols * RC / 8];
+  __shared__ __align__(16) uint16_t lds[UpShape<TO, RC>::kParts * kLoraTile * UpShape<TO, RC>::kPitch];
+  __shared__ uint4 blds[kWaves][kUpCols * UpShape<TO, RC>::kSeg];
   const int n = find_tile(p.tile, sh, blockIdx.x / p.across);
   if (n == 0) return;
   const bool none = sh.adapter == p.tile.L;

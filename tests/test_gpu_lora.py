@@ -377,3 +377,39 @@ def test_lora_backward_larger_than_the_cache():
     bare = moe.lora_backward(*many[:4], a, b, s)
     zero = moe.lora_backward(*many[:4], a, b, s, dx_base=torch.zeros_like(place))
     assert torch.equal(bare[0], zero[0])
+
+
+@pytest.mark.parametrize("r", [8, 16, 32, 40, 64, 72, 128])
+@pytest.mark.parametrize("f32", [False, True])
+def test_lora_expansion_keeps_all_bits(r, f32):
+    """h (forward) and dh (backward) reach the result with all 24 bits of fp32,
+    whatever the result's type. Three ranks hold v = p1 + p2 + p3 (three bf16
+    numbers of 8 bits each, so v has 24), -p1 and -p2, and the other weights make
+    every column their sum, p3. All terms are multiples of p3's last bit u, and any
+    of them add up to less than 2^24 u, so no order of the additions rounds: the
+    result is p3 exactly. With the last 8 bits of v lost it would be 0."""
+    M, K, N, L = 150, 64, 40, 3
+    rng = np.random.default_rng(r)
+    u = 2.0 ** -20
+    p3 = rng.integers(64, 128, M) * rng.choice([-1.0, 1.0], M) * u
+    p2 = rng.integers(64, 127, M) * 2.0 ** 8 * u
+    p1 = rng.integers(64, 127, M) * 2.0 ** 16 * u
+    pieces = np.stack([p1, p2, p3], 1)
+    assert (np.abs(pieces).sum(1) < 2.0 ** 24 * u).all()
+    ids = torch.from_numpy((np.arange(M) % L).astype(np.int32)).cuda()
+    mix = np.array([[1.0, 1.0, 1.0], [-1.0, 0.0, 0.0], [0.0, -1.0, 0.0]])  # the three ranks' values of the pieces
+    side = torch.float32 if f32 else torch.bfloat16
+
+    x, a, b = np.zeros((M, K)), np.zeros((L, r, K)), np.zeros((L, N, r))
+    x[:, :3], a[:, r - 3:, :3], b[:, :, r - 3:] = pieces, mix, 1.0
+    h = torch.empty((M, r), device="cuda")
+    out = moe.lora_forward(bf16(x).cuda(), ids, bf16(a).cuda(), bf16(b).cuda(),
+                           base=torch.zeros((M, N), dtype=side, device="cuda"), h=h)
+    np.testing.assert_array_equal(h.double().cpu().numpy()[:, r - 3:], pieces @ mix.T)
+    np.testing.assert_array_equal(out.double().cpu().numpy(), np.repeat(p3[:, None], N, 1))
+
+    g, a, b = np.zeros((M, N)), np.zeros((L, r, K)), np.zeros((L, N, r))
+    g[:, :3], b[:, :3, r - 3:], a[:, r - 3:] = pieces, mix.T, 1.0
+    dx, _, _ = moe.lora_backward(torch.from_numpy(g).to(side).cuda(), bf16(x).cuda(), ids, h, bf16(a).cuda(),
+                                 bf16(b).cuda())
+    np.testing.assert_array_equal(dx.double().cpu().numpy(), np.repeat(p3[:, None], K, 1))
