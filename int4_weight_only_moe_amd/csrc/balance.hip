@@ -165,6 +165,10 @@ __device__ __forceinline__ void join_rows(const float (&v)[4 * NV], float* out) 
 constexpr int kSumThreads = 1024;
 constexpr int kSumWaves = kSumThreads / 64;
 constexpr int kSumRows = kSumThreads / 16;  // rows of a forward pass at 16 lanes a row
+// Passes whose rows a lane adds in fp32. Longer chunks (from 2^20 rows on) add the
+// runs in fp64: equal rows round in the same direction at every addition, and one
+// run of 4096 additions was off by 4e-5.
+constexpr int kSumRun = 64;
 
 // One chunk of rows: for each sequence in it, the chunk's sums of
 // probabilities, counts and valid rows, to slot chunk + sequence. 16 waves, so
@@ -226,36 +230,44 @@ __global__ __launch_bounds__(kSumThreads) void balance_rows_kernel(BalanceArgs a
       const int e = chunk_ids[at];
       if (e >= 0 && e < E && (!a.valid || a.valid[r0 + at / (unsigned)k])) atomicAdd(&cnt[e], 1);
     }
-    float acc[4 * NV];
+    double total = 0.0;
+    for (int from = lo;;) {  // a run of rows
+      const int to = hi - from > kSumRun * kRows ? from + kSumRun * kRows : hi;
+      float acc[4 * NV];
 #pragma unroll
-    for (int i = 0; i < 4 * NV; ++i) acc[i] = 0.0f;
-    int rows = 0;
-    for (int t = lo + group; t < hi; t += kRows) {
-      if (!fetched || t != r0 + group) fetch(t, hi);
-      if (!live) continue;
-      ++rows;
-      const float inv = exp_row<Lanes>(v);
+      for (int i = 0; i < 4 * NV; ++i) acc[i] = 0.0f;
+      int rows = 0;
+      for (int t = from + group; t < to; t += kRows) {
+        if (!fetched || t != r0 + group) fetch(t, hi);
+        if (!live) continue;
+        ++rows;
+        const float inv = exp_row<Lanes>(v);
 #pragma unroll
-      for (int i = 0; i < 4 * NV; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
+        for (int i = 0; i < 4 * NV; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
+      }
+      fetched = false;
+      if (l == 0 && rows) atomicAdd(&live_rows, rows);
+      // the wave's rows, then the waves
+      join_rows<Lanes, NV>(acc, sums[wave]);
+      __syncthreads();
+      float sum = 0.0f;
+      if (tid < E) {
+#pragma unroll
+        for (int w = 0; w < kSumWaves; ++w) sum += sums[w][tid];
+      }
+      total += (double)sum;
+      from = to;
+      if (from >= hi) break;
+      __syncthreads();
     }
-    fetched = false;
-    if (l == 0 && rows) atomicAdd(&live_rows, rows);
-    // the wave's rows, then the waves
-    join_rows<Lanes, NV>(acc, sums[wave]);
-    __syncthreads();
     const int64_t slot = (int64_t)blockIdx.x + s;
-    float sum = 0.0f;
-    if (tid < E) {
-#pragma unroll
-      for (int w = 0; w < kSumWaves; ++w) sum += sums[w][tid];
-    }
     if (only) {  // all of the sequence is here
-      double part = tid < E ? (double)sum * (double)cnt[tid] : 0.0;
+      double part = tid < E ? total * (double)cnt[tid] : 0.0;
 #pragma unroll
       for (int d = 32; d; d >>= 1) part += __shfl_xor(part, d, 64);
       if ((tid & 63) == 0) parts[wave] = part;
       if (tid < E) {
-        a.prob_sums[(int64_t)s * E + tid] = sum;
+        a.prob_sums[(int64_t)s * E + tid] = (float)total;
         a.counts[(int64_t)s * E + tid] = cnt[tid];
       }
       __syncthreads();
@@ -270,7 +282,7 @@ __global__ __launch_bounds__(kSumThreads) void balance_rows_kernel(BalanceArgs a
       continue;
     }
     if (tid < E) {
-      psums[slot * E + tid] = sum;
+      psums[slot * E + tid] = (float)total;
       pcounts[slot * E + tid] = cnt[tid];
     }
     if (tid == 0) ptokens[slot] = live_rows;

@@ -297,3 +297,53 @@ def test_balance_most_rows():
         assert (np.abs(grad[lo:lo + 1000].cpu().numpy() - want) <= n * U * bound).all()
     step = 1 << 24
     assert all(bool((grad[i:i + step] != 7.0).all()) for i in range(0, M, step))
+
+
+def balance_on_device(logits, topk_ids, offsets, valid, S):
+    """Counts, sums of probabilities, tokens and loss in float64, some rows at a time (logits finite where valid)."""
+    M, E = logits.shape
+    k = topk_ids.shape[1]
+    counts = torch.zeros(S * E, dtype=torch.int64, device="cuda")
+    sums = torch.zeros((S, E), dtype=torch.float64, device="cuda")
+    tokens = torch.zeros(S, dtype=torch.int64, device="cuda")
+    for s in range(S):
+        for lo in range(offsets[s], offsets[s + 1], 1 << 20):
+            rows = slice(lo, min(lo + (1 << 20), offsets[s + 1]))
+            p = torch.softmax(logits[rows].double(), 1)
+            live = torch.ones(p.shape[0], dtype=torch.bool, device="cuda") if valid is None else valid[rows]
+            sums[s] += p[live].sum(0)
+            tokens[s] += live.sum()
+            counts[s * E:(s + 1) * E] += torch.bincount(topk_ids[rows][live].long().reshape(-1), minlength=E)
+    counts = counts.view(S, E)
+    loss = E / (k * tokens.double() ** 2) * (counts * sums).sum(1)
+    return counts, sums, tokens, loss
+
+
+@pytest.mark.parametrize("M,E,k,cuts,masked,spread", [
+    (2**26 + 777, 5, 1, (), False, 0.0),       # equal rows: every addition rounds the same way
+    (2**26 + 777, 5, 2, (0.3, 0.3, 0.9), True, 4.0),
+    (2**22 + 1, 100, 3, (0.5,), False, 0.0),
+    (600_001, 516, 4, (0.1, 0.77), True, 2.0),  # 32 lanes a row
+])
+def test_balance_sums_of_many_rows(M, E, k, cuts, masked, spread):
+    """A lane adds at most 64 rows in fp32, whatever the number of rows: 64
+    roundings, 2 to join a wave's rows, 15 its waves, and two to fp32 (a chunk's
+    sum, the result); the longer sums are fp64. The rows of spread s differ by at
+    most s, and the loss is rounded once more."""
+    g = torch.Generator(device="cuda").manual_seed(M + E)
+    logits = torch.rand((M, E), device="cuda", generator=g).mul_(spread)
+    ids = torch.randint(0, E, (M, k), device="cuda", generator=g, dtype=torch.int32)
+    S = len(cuts) + 1
+    off = [0, *[int(c * M) for c in cuts], M]
+    valid = torch.rand(M, device="cuda", generator=g) > 0.1 if masked else None
+    want = balance_on_device(logits, ids, off, valid, S)
+    if masked:
+        logits[~valid] = float("nan")
+    bufs = moe.balance_loss(logits, ids, moe.alloc_balance_buffers(M, E, S),
+                            torch.tensor(off, dtype=torch.int32, device="cuda") if S > 1 else None, valid)
+    assert torch.equal(bufs.expert_counts.long(), want[0]) and torch.equal(bufs.seq_tokens.long(), want[2])
+    n = spread + 6 + 4 * (-(-E // 64)) + 4 + 64 + 2 + 15 + 2
+    off_by = ((bufs.prob_sums.double() - want[1]).abs() / want[1].clamp(min=1e-30)).max().item()
+    loss_off = ((bufs.loss.double() - want[3]).abs() / want[3].clamp(min=1e-30)).nan_to_num(0.0).max().item()
+    print(f"sums off by {off_by / U:.1f} roundings, loss by {loss_off / U:.1f}, of {n:.0f}")
+    assert off_by <= n * U and loss_off <= (n + 1) * U
