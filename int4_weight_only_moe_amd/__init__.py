@@ -224,15 +224,21 @@ def lora_backward(grad_out: torch.Tensor, x: torch.Tensor, adapter_ids: torch.Te
                   workspace: torch.Tensor | None = None, stream=None) -> tuple:
     """Gradients of lora_forward: (dx bf16 [M, K] = dx_base + the adapters'
     part, grad_a fp32 like lora_a, grad_b fp32 like lora_b). need_dx=False
-    leaves dx out (None). grads: buffers of an earlier call to write into."""
-    if grads is None:
+    leaves dx out (None). grads: buffers of an earlier call to write into; one
+    that is None there is allocated if it is needed."""
+    dx, grad_a, grad_b = (None, None, None) if grads is None else grads
+    if not need_dx:
+        dx = None
+    if (need_dx and dx is None) or grad_a is None or grad_b is None:
         with _memory_of(stream, x.device):
-            grads = (torch.empty(x.shape, dtype=torch.bfloat16, device=x.device) if need_dx else None,
-                     torch.empty(lora_a.shape, dtype=torch.float32, device=x.device),
-                     torch.empty(lora_b.shape, dtype=torch.float32, device=x.device))
-    dx, grad_a, grad_b = grads
+            if need_dx and dx is None:
+                dx = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+            if grad_a is None:
+                grad_a = torch.empty(lora_a.shape, dtype=torch.float32, device=x.device)
+            if grad_b is None:
+                grad_b = torch.empty(lora_b.shape, dtype=torch.float32, device=x.device)
     if workspace is None:
         workspace = _lora_workspace(x, lora_a, lora_b, True, stream)
     moe_lora_backward(grad_out, x, adapter_ids, h, lora_a, lora_b, grad_a, grad_b, workspace, scales=scales, dx=dx,
                       dx_base=dx_base, stream=stream)
-    return grads
+    return dx, grad_a, grad_b

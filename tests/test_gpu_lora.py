@@ -413,3 +413,22 @@ def test_lora_expansion_keeps_all_bits(r, f32):
     dx, _, _ = moe.lora_backward(torch.from_numpy(g).to(side).cuda(), bf16(x).cuda(), ids, h, bf16(a).cuda(),
                                  bf16(b).cuda())
     np.testing.assert_array_equal(dx.double().cpu().numpy(), np.repeat(p3[:, None], K, 1))
+
+
+def test_lora_backward_buffers_and_need_dx():
+    """need_dx decides about dx, whatever buffers the caller passes: one that is there is left
+    as it was without it, one that is missing is allocated with it."""
+    M, L, K, N, r = 40, 2, 64, 48, 8
+    c = Case(M, L, K, N, r, False, "mixed", seed=62)
+    gids, x, a, b, dout = torch.from_numpy(c.ids).cuda(), c.x.cuda(), c.a.cuda(), c.b.cuda(), c.dout.cuda()
+    h = torch.empty((M, r), device="cuda")
+    moe.lora_forward(x, gids, a, b, h=h)
+    want = moe.lora_backward(dout, x, gids, h, a, b)
+    kept = (torch.full_like(x, 7.0), torch.zeros_like(want[1]), torch.zeros_like(want[2]))
+    got = moe.lora_backward(dout, x, gids, h, a, b, need_dx=False, grads=kept)
+    assert got[0] is None and got[1] is kept[1] and got[2] is kept[2] and (kept[0] == 7.0).all()
+    assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+    more = moe.lora_backward(dout, x, gids, h, a, b, grads=got)  # those of a call without dx
+    assert torch.equal(more[0], want[0]) and more[1] is kept[1] and more[2] is kept[2]
+    again = moe.lora_backward(dout, x, gids, h, a, b, grads=kept)
+    assert all(p is q for p, q in zip(again, kept)) and torch.equal(kept[0], want[0])
