@@ -117,3 +117,36 @@ def test_lora_many_tiles_of_wide_rows(M, r, N, f32):
 @pytest.mark.parametrize("M,f32", [(37, True), (150, False), (300, True), (520, False)])
 def test_lora_every_rank(r, M, f32):
     check(Case(M, 3, 136, 72 if r % 16 else 75, r, f32, "mixed", seed=73))
+
+
+def test_lora_many_rows_exact():
+    """Tiles past 65535 of rows that have an adapter. All values are small whole
+    numbers and every sum of magnitudes stays below 2^24, so every result is exact
+    in any order (those in bf16 are at most 256): a tile left out or taken twice shows."""
+    M, L, K, N, r = 4_300_000, 2, 8, 8, 8
+    g = torch.Generator(device="cuda").manual_seed(5)
+
+    def small(*shape):
+        return torch.randint(-1, 2, shape, device="cuda", generator=g)
+
+    x, dout, a, b = small(M, K), small(M, N), small(L, r, K), small(L, N, r)
+    gids = torch.randint(0, L, (M,), device="cuda", generator=g, dtype=torch.int32)
+    gids[torch.randint(0, M, (500,), device="cuda", generator=g)] = -1
+    assert int((gids >= 0).sum()) > 64 * 65536 and bool((gids == L - 1).any())
+    bf = torch.bfloat16
+    h = torch.empty((M, r), device="cuda")
+    base = torch.ones((M, N), device="cuda")
+    out = moe.lora_forward(x.to(bf), gids, a.to(bf), b.to(bf), base=base, h=h)
+    dx, da, db = moe.lora_backward(dout.float(), x.to(bf), gids, h, a.to(bf), b.to(bf))
+    x, dout, a, b = x.double(), dout.double(), a.double(), b.double()
+    for i in range(L):
+        rows = (gids == i).nonzero()[:, 0]
+        wh, dh = x[rows] @ a[i].T, dout[rows] @ b[i]
+        assert torch.equal(h[rows].double(), wh)
+        assert torch.equal(out[rows].double(), 1 + wh @ b[i].T)
+        assert torch.equal(dx[rows].double(), dh @ a[i])
+        for got, p, q in ((da[i], dh, x[rows]), (db[i], dout[rows], wh)):
+            assert (p.abs().T @ q.abs()).max() < 2 ** 24
+            assert torch.equal(got.double(), p.T @ q)
+    none = (gids < 0).nonzero()[:, 0]
+    assert (out[none] == 1).all() and (dx[none] == 0).all() and (h[none] == 0).all()
