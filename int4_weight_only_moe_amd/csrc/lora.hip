@@ -16,11 +16,12 @@
 //   join    backward: dh, the sum of its splits, as it is and rank-major, and
 //           s h rank-major (the transposed weights are made beside the grouping);
 //   outer   sums rows' outer products (dA, dB), reduce joins what was cut.
-// With r <= 128 each of them moves the wide side once and is bound by that
-// traffic (a copy reaches 5.2 TB/s read and written, a read 7), a small call by
-// the launches (3.6 us each), so the products are made exact where that is
-// free: bf16 operands multiply exactly into fp32, and an fp32 factor (h, dh, an
-// fp32 side) enters as three bf16 parts of 8 bits each, all 24 bits of fp32.
+// With r <= 128 each of them moves the wide side once, and that traffic is its
+// floor (a copy reaches 5.2 TB/s read and written, a read 7); a small call is bound
+// by its launches (one follows another every 3.6 us). The matrix cores have room,
+// so the products are made exact: bf16 operands multiply exactly into fp32, and an
+// fp32 factor (h, dh, an fp32 side) enters as three bf16 parts of 8 bits each, all
+// 24 bits of fp32.
 #include <type_traits>
 
 #include "device_common.h"
@@ -193,8 +194,11 @@ __device__ __forceinline__ void transpose_weights(const GroupArgs& g, const Tran
 // adapter of a step, so rows of one adapter in a run cost no more than mixed
 // ones), the counts become each wave's first positions, and a second walk
 // places the rows. Up to 8192 rows are read once. Bound by the latency of its
-// passes: 6.4 us for 8192 rows, with the weights' transposition beside it (rank
-// 64, [7168] both sides) too.
+// passes: 6.5 us for 8192 rows, with the weights' transposition beside it (rank
+// 64, [7168] both sides) too. One workgroup whatever the number of rows, so it
+// grows with them: 23 us for 32768 rows in runs, 44 for 65536 (86 if the 64
+// adapters are mixed), 1.3 ms for 2^20; the other workgroups' own reading of the ids
+// does not show beside that.
 __global__ __launch_bounds__(kGroupThreads, 8) void lora_group_kernel(GroupArgs p, TransposeArgs weights) {
   __shared__ __align__(16) int cnt[kGroupWaves][kMaxKeys];
   __shared__ int off[kMaxKeys + 1], rows_of[kMaxKeys];
@@ -948,11 +952,14 @@ constexpr int kPiece = 1024;  // positions whose rows are in LDS at a time
 // chunk go to the output, those of one that crosses the chunk's start or end to
 // slots 2 c or 2 c + 1, which the reduce kernel adds in order. Ranks above 64
 // are further workgroups, eight apart: on the same XCD, whose L2 has the columns.
-// Bound by the reading of both sides: x and grad_out of [8192, 7168], rank 64,
-// 68 us (3.5 TB/s); [1999, 7168] and [1999, 2048] of rank 16 12 us. One wave or
-// two a SIMD, loads one to three steps ahead and 32 ranks a wave or 64 were all
-// within 15 % of each other. An fp32 side enters as three parts, of whose
-// products with the factor's three the six above 2^-24 are taken.
+// x and grad_out of [8192, 7168], rank 64, 68 us: their 235 MB at 3.5 TB/s, where a
+// read reaches 7. Beside them come 12 KB of factor parts from L2 for each 8 KB of a
+// side (rank 64: 352 MB), and the two waves of a rank pair load the same side; one
+// wave or two a SIMD, loads one to three steps ahead and 32 ranks a wave or 64 leave
+// that as it is and were within 15 % of each other. [1999, 7168] and [1999, 2048]
+// of rank 16 13 us. An fp32 side enters as three parts, of whose products with the
+// factor's three all are taken but the last with the last (2^-32 of the whole; a
+// part is up to 2^-8 of the one before it, and fp32 rounds a product by 2^-24).
 template <typename TU, int JT, int H, bool VecU, bool RankMinor>
 __device__ __forceinline__ void outer_block(const OuterArgs& p, const OuterSide& side, int block,
                                             f32x4_t (*joined)[8 * JT][64], int64_t* offs) {
@@ -1020,7 +1027,9 @@ __device__ __forceinline__ void outer_block(const OuterArgs& p, const OuterSide&
         mac(uf[0], 2);
         mac(uf[1], 0);
         mac(uf[1], 1);
+        mac(uf[1], 2);
         mac(uf[2], 0);
+        mac(uf[2], 1);
       } else {
         // 16-bit element i of rows 2m and 2m + 1
         const uint32_t sel = (i & 1) ? 0x07060302u : 0x05040100u;

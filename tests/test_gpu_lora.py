@@ -432,3 +432,24 @@ def test_lora_backward_buffers_and_need_dx():
     assert torch.equal(more[0], want[0]) and more[1] is kept[1] and more[2] is kept[2]
     again = moe.lora_backward(dout, x, gids, h, a, b, grads=kept)
     assert all(p is q for p, q in zip(again, kept)) and torch.equal(kept[0], want[0])
+
+
+@pytest.mark.parametrize("swap", [False, True])
+def test_lora_weight_gradient_keeps_all_bits(swap):
+    """grad_b of fp32 gradients: u v with u = 1 + 2^-8 (two bf16 parts) and
+    v = 1 + 2^-8 - 2^-17 (three), in either role. Further rows take every product
+    of their parts away again but the one of the smaller parts, -2^-25, which fp32
+    holds beside nothing else: all terms are multiples of it, and what is left of
+    each pair of parts is below 2^-6."""
+    u, v = (1.0, 2.0 ** -8), (1.0, 2.0 ** -8, -2.0 ** -17)
+    rows = [(sum(u), sum(v))] + [(-p, q) for p in u for q in v if (p, q) != (u[1], v[2])]
+    if swap:
+        rows = [(q, p) for p, q in rows]
+    M, L, K, N, r = len(rows), 1, 64, 40, 16
+    side = torch.tensor(rows, dtype=torch.float64)
+    assert (side.float().double() == side).all()
+    dout = side[:, :1].float().expand(M, N).contiguous().cuda()
+    h = side[:, 1:].float().expand(M, r).contiguous().cuda()
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    _, _, db = moe.lora_backward(dout, z(M, K), torch.zeros(M, dtype=torch.int32, device="cuda"), h, z(L, r, K), z(L, N, r))
+    assert (db == -2.0 ** -25).all()
