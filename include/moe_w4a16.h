@@ -370,8 +370,8 @@ int moe_mxfp4_layer(const float* logits, const uint16_t* x_bf16, int32_t M, int3
  *               (dropped choices) are not counted.
  *   seq_offsets int32 [S + 1], ascending: sequence s has the rows
  *               [seq_offsets[s], seq_offsets[s + 1]); NULL (S = 1 only): all
- *               rows. Rows of no sequence are not read, and their rows of
- *               grad_logits are left as they were.
+ *               rows. What the logits of rows of no sequence hold is not used, and
+ *               their rows of grad_logits are left as they were.
  *   row_valid   uint8 [M] or NULL: rows with 0 (padding) are not counted, what
  *               their logits hold is not used; their rows of grad_logits are 0.
  *   expert_counts int32 [S, E], prob_sums fp32 [S, E], seq_tokens int32 [S]
@@ -425,8 +425,11 @@ int moe_balance_loss_backward(const float* logits, int32_t M, int32_t E, int32_t
  *               With M = 0 too: zeros.
  *   workspace   >= moe_lora_workspace_bytes(M, L, K, N, rank, backward) bytes;
  *               contents on entry do not matter. One for a larger M serves
- *               smaller ones, a backward call's serves the forward call.
- * out and dx are accumulated in fp32 and rounded once; h and dh stay fp32. A
+ *               smaller ones, a backward call's serves the forward call. A
+ *               backward call's has room for all L adapters once more
+ *               (2 * L * rank * (K + N) bytes), whichever have rows.
+ * out and dx are accumulated in fp32 and rounded once; h and dh are fp32 and
+ * enter every result with all their bits. A
  * row that is not finite (or whose adapter is not) makes its own row of the
  * results not finite, and its adapter's gradients.
  * Results are identical on every call.
