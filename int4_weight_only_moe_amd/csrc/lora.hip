@@ -659,17 +659,19 @@ __device__ __forceinline__ void store4(TO* row, int n, int N, uint4 v) {
 }
 
 // LDS of a workgroup: the factor as three bf16 parts, and a wave's 64 rows of b.
-// For bf16 results of ranks 33 to 64 b goes through LDS in two turns, half of its
-// ranks each, so that a CU holds three workgroups: rank 64, [7168] columns of 8192
-// rows 65 us and of 4096 rows 33.5, in one turn with two workgroups 72.5 and 32.4.
-// Up to rank 32 three fit either way, above 64 one does, and with fp32 results the
-// registers hold two.
+// For bf16 results b goes through LDS in turns of 32 ranks each, so that a CU holds
+// three workgroups up to rank 64 and two above: rank 64, [7168] columns of 8192
+// rows 65 us and of 4096 rows 33.5, in one turn with two workgroups 72.5 and 32.4;
+// rank 128 of 4096 rows 47.5, in one turn with one workgroup 57. With fp32 results
+// the registers hold two and one (as two workgroups rank 128 of 2048 rows of [7165]
+// takes 92 us instead of 67), for which one turn leaves room.
 template <typename TO, int RC>
 struct UpShape {
   static constexpr int kParts = 3;
-  static constexpr int kPitch = RC + 8;                                // of the factor's rows
-  static constexpr int kTurns = RC == 64 && sizeof(TO) == 2 ? 2 : 1;
-  static constexpr int kSeg = RC / 8 / kTurns;                         // 8-wide chunks of a row in a turn
+  static constexpr int kPitch = RC + 8;                                        // of the factor's rows
+  static constexpr int kTurns = sizeof(TO) == 2 && RC > 32 ? RC / 32 : 1;
+  static constexpr int kSeg = RC / 8 / kTurns;                                 // 8-wide chunks of a row in a turn
+  static constexpr int kWorkgroups = RC <= 64 ? 3 : (sizeof(TO) == 2 ? 2 : 1);  // a CU, aimed at
 };
 
 // The tile's factor: the sums of the partial sums, scaled.
@@ -721,7 +723,7 @@ constexpr int kUpCols = 64;  // columns of a wave
 // Bound by reading the base and writing out, beside which b comes from L2 and the
 // matrix cores run: [8192, 7168] bf16 of rank 64 65 us (3.6 TB/s; 60.5 with a factor
 // of two parts, 16 bits, whose loss shows in a bf16 result that cancels), [4096,
-// 7168] 33.5 us, rank 16 [1999, 7168] 16 us.
+// 7168] 33.5 us, of rank 128 47.5, rank 16 [1999, 7168] 16 us.
 template <typename TO, int RC, bool Vec, bool Past, int NSUB, bool None = false>
 __device__ __forceinline__ void up_tile(const UpArgs& p, const Tile& sh, int n, uint16_t* lds, uint4* blds,
                                         int64_t (*offs)[kLoraTile]) {
@@ -774,7 +776,7 @@ __device__ __forceinline__ void up_tile(const UpArgs& p, const Tile& sh, int n, 
     bf16x8_t bf[4][kFrags];
     if constexpr (!None) {
       // the 16 rows 4 c + i of a fragment in different banks: row m, chunk k at slot
-      // k ^ (m / 4), or in two turns the rows of a fragment together, and chunks
+      // k ^ (m / 4), or in several turns the rows of a fragment together, and chunks
       // exchanged by four rows of it
       auto at = [](int m, int k) {
         if constexpr (Shape::kTurns == 1) return m * kSeg + (k ^ ((m >> 2) & (kSeg - 1)));
@@ -839,7 +841,7 @@ __device__ __forceinline__ void up_tile(const UpArgs& p, const Tile& sh, int n, 
 }
 
 template <typename TO, int RC, bool Vec, bool Past>
-__global__ __launch_bounds__(kThreads, RC <= 64 ? 3 : 1) void lora_up_kernel(UpArgs p) {
+__global__ __launch_bounds__(kThreads, (UpShape<TO, RC>::kWorkgroups)) void lora_up_kernel(UpArgs p) {
   __shared__ __align__(16) Tile sh;
   __shared__ __align__(16) uint16_t lds[UpShape<TO, RC>::kParts * kLoraTile * UpShape<TO, RC>::kPitch];
   __shared__ uint4 blds[kWaves][kUpCols * UpShape<TO, RC>::kSeg];
@@ -1208,7 +1210,7 @@ hipError_t launch_up(UpArgs p, bool out_f32, bool past, int tiles, hipStream_t s
   // blocks of a tile are neighbours, so that together they read whole rows
   // (rank 16, [1999, 7168]: 24 us with the tiles as neighbours, 15 so)
   const int64_t cols = ceil_div(p.N, kWaves * kUpCols);
-  int64_t across = 256 * (p.r <= 64 ? 3 : 1) / tiles;
+  int64_t across = 256 * (p.r <= 64 ? 3 : (out_f32 ? 1 : 2)) / tiles;
   across = across < 1 ? 1 : (across > cols ? cols : across);
   p.n_block = (int)(ceil_div(cols, across) * kWaves * kUpCols);
   p.across = (int)ceil_div(p.N, p.n_block);
