@@ -79,8 +79,10 @@ __device__ __forceinline__ void load_row(const float* __restrict__ row, int E, i
 // 1 / their sum. A row of nothing but -inf has none: 0. A NaN or +inf gives NaN.
 // exp(v - m) = 2^(v log2(e) - m log2(e)) in one fused step: the rounding of
 // m log2(e), at most 2^-4 for |m| < 2^20, is the same factor for the whole row
-// and goes out with the sum. A larger |m| would make that factor large (it
-// overflows from 2^30 on): there the difference is taken first.
+// and goes out with the sum. What stays is the step's own rounding (a difference
+// taken first would have the like) and the constant's, |v - m| 2^-26: in fp32 steps
+// |v - m| at most. A larger |m| would make the common factor large (it overflows
+// from 2^30 on): there the difference is taken first.
 template <int Lanes, int N>
 __device__ __forceinline__ float exp_row(float (&v)[N]) {
   constexpr float kLog2e = 1.4426950408889634f;

@@ -1363,7 +1363,7 @@ hipError_t launch_lora_forward(const LoraArgs& a, hipStream_t stream) {
   if (err != hipSuccess) return err;
   // up's workgroups each add their tile's splits again; where that is more than
   // the rest of what they read (64 rows of a few hundred columns), a launch of
-  // its own does it once (4096 rows of rank 64: 5 + 31 us instead of 61)
+  // its own does it once (4096 rows of rank 64: 5 + 33 us instead of more than 60)
   if (o.splits * a.r > 128 && !o.small) {
     float* h = a.h ? a.h : (float*)(a.ws + o.h_off);
     const int64_t size = (int64_t)a.M * a.r;
