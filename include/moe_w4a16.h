@@ -429,7 +429,8 @@ int moe_balance_loss_backward(const float* logits, int32_t M, int32_t E, int32_t
  *               backward call's has room for all L adapters once more
  *               (2 * L * rank * (K + N) bytes), whichever have rows.
  * out and dx are accumulated in fp32 and rounded once; h and dh are fp32 and
- * enter every result with all their bits. A
+ * enter every result with all their bits (from a magnitude of 2^-102 up; fp32
+ * values beyond the largest finite bf16, 3.389e38, count as not finite). A
  * row that is not finite (or whose adapter is not) makes its own row of the
  * results not finite, and its adapter's gradients.
  * Results are identical on every call.
