@@ -1,5 +1,5 @@
-"""Low-rank adapters: sizes that take the kernels' less common ways, all on one
-checker against float64 on the device.
+"""Low-rank adapters: sizes that take the kernels' less common ways, all
+compared with float64 on the device.
 
 Tolerances are counted as in test_gpu_lora.py; h and dh reach every result with
 all their bits, so a result in bf16 adds its own half step, 2^-8, and nothing
