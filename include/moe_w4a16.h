@@ -56,7 +56,9 @@
  * scale per 32 input channels.
  *
  * Operators beside the layer (moe_balance_*, moe_lora_* at the end): what
- * trains the router and adapts the frozen weights to a task or a request.
+ * trains the router and adapts the frozen weights to a task or a request; and
+ * what stands between the layer and the rest of a model (moe_route_scored*,
+ * moe_add_rms_norm*, moe_grad_*).
  */
 #ifndef MOE_W4A16_H
 #define MOE_W4A16_H
@@ -453,6 +455,147 @@ int moe_lora_backward(const void* grad_out, int64_t ld_grad_out, int32_t out_dty
                       int32_t N, int32_t rank, const uint16_t* a_bf16, const uint16_t* b_bf16, const float* scales,
                       const uint16_t* dx_base, int64_t ld_dx_base, uint16_t* dx, int64_t ld_dx, float* grad_a,
                       float* grad_b, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * ---- Routing by scores -----------------------------------------------------
+ * moe_route_align with the choices that other routers make: scores of all
+ * experts, a bias that balances the choice without entering the weights,
+ * experts in groups, weights that are renormalised or not, and scaled. For a
+ * token's logits l:
+ *   s[e] = softmax(l)[e] over the E experts (MOE_SCORE_SOFTMAX), or
+ *          1 / (1 + exp(-l[e])) (MOE_SCORE_SIGMOID);
+ *   c[e] = s[e] + bias[e];
+ *   groups: the experts are n_groups runs of E / n_groups. A group's score is
+ *          the sum of its group_top (1 or 2) highest c; only experts of the
+ *          top_groups groups of the highest scores are chosen from (equal
+ *          scores: the lower group);
+ *   topk_ids: the top_k of these experts with the highest c, highest first
+ *          (equal c: the lower expert). Without a bias that is the order of the
+ *          logits;
+ *   topk_weights[j] = scale * s[e_j], or with renormalise scale * s[e_j] / sum
+ *          of the kept s (softmax: the softmax over the kept logits; sigmoid:
+ *          the sum plus 1e-20).
+ * The choice is that of c in fp64, however close two experts are.
+ *
+ *   logits      fp32 [M, E]. An expert whose logit or bias is -inf is absent:
+ *               never chosen, and a group of none but such is never chosen
+ *               either (a group score leaves them out). Slots that no expert
+ *               is left for have id -1 and weight 0, which the grouping, the
+ *               layer, the balance loss and the backward call leave out. NaN
+ *               counts as the highest value.
+ *   bias        fp32 [E] or NULL.
+ *   row_valid   uint8 [M] or NULL: all slots of rows with 0 (padding) are -1,
+ *               what their logits hold is not used.
+ *   grouping outputs as moe_route_align's, whole: sorted_token_ids past the
+ *               padded total is M*top_k, block_expert_ids there -1 (all cap and
+ *               cap / block_m entries are written). All four NULL: none are
+ *               wanted; block_m and cap are then not used.
+ * Limits: those of moe_route_align; E a multiple of n_groups, 1 <= n_groups <=
+ * 64, 1 <= top_groups <= n_groups, top_k <= top_groups * E / n_groups,
+ * group_top <= E / n_groups. Results are identical on every call.
+ *
+ * moe_route_scored_backward: the logits' gradient from the weights'
+ * (grad_weights fp32 [M, top_k]); the choice and the bias have none:
+ *   softmax:              s[e] * (g[e] - sum_i g[i] s[i]), g[e_j] = scale * grad_weights[j], else 0
+ *   softmax, renormalised: the same with the softmax over the kept logits
+ *   sigmoid:              g[j] s (1 - s) at e_j
+ *   sigmoid, renormalised: s (1 - s) / S * (g[j] - sum_i g[i] s[i] / S) at e_j, S the sum plus 1e-20
+ * plus grad_base (fp32 [M, E], or NULL: zeros), for instance the balance
+ * loss's gradient. grad_base may be grad_logits: it is then added to in place.
+ * topk_ids are the forward's, those of a row distinct; entries outside [0, E)
+ * are left out, a row of none but such has no gradient whatever its logits.
+ */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+int moe_route_scored(const float* logits, int32_t M, int32_t E, int32_t top_k, int32_t scoring, const float* bias,
+                     int32_t n_groups, int32_t top_groups, int32_t group_top, int32_t renormalise, float scale,
+                     const uint8_t* row_valid, int32_t block_m, int32_t* topk_ids, float* topk_weights,
+                     int32_t* sorted_token_ids, int32_t* block_expert_ids, int32_t* expert_offsets,
+                     int32_t* num_tokens_post_pad, int64_t cap, void* stream);
+int moe_route_scored_backward(const float* logits, int32_t M, int32_t E, int32_t top_k, int32_t scoring,
+                              int32_t renormalise, float scale, const int32_t* topk_ids, const float* grad_weights,
+                              const float* grad_base, float* grad_logits, void* stream);
+
+/*
+ * ---- Root-mean-square norm with the residual's addition ---------------------
+ * What stands before the layer: the residual stream takes the last sublayer's
+ * output (moe_w4a16_forward's, for instance) and is normalised into the next
+ * one's x. For each row
+ *   h = x + residual, rounded to the stream's type
+ *   r = 1 / sqrt(mean(h^2) + eps)
+ *   out = bf16(h * r * weight), rounded once
+ *   out8 = e4m3(y / s), y = h * r * weight unrounded, s = max(max |y| / 448, 2^-126)
+ *          in fp32 over quant_group columns (out8 is what y / s rounds to in
+ *          exact arithmetic: nearest, ties to even).
+ *
+ *   x           bf16 [M, N], row stride ldx (elements), or NULL: 0.
+ *   residual    [M, N] of res_dtype (bf16 or fp32), or NULL: 0 (h = x; res_dtype
+ *               bf16). Not both NULL.
+ *   residual_out [M, N] of res_dtype: h, or NULL. May be the same matrix as
+ *               residual (in place), or as x where that has its type.
+ *   weight      bf16 [N].
+ *   out_bf16    bf16 [M, N], or NULL. May be the same matrix as x.
+ *   out8_e4m3   uint8 [M, N] of OCP e4m3 values, scales fp32 [M, N / quant_group]
+ *               (contiguous), or both NULL. quant_group 32, 64 or 128, a divisor
+ *               of N, or N (a scale a row).
+ *   rstd        fp32 [M]: r, for the backward call, or NULL.
+ * At least one of out_bf16 and out8_e4m3. A row that holds NaN is NaN, one that
+ * holds an infinity has r = 0.
+ * Sums are fp64. Results are identical on every call.
+ *
+ * moe_add_rms_norm_backward, from grad_out (bf16 [M, N]):
+ *   n = h * r, u = weight * grad_out
+ *   grad_h = grad_residual + r * (u - n * mean(u * n))     (of x and of residual alike)
+ *   grad_weight = sum over the rows of grad_out * n
+ *   h           the forward's residual_out (or x, where there was no residual).
+ *   grad_residual [M, N] of res_dtype, what reaches h beside the norm, or NULL.
+ *   grad_h      [M, N] of res_dtype; may be the same matrix as grad_residual
+ *               or, where the type is the same, as grad_out or h; or NULL.
+ *   grad_weight fp32 [N], every element written (M = 0: zeros), or NULL.
+ *   workspace   >= moe_add_rms_norm_workspace_bytes(M, N) bytes, 16-byte
+ *               aligned; contents on entry do not matter. One for a larger M
+ *               serves smaller ones. Not used (may be NULL) without grad_weight.
+ * All matrices need their elements' alignment only (16-byte aligned rows of a
+ * multiple of 8 elements are faster). Other overlaps of buffers are not allowed.
+ * Limits: 1 <= N <= 32768, M <= 2^24; eps >= 0 and finite.
+ */
+int moe_add_rms_norm(const uint16_t* x_bf16, int64_t ldx, const void* residual, int64_t ld_residual, int32_t res_dtype,
+                     int32_t M, int32_t N, const uint16_t* weight_bf16, double eps, void* residual_out,
+                     int64_t ld_residual_out, uint16_t* out_bf16, int64_t ld_out, uint8_t* out8_e4m3, int64_t ld_out8,
+                     float* scales, int32_t quant_group, float* rstd, void* stream);
+int64_t moe_add_rms_norm_workspace_bytes(int32_t M, int32_t N); /* host; -1 on invalid sizes */
+int moe_add_rms_norm_backward(const uint16_t* grad_out_bf16, int64_t ld_grad_out, const void* h, int64_t ld_h,
+                              int32_t res_dtype, const float* rstd, int32_t M, int32_t N, const uint16_t* weight_bf16,
+                              const void* grad_residual, int64_t ld_grad_residual, void* grad_h, int64_t ld_grad_h,
+                              float* grad_weight, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * ---- Global gradient norm and clipping --------------------------------------
+ * Over n gradients at once (the adapters', the router's, the norms'):
+ *   sumsq = sum of the squares of all elements, fp64
+ *   norm = sqrt(sumsq);  out_i = grad_i * (norm > max_norm ? max_norm / norm : 1)
+ * moe_grad_sumsq writes sumsq; a data-parallel job may sum it over its ranks
+ * before moe_grad_clip scales. A sum that is not finite scales nothing (norm
+ * says so: leave the step out).
+ *
+ *   grads, outs, sizes, dtypes: host arrays of n entries, read during the call:
+ *               contiguous device tensors (outs_i may be grads_i: in place),
+ *               their numbers of elements (0 is valid) and MOE_DTYPE_*. An out
+ *               may overlap neither another out nor another entry's gradient
+ *               (MOE_ERR_INVALID_ARG). A gradient in place that is not scaled is
+ *               not written.
+ *   sumsq       fp64 [1]. norm fp32 [1], or NULL.
+ *   max_norm    >= 0, infinity included.
+ *   workspace   >= moe_grad_norm_workspace_bytes(n) bytes, 16-byte aligned;
+ *               contents on entry do not matter. One for a larger n serves
+ *               smaller ones.
+ * Results are identical on every call. n = 0: sumsq and norm are 0.
+ * Limits: n <= 8192, 2^40 elements a tensor.
+ */
+int64_t moe_grad_norm_workspace_bytes(int32_t n); /* host; -1 on invalid sizes */
+int moe_grad_sumsq(const void* const* grads, const int64_t* sizes, const int32_t* dtypes, int32_t n, double* sumsq,
+                   void* workspace, int64_t workspace_bytes, void* stream);
+int moe_grad_clip(const void* const* grads, void* const* outs, const int64_t* sizes, const int32_t* dtypes, int32_t n,
+                  const double* sumsq, float max_norm, float* norm, void* stream);
 
 /* Measurement helpers (not part of the layer). They measure what this GPU
  * sustains, so that a layer kernel's rate can be stated as a fraction of the

@@ -5,8 +5,12 @@ Road to B300" (section "Phase 3: The INT4 Marlin MoE Throughput Lever"):
 top-k routing, per-expert grouping padded to the tile size, FC1 gate/up with
 SiLU*mul and FC2 with the routing-weighted sum, as HIP kernels for gfx950
 behind the C ABI of include/moe_w4a16.h, and beside it the router's balance
-loss with its gradient (balance_loss, balance_loss_backward) and low-rank
-adapters of many requests, forward and backward (lora_forward, lora_backward).
+loss with its gradient (balance_loss, balance_loss_backward), low-rank
+adapters of many requests, forward and backward (lora_forward, lora_backward),
+and what stands between the layer and the rest of a model: routing by scores
+(route_scored, route_scored_backward), the root-mean-square norm with the
+residual's addition (add_rms_norm, add_rms_norm_backward) and clipping by the
+global gradient norm (grad_sumsq, grad_clip, clip_grad_norm).
 This package is the Python binding (ctypes; PyTorch only provides device memory
 and streams) plus helpers that allocate the buffers a call needs.
 """
@@ -26,6 +30,9 @@ from ._binding import (  # noqa: F401
     moe_mxfp4_unpack, status_string, moe_calib_read_granule, moe_calib_hbm_read, moe_calib_mfma_f16,
     MOE_DTYPE_BF16, MOE_DTYPE_F32, moe_balance_loss, moe_balance_loss_backward, moe_balance_workspace_bytes,
     moe_lora_backward, moe_lora_forward, moe_lora_workspace_bytes,
+    MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX, moe_route_scored, moe_route_scored_backward, moe_add_rms_norm,
+    moe_add_rms_norm_backward, moe_add_rms_norm_workspace_bytes, moe_grad_clip, moe_grad_norm_workspace_bytes,
+    moe_grad_sumsq,
 )
 
 FORMATS = ("int4", "mxfp4")  # weight formats: INT4 g32 + fp16 scales, MXFP4 (e2m1 + E8M0 per 32)
@@ -242,3 +249,146 @@ def lora_backward(grad_out: torch.Tensor, x: torch.Tensor, adapter_ids: torch.Te
     moe_lora_backward(grad_out, x, adapter_ids, h, lora_a, lora_b, grad_a, grad_b, workspace, scales=scales, dx=dx,
                       dx_base=dx_base, stream=stream)
     return dx, grad_a, grad_b
+
+
+def route_scored(logits: torch.Tensor, rb: RouteBuffers, scoring: str = "softmax", bias: torch.Tensor | None = None,
+                 n_groups: int = 1, top_groups: int = 1, group_top: int = 1, renormalise: bool = True,
+                 scale: float = 1.0, row_valid: torch.Tensor | None = None, grouping: bool = True,
+                 stream=None) -> RouteBuffers:
+    """route_align by scores: softmax or sigmoid of the logits, a bias [E] in
+    the choice only, the top_k experts of the top_groups best of n_groups groups
+    (by the sum of a group's group_top highest), weights renormalised and
+    scaled. row_valid: bool [M] (None: all); padding rows get ids of -1 and
+    weights of 0. grouping=False: only topk_ids and topk_weights are written."""
+    lists = dict(sorted_token_ids=rb.sorted_token_ids, block_expert_ids=rb.block_expert_ids,
+                 expert_offsets=rb.expert_offsets, num_tokens_post_pad=rb.num_tokens_post_pad,
+                 cap=rb.cap) if grouping else {}
+    moe_route_scored(logits, rb.top_k, rb.topk_ids, rb.topk_weights, scoring=scoring, bias=bias, n_groups=n_groups,
+                     top_groups=top_groups, group_top=group_top, renormalise=renormalise, scale=scale,
+                     row_valid=row_valid, block_m=rb.block_m, stream=stream, **lists)
+    return rb
+
+
+def route_scored_backward(logits: torch.Tensor, topk_ids: torch.Tensor, grad_weights: torch.Tensor,
+                          scoring: str = "softmax", renormalise: bool = True, scale: float = 1.0,
+                          grad_base: torch.Tensor | None = None, grad_logits: torch.Tensor | None = None,
+                          stream=None) -> torch.Tensor:
+    """The gradient of sum(grad_weights * topk_weights) with respect to the
+    logits plus grad_base (None: zeros), fp32 [M, E]. grad_logits=grad_base adds
+    in place."""
+    if grad_logits is None:
+        with _memory_of(stream, logits.device):
+            grad_logits = torch.empty_like(logits)
+    moe_route_scored_backward(logits, topk_ids, grad_weights, grad_logits, scoring=scoring, renormalise=renormalise,
+                              scale=scale, grad_base=grad_base, stream=stream)
+    return grad_logits
+
+
+@dataclass
+class NormBuffers:
+    """Outputs of moe_add_rms_norm for M rows of N columns; those that are None
+    are not wanted. out8 holds e4m3 values of out / scales."""
+    M: int
+    N: int
+    quant_group: int
+    residual_out: torch.Tensor | None
+    out: torch.Tensor | None
+    out8: torch.Tensor | None
+    scales: torch.Tensor | None
+    rstd: torch.Tensor | None
+
+
+def alloc_norm_buffers(M: int, N: int, residual_dtype: torch.dtype | None = None, out: bool = True, rstd: bool = False,
+                       quant_group: int = 0, device="cuda") -> NormBuffers:
+    """residual_dtype: the stream's type (None: no residual_out; set it to the
+    residual itself for an update in place). quant_group: columns that share a
+    scale of the 8-bit output (N: a row; 0: no such output)."""
+    if quant_group < 0 or (quant_group and N % quant_group):
+        raise ValueError("quant_group must divide N")
+
+    def empty(shape, dtype):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+    return NormBuffers(M, N, quant_group, None if residual_dtype is None else empty((M, N), residual_dtype),
+                       empty((M, N), torch.bfloat16) if out else None,
+                       empty((M, N), torch.float8_e4m3fn) if quant_group else None,
+                       empty((M, N // quant_group), torch.float32) if quant_group else None,
+                       empty(M, torch.float32) if rstd else None)
+
+
+def add_rms_norm(x: torch.Tensor | None, weight: torch.Tensor, bufs: NormBuffers, residual: torch.Tensor | None = None,
+                 eps: float = 1e-6, stream=None) -> NormBuffers:
+    """h = x + residual (either may be None) to bufs.residual_out, its
+    root-mean-square norm times weight to bufs.out (bf16) and bufs.out8 with
+    bufs.scales, 1 / sqrt(mean(h^2) + eps) to bufs.rstd."""
+    moe_add_rms_norm(weight, x, residual, eps, residual_out=bufs.residual_out, out=bufs.out, out8=bufs.out8,
+                     scales=bufs.scales, quant_group=bufs.quant_group, rstd=bufs.rstd, stream=stream)
+    return bufs
+
+
+def add_rms_norm_backward(grad_out: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor,
+                          grad_residual: torch.Tensor | None = None, need_h: bool = True, need_weight: bool = True,
+                          grads: tuple | None = None, workspace: torch.Tensor | None = None, stream=None) -> tuple:
+    """Gradients of add_rms_norm: (grad_h like h = grad_residual + the norm's
+    part, of x and of the residual alike; grad_weight fp32 [N]). h: the
+    forward's residual_out (x, where there was no residual). need_h=False or
+    need_weight=False leave one out (None). grads: buffers of an earlier call to
+    write into; one that is None there is allocated if it is needed."""
+    grad_h, grad_weight = (None, None) if grads is None else grads
+    grad_h = grad_h if need_h else None
+    grad_weight = grad_weight if need_weight else None
+    M, N = h.shape
+    with _memory_of(stream, h.device):
+        if need_h and grad_h is None:
+            grad_h = torch.empty((M, N), dtype=h.dtype, device=h.device)
+        if need_weight and grad_weight is None:
+            grad_weight = torch.empty(N, dtype=torch.float32, device=h.device)
+        if need_weight and workspace is None:
+            nbytes = moe_add_rms_norm_workspace_bytes(M, N)
+            if nbytes < 0:
+                raise ValueError("unsupported sizes")
+            workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=h.device)
+    moe_add_rms_norm_backward(grad_out, h, rstd, weight, grad_h, grad_weight, workspace, grad_residual=grad_residual,
+                              stream=stream)
+    return grad_h, grad_weight
+
+
+def _grads_workspace(grads, device, workspace, stream):
+    if workspace is None:
+        nbytes = moe_grad_norm_workspace_bytes(len(grads))
+        if nbytes < 0:
+            raise ValueError("too many gradients")
+        with _memory_of(stream, device):
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return workspace
+
+
+def grad_sumsq(grads, sumsq: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The sum of the squares of all elements of a sequence of gradients (bf16
+    or fp32), float64 [1]. A data-parallel job may add it over its ranks."""
+    if not grads and sumsq is None:
+        raise ValueError("no gradients, and no sumsq to write to")
+    device = sumsq.device if sumsq is not None else grads[0].device
+    workspace = _grads_workspace(grads, device, workspace, stream)
+    if sumsq is None:
+        with _memory_of(stream, device):
+            sumsq = torch.empty(1, dtype=torch.float64, device=device)
+    moe_grad_sumsq(grads, sumsq, workspace, stream=stream)
+    return sumsq
+
+
+def grad_clip(grads, sumsq: torch.Tensor, max_norm: float, out=None, norm: torch.Tensor | None = None,
+              stream=None) -> torch.Tensor:
+    """Scales gradients whose norm sqrt(sumsq) is above max_norm down to it, in
+    place or into the tensors of out; returns the norm, float32 [1]."""
+    if norm is None:
+        with _memory_of(stream, sumsq.device):
+            norm = torch.empty(1, dtype=torch.float32, device=sumsq.device)
+    moe_grad_clip(grads, grads if out is None else out, sumsq, max_norm, norm=norm, stream=stream)
+    return norm
+
+
+def clip_grad_norm(grads, max_norm: float, out=None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """grad_sumsq and grad_clip: clips the gradients by their global norm, in
+    place or into the tensors of out; returns the norm before, float32 [1]."""
+    return grad_clip(grads, grad_sumsq(grads, workspace=workspace, stream=stream), max_norm, out=out, stream=stream)

@@ -29,6 +29,10 @@ MOE_DTYPE_BF16 = 0
 MOE_DTYPE_F32 = 1
 _SIDE_DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32}
 
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
+_SCORINGS = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
+
 KIND_W13 = 0
 KIND_W2 = 1
 GROUP = 32
@@ -68,6 +72,19 @@ _SIGNATURES["moe_lora_forward"] = (ctypes.c_int, [_vp, _i64, _vp, _i32, _i32, _i
                                                   _i64, _vp, _i64, _i32, _vp, _vp, _i64, _vp])
 _SIGNATURES["moe_lora_backward"] = (ctypes.c_int, [_vp, _i64, _i32, _vp, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
                                                    _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp])
+_f32 = ctypes.c_float
+_SIGNATURES["moe_route_scored"] = (ctypes.c_int, [_vp, _i32, _i32, _i32, _i32, _vp, _i32, _i32, _i32, _i32, _f32, _vp,
+                                                  _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp])
+_SIGNATURES["moe_route_scored_backward"] = (ctypes.c_int, [_vp, _i32, _i32, _i32, _i32, _i32, _f32, _vp, _vp, _vp, _vp,
+                                                           _vp])
+_SIGNATURES["moe_add_rms_norm"] = (ctypes.c_int, [_vp, _i64, _vp, _i64, _i32, _i32, _i32, _vp, ctypes.c_double, _vp, _i64,
+                                                  _vp, _i64, _vp, _i64, _vp, _i32, _vp, _vp])
+_SIGNATURES["moe_add_rms_norm_workspace_bytes"] = (_i64, [_i32, _i32])
+_SIGNATURES["moe_add_rms_norm_backward"] = (ctypes.c_int, [_vp, _i64, _vp, _i64, _i32, _vp, _i32, _i32, _vp, _vp, _i64,
+                                                           _vp, _i64, _vp, _vp, _i64, _vp])
+_SIGNATURES["moe_grad_norm_workspace_bytes"] = (_i64, [_i32])
+_SIGNATURES["moe_grad_sumsq"] = (ctypes.c_int, [_vp, _vp, _vp, _i32, _vp, _vp, _i64, _vp])
+_SIGNATURES["moe_grad_clip"] = (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _vp, _f32, _vp, _vp])
 _SIGNATURES["moe_calib_read_granule"] = (_i64, [])
 _SIGNATURES["moe_calib_hbm_read"] = (ctypes.c_int, [_vp, _i64, _i32, _vp, _vp])
 _SIGNATURES["moe_calib_mfma_f16"] = (ctypes.c_int, [_i64, _i32, _vp, _vp])
@@ -494,6 +511,147 @@ def moe_lora_backward(grad_out: torch.Tensor, x: torch.Tensor, adapter_ids: torc
                _shaped(scales, f32, (L,), "scales", dev), pb, ldb, pd, ldd,
                _shaped(grad_a, f32, (L, r, K), "grad_a", dev), _shaped(grad_b, f32, (L, N, r), "grad_b", dev),
                *_buffer(workspace, "workspace", dev))
+
+
+def _scoring(name: str) -> int:
+    if name not in _SCORINGS:
+        raise ValueError(f"scoring must be one of {tuple(_SCORINGS)}, got {name!r}")
+    return _SCORINGS[name]
+
+
+def moe_route_scored(logits: torch.Tensor, top_k: int, topk_ids: torch.Tensor, topk_weights: torch.Tensor,
+                     scoring: str = "softmax", bias: torch.Tensor | None = None, n_groups: int = 1,
+                     top_groups: int = 1, group_top: int = 1, renormalise: bool = True, scale: float = 1.0,
+                     row_valid: torch.Tensor | None = None, block_m: int = 16,
+                     sorted_token_ids: torch.Tensor | None = None, block_expert_ids: torch.Tensor | None = None,
+                     expert_offsets: torch.Tensor | None = None, num_tokens_post_pad: torch.Tensor | None = None,
+                     cap: int | None = None, stream=None) -> None:
+    """row_valid: bool or uint8 [M]. The four grouping outputs together or none of them."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be a matrix [M, E]")
+    M, E = logits.shape
+    dev, i32, f32 = logits.device, torch.int32, torch.float32
+    if row_valid is not None and row_valid.dtype == torch.bool:
+        row_valid = row_valid.view(torch.uint8)
+    if cap is None:
+        cap = 0 if sorted_token_ids is None else sorted_token_ids.numel()
+    if sorted_token_ids is not None and sorted_token_ids.numel() < cap:
+        raise ValueError("sorted_token_ids must have cap entries")
+    if block_expert_ids is not None and block_m > 0 and block_expert_ids.numel() < cap // block_m:
+        raise ValueError("block_expert_ids must have cap / block_m entries")
+
+    def flat(t, what):
+        return 0 if t is None else _shaped(t, i32, (t.numel(),), what, dev)
+
+    _on_device(dev, "moe_route_scored", stream, _shaped(logits, f32, (M, E), "logits", dev), M, E, top_k,
+               _scoring(scoring), _shaped(bias, f32, (E,), "bias", dev), n_groups, top_groups, group_top,
+               int(renormalise), scale, _shaped(row_valid, torch.uint8, (M,), "row_valid", dev), block_m,
+               _shaped(topk_ids, i32, (M, top_k), "topk_ids", dev),
+               _shaped(topk_weights, f32, (M, top_k), "topk_weights", dev), flat(sorted_token_ids, "sorted_token_ids"),
+               flat(block_expert_ids, "block_expert_ids"), _shaped(expert_offsets, i32, (E + 1,), "expert_offsets", dev),
+               _shaped(num_tokens_post_pad, i32, (1,), "num_tokens_post_pad", dev), cap)
+
+
+def moe_route_scored_backward(logits: torch.Tensor, topk_ids: torch.Tensor, grad_weights: torch.Tensor,
+                              grad_logits: torch.Tensor, scoring: str = "softmax", renormalise: bool = True,
+                              scale: float = 1.0, grad_base: torch.Tensor | None = None, stream=None) -> None:
+    if logits.dim() != 2 or topk_ids.dim() != 2:
+        raise ValueError("logits must be [M, E] and topk_ids [M, top_k]")
+    M, E = logits.shape
+    k = topk_ids.shape[1]
+    dev, f32 = logits.device, torch.float32
+    _on_device(dev, "moe_route_scored_backward", stream, _shaped(logits, f32, (M, E), "logits", dev), M, E, k,
+               _scoring(scoring), int(renormalise), scale, _shaped(topk_ids, torch.int32, (M, k), "topk_ids", dev),
+               _shaped(grad_weights, f32, (M, k), "grad_weights", dev),
+               _shaped(grad_base, f32, (M, E), "grad_base", dev),
+               _shaped(grad_logits, f32, (M, E), "grad_logits", dev))
+
+
+def moe_add_rms_norm(weight: torch.Tensor, x: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                     eps: float = 1e-6, residual_out: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                     out8: torch.Tensor | None = None, scales: torch.Tensor | None = None, quant_group: int = 0,
+                     rstd: torch.Tensor | None = None, stream=None) -> None:
+    """out8: uint8 or float8_e4m3fn [M, N]."""
+    first = x if x is not None else residual
+    if first is None or first.dim() != 2:
+        raise ValueError("x or residual must be a matrix [M, N]")
+    M, N = first.shape
+    dev, bf16, f32 = first.device, torch.bfloat16, torch.float32
+    res_type = residual.dtype if residual is not None else bf16
+    kind = _side_dtype(first if residual is None else residual, "residual")
+    if out8 is not None and out8.dtype == torch.float8_e4m3fn:
+        out8 = out8.view(torch.uint8)
+    groups = N // quant_group if quant_group > 0 else 0
+    px, ldx = _matrix(x, bf16, (M, N), "x", dev)
+    pr, ldr = _matrix(residual, res_type, (M, N), "residual", dev)
+    ps, lds = _matrix(residual_out, res_type, (M, N), "residual_out", dev)
+    po, ldo = _matrix(out, bf16, (M, N), "out", dev)
+    p8, ld8 = _matrix(out8, torch.uint8, (M, N), "out8", dev)
+    _on_device(dev, "moe_add_rms_norm", stream, px, ldx, pr, ldr, kind, M, N, _shaped(weight, bf16, (N,), "weight", dev),
+               eps, ps, lds, po, ldo, p8, ld8, _shaped(scales, f32, (M, groups), "scales", dev), quant_group,
+               _shaped(rstd, f32, (M,), "rstd", dev))
+
+
+def moe_add_rms_norm_workspace_bytes(M: int, N: int) -> int:
+    return lib().moe_add_rms_norm_workspace_bytes(M, N)
+
+
+def moe_add_rms_norm_backward(grad_out: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor,
+                              grad_h: torch.Tensor | None = None, grad_weight: torch.Tensor | None = None,
+                              workspace: torch.Tensor | None = None, grad_residual: torch.Tensor | None = None,
+                              stream=None) -> None:
+    if grad_out.dim() != 2:
+        raise ValueError("grad_out must be a matrix [M, N]")
+    M, N = grad_out.shape
+    dev, bf16, f32 = grad_out.device, torch.bfloat16, torch.float32
+    kind = _side_dtype(h, "h")
+    pg, ldg = _matrix(grad_out, bf16, (M, N), "grad_out", dev)
+    ph, ldh = _matrix(h, h.dtype, (M, N), "h", dev)
+    pr, ldr = _matrix(grad_residual, h.dtype, (M, N), "grad_residual", dev)
+    pd, ldd = _matrix(grad_h, h.dtype, (M, N), "grad_h", dev)
+    _on_device(dev, "moe_add_rms_norm_backward", stream, pg, ldg, ph, ldh, kind, _shaped(rstd, f32, (M,), "rstd", dev),
+               M, N, _shaped(weight, bf16, (N,), "weight", dev), pr, ldr, pd, ldd,
+               _shaped(grad_weight, f32, (N,), "grad_weight", dev),
+               *((0, 0) if workspace is None else _buffer(workspace, "workspace", dev)))
+
+
+def moe_grad_norm_workspace_bytes(n: int) -> int:
+    return lib().moe_grad_norm_workspace_bytes(n)
+
+
+def _grad_arrays(grads, device: torch.device) -> tuple:
+    """(pointers, sizes, types) of contiguous bf16 or fp32 tensors, as host arrays."""
+    for t in grads:
+        if t.dtype not in _SIDE_DTYPES or t.device != device or not t.is_contiguous():
+            raise ValueError(f"gradients must be contiguous bfloat16 or float32 tensors on {device}")
+    n = len(grads)
+    return ((ctypes.c_void_p * n)(*[t.data_ptr() for t in grads]), (_i64 * n)(*[t.numel() for t in grads]),
+            (_i32 * n)(*[_SIDE_DTYPES[t.dtype] for t in grads]))
+
+
+def moe_grad_sumsq(grads, sumsq: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
+    """grads: a sequence of tensors; sumsq: float64 [1]."""
+    dev = sumsq.device
+    ptrs, sizes, kinds = _grad_arrays(grads, dev)
+    _on_device(dev, "moe_grad_sumsq", stream, ptrs, sizes, kinds, len(grads),
+               _shaped(sumsq, torch.float64, (1,), "sumsq", dev), *_buffer(workspace, "workspace", dev))
+
+
+def moe_grad_clip(grads, outs, sumsq: torch.Tensor, max_norm: float, norm: torch.Tensor | None = None,
+                  stream=None) -> None:
+    """outs: a sequence of tensors like grads (the same ones: in place)."""
+    dev = sumsq.device
+    if len(outs) != len(grads):
+        raise ValueError("outs must have as many tensors as grads")
+    ptrs, sizes, kinds = _grad_arrays(grads, dev)
+    to = ptrs
+    if outs is not grads:
+        to, osizes, okinds = _grad_arrays(outs, dev)
+        if list(osizes) != list(sizes) or list(okinds) != list(kinds):
+            raise ValueError("outs must have the sizes and types of grads")
+    _on_device(dev, "moe_grad_clip", stream, ptrs, to, sizes, kinds, len(grads),
+               _shaped(sumsq, torch.float64, (1,), "sumsq", dev), max_norm,
+               _shaped(norm, torch.float32, (1,), "norm", dev))
 
 
 # ------------------------------------------------------------------ measurement helpers

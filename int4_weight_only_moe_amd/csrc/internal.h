@@ -128,6 +128,10 @@ hipError_t launch_route_align(const float* logits, int M, int E, int k, int bloc
                               int32_t* block_expert, int32_t* offsets, int32_t* npp,
                               int64_t cap, hipStream_t stream);
 
+// The grouping alone: `ids` [MK] (entries outside [0, E) belong to no expert).
+hipError_t launch_align(const int32_t* ids, int MK, int E, int block_m, int32_t* sorted_ids, int32_t* block_expert,
+                        int32_t* offsets, int32_t* npp, hipStream_t stream);
+
 // s: fp16 scales (kFmtInt4) or E8M0 bytes (kFmtMxfp4), [E, N, K/32].
 hipError_t launch_repack(int fmt, const uint8_t* q, const void* s, int E, int N, int K, int kind,
                          uint8_t* packed, hipStream_t stream);

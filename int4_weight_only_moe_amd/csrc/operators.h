@@ -1,6 +1,8 @@
 // Internal declarations of the operators beside the layer: the balance loss
-// of the router (balance.hip) and low-rank adapters (lora.hip). The entry
-// points are in abi_operators.hip.
+// of the router (balance.hip), low-rank adapters (lora.hip), routing by scores
+// (route_scored.hip), the norm with the residual's addition (norm.hip) and the
+// gradient norm with clipping (clip.hip). The entry points are in
+// abi_operators.hip.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -92,5 +94,99 @@ LoraLayout lora_layout(int64_t M, int64_t L, int64_t K, int64_t N, int64_t r, bo
 
 hipError_t launch_lora_forward(const LoraArgs& a, hipStream_t stream);
 hipError_t launch_lora_backward(const LoraArgs& a, hipStream_t stream);
+
+// ---- routing by scores ------------------------------------------------------
+struct ScoredArgs {
+  const float* logits;       // [M, E]
+  const float* bias;         // [E] or null
+  const uint8_t* valid;      // [M] or null
+  int M, E, k;
+  bool sigmoid, renorm;
+  float scale;
+  int groups, top_groups, group_top;
+  int32_t* ids;              // [M, k]
+  float* weights;            // [M, k]
+  // grouping, or all null
+  int block_m;
+  int32_t* sorted_ids;       // [cap]
+  int32_t* block_expert;     // [cap / block_m]
+  int32_t* offsets;          // [E + 1]
+  int32_t* npp;              // [1]
+  int64_t cap;
+};
+hipError_t launch_route_scored(const ScoredArgs& a, hipStream_t stream);
+
+struct ScoredBackwardArgs {
+  const float* logits;
+  int M, E, k;
+  bool sigmoid, renorm;
+  float scale;
+  const int32_t* ids;
+  const float* dweights;
+  const float* base;         // [M, E], null, or grad
+  float* grad;               // [M, E]
+};
+hipError_t launch_route_scored_backward(const ScoredBackwardArgs& a, hipStream_t stream);
+
+// ---- norm -------------------------------------------------------------------
+constexpr int kNormMaxWidth = 32768;
+struct NormArgs {
+  const uint16_t* x;         // [M, N] or null
+  int64_t ldx;
+  const void* res;           // [M, N] or null
+  int64_t ld_res;
+  bool f32;                  // the stream's type
+  int M, N;
+  const uint16_t* w;         // [N]
+  double eps;
+  void* res_out;             // [M, N] or null
+  int64_t ld_res_out;
+  uint16_t* out;             // [M, N] or null
+  int64_t ld_out;
+  uint8_t* out8;             // [M, N] or null
+  int64_t ld_out8;
+  float* scales;             // [M, N / group]
+  int group;
+  float* rstd;               // [M] or null
+};
+hipError_t launch_norm(const NormArgs& a, hipStream_t stream);
+
+struct NormBackwardArgs {
+  const uint16_t* dout;      // [M, N]
+  int64_t ld_dout;
+  const void* h;             // [M, N]
+  int64_t ld_h;
+  bool f32;
+  const float* rstd;         // [M]
+  int M, N;
+  const uint16_t* w;         // [N]
+  const void* dres;          // [M, N] or null
+  int64_t ld_dres;
+  void* dh;                  // [M, N] or null
+  int64_t ld_dh;
+  float* dw;                 // [N] or null
+  float* parts;              // [norm_backward_parts(M), N]
+};
+int norm_backward_parts(int64_t M);  // rows of partial weight gradients
+hipError_t launch_norm_backward(const NormBackwardArgs& a, hipStream_t stream);
+
+// ---- gradient norm and clipping ----------------------------------------------
+constexpr int kClipMaxTensors = 8192;
+constexpr int kClipTensorsPerLaunch = 96;
+constexpr int kSumsqBlocks = 2048;        // partial sums of a launch
+struct ClipArgs {
+  const void* const* grads;
+  void* const* outs;         // clip only
+  const int64_t* sizes;
+  const int32_t* dtypes;
+  int n;
+  double* sumsq;
+  float max_norm;            // clip only
+  float* norm;               // clip only, or null
+  double* parts;             // sumsq only: [launches, kSumsqBlocks]
+};
+inline int64_t clip_launches(int64_t n) { return ceil_div(n, kClipTensorsPerLaunch); }
+hipError_t launch_grad_sumsq(const ClipArgs& a, hipStream_t stream);
+hipError_t launch_grad_clip(const ClipArgs& a, hipStream_t stream);
 
 }  // namespace moe

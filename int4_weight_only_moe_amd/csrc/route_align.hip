@@ -383,23 +383,26 @@ hipError_t launch_vpl(const float* logits, int M, int E, int k, int block_m, int
   topk_kernel<VPL><<<blocks, 64 * kTopkWavesPerBlock, 0, stream>>>(logits, M, E, k, topk_ids, topk_w);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  const int MK = M * k;
+  return launch_align(topk_ids, M * k, E, block_m, sorted_ids, block_expert, offsets, npp, stream);
+}
+
+}  // namespace
+
+hipError_t launch_align(const int32_t* ids, int MK, int E, int block_m, int32_t* sorted_ids, int32_t* block_expert,
+                        int32_t* offsets, int32_t* npp, hipStream_t stream) {
   if (MK >= kAlignGridMinIds) {
     // segments of at least kAlignGridSegIds assignments, at most
     // kAlignGridMaxBlocks workgroups (each histograms all M*k ids)
     const int64_t per = ((int64_t)MK + kAlignGridMaxBlocks - 1) / kAlignGridMaxBlocks;
     const int seg = (int)(per > kAlignGridSegIds ? (per + 1023) / 1024 * 1024 : kAlignGridSegIds);
     const int grid = (MK + seg - 1) / seg;
-    align_grid_kernel<<<grid, kAlignThreads, 0, stream>>>(topk_ids, MK, E, block_m, seg, sorted_ids, block_expert,
-                                                          offsets, npp);
+    align_grid_kernel<<<grid, kAlignThreads, 0, stream>>>(ids, MK, E, block_m, seg, sorted_ids, block_expert, offsets,
+                                                          npp);
   } else {
-    align_kernel<<<1, kAlignThreads, 0, stream>>>(topk_ids, MK, E, block_m, sorted_ids, block_expert, offsets,
-                                                  npp);
+    align_kernel<<<1, kAlignThreads, 0, stream>>>(ids, MK, E, block_m, sorted_ids, block_expert, offsets, npp);
   }
   return hipGetLastError();
 }
-
-}  // namespace
 
 hipError_t launch_route_align(const float* logits, int M, int E, int k, int block_m,
                               int32_t* topk_ids, float* topk_weights, int32_t* sorted_ids,

@@ -245,18 +245,18 @@ __device__ __forceinline__ int small_rank(const SmallRoute& sh, int x) {
   return sh.before[w] + __builtin_popcount(sh.bits[w] & ((1u << b) - 1u));
 }
 
-// Fills sh for the batch; returns the number of touched experts (= blocks).
-// Every thread of the workgroup (kThreads, at least 64 * M) must call it:
-// it contains barriers.
-template <int VPL, int kThreads>
-__device__ int small_route(SmallRoute& sh, const float* __restrict__ logits, int M, int E, int k) {
+// Groups the MK assignments of sh.ids; returns the number of touched experts
+// (= blocks). Every thread of the workgroup must call it, with sh.ids written
+// and sh.bits cleared: it begins with a barrier and contains others. kDropped:
+// entries outside [0, E) belong to no expert.
+template <int kThreads, bool kDropped>
+__device__ __forceinline__ int small_group(SmallRoute& sh, int MK, int E) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int MK = M * k, nwords = (E + 31) / 32;
-  if (tid < nwords) sh.bits[tid] = 0u;
-  if (wave < M) topk_token<VPL>(logits, wave, E, k, sh.ids, sh.wts);
+  const int nwords = (E + 31) / 32;
   __syncthreads();
-  for (int f = tid; f < MK; f += kThreads) atomicOr(&sh.bits[sh.ids[f] >> 5], 1u << (sh.ids[f] & 31));
+  for (int f = tid; f < MK; f += kThreads)
+    if (!kDropped || (unsigned)sh.ids[f] < (unsigned)E) atomicOr(&sh.bits[sh.ids[f] >> 5], 1u << (sh.ids[f] & 31));
   __syncthreads();
   if (wave == 0) {  // exclusive prefix of the words' popcounts (nwords <= 32)
     const int c = lane < nwords ? __builtin_popcount(sh.bits[lane]) : 0;
@@ -290,6 +290,18 @@ __device__ int small_route(SmallRoute& sh, const float* __restrict__ logits, int
   }
   __syncthreads();
   return nd;
+}
+
+// Fills sh for the batch; returns the number of touched experts (= blocks).
+// Every thread of the workgroup (kThreads, at least 64 * M) must call it:
+// it contains barriers.
+template <int VPL, int kThreads>
+__device__ int small_route(SmallRoute& sh, const float* __restrict__ logits, int M, int E, int k) {
+  const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  if (tid < (E + 31) / 32) sh.bits[tid] = 0u;
+  if (wave < M) topk_token<VPL>(logits, wave, E, k, sh.ids, sh.wts);
+  return small_group<kThreads, false>(sh, M * k, E);
 }
 
 // The routing and grouping outputs exactly as moe_route_align lays them out

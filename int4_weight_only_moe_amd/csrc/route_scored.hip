@@ -1,0 +1,627 @@
+// Routing by scores and its gradient.
+//
+// s = softmax(l) or sigmoid(l) of a token's logits, c = s + bias; the groups of
+// the highest scores, the k experts of the highest c in them, weights from s.
+// A row of logits lies in the registers of 16 lanes (32 from 513 experts on).
+//
+// Finding the k highest without k passes over the row: the k-th highest of the
+// lanes' own maxima (k exchanges within the row) is a threshold that at least k
+// values reach and few others do (for 384 values and k = 8 some 11). These
+// candidates go to LDS, where each is ranked by counting the higher ones.
+//
+// The choice is that of c in fp64, but no row needs fp64 for that: where fp32
+// values that decide the choice are closer than their error bound, and where
+// something is not finite or the candidates are too many, the wave computes
+// the row again in fp64 (route_row_exact). Equal logits with equal biases need
+// no such decision (the lower expert goes first).
+#include <type_traits>
+
+#include "device_common.h"
+#include "internal.h"
+#include "operators.h"
+#include "row_common.h"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int kMaxCand = 64;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kDenom = 1e-20f;  // added to the kept sigmoid scores' sum
+
+// LDS written by lanes of this wave becomes visible to its other lanes.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+template <int Lanes>
+__device__ __forceinline__ uint32_t row_max_u32(uint32_t v) {
+  v = umax(v, dpp<kQuadSwap1>(v));
+  v = umax(v, dpp<kQuadSwap2>(v));
+  v = umax(v, dpp<kRowHalfMirror>(v));
+  v = umax(v, dpp<kRowMirror>(v));
+  if constexpr (Lanes == 32) {
+    const auto h = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = umax(h[0], h[1]);
+  }
+  return v;
+}
+
+// Sum over the lower lanes of the row; `total` over all of them.
+template <int Lanes>
+__device__ __forceinline__ int row_before(int v, int& total) {
+  uint32_t incl = (uint32_t)v;
+  incl += dpp<0x111>(incl);  // row_shr by 1, 2, 4, 8: lanes without a source add 0
+  incl += dpp<0x112>(incl);
+  incl += dpp<0x114>(incl);
+  incl += dpp<0x118>(incl);
+  uint32_t all = row_max_u32<16>(incl);
+  if constexpr (Lanes == 32) {
+    const auto h = __builtin_amdgcn_permlane16_swap(all, all, false, false);
+    const uint32_t both = h[0] + h[1];
+    incl += (threadIdx.x & 16) ? both - all : 0u;
+    all = both;
+  }
+  total = (int)all;
+  return (int)incl - v;
+}
+
+// Whether any lane of the row says so (the whole wave calls it).
+template <int Lanes>
+__device__ __forceinline__ bool row_any(bool b) {
+  const uint64_t m = __ballot(b) >> (threadIdx.x & (64 - Lanes));
+  return Lanes == 32 ? (uint32_t)m != 0 : (m & 0xffffu) != 0;
+}
+
+// Order-preserving keys: absent (-inf) 0, NaN the highest.
+__device__ __forceinline__ uint32_t key32(float v) {
+  const uint32_t k = order_key(v);
+  return v == -INFINITY ? 0u : v != v ? 0xFFFFFFFFu : k;
+}
+__device__ __forceinline__ uint64_t key64(double v) {
+  const uint64_t u = (uint64_t)__double_as_longlong(v + 0.0);
+  const uint64_t k = (u >> 63) ? ~u : (u | 0x8000000000000000ull);
+  return v != v ? ~0ull : k;
+}
+__device__ __forceinline__ double key64_value(uint64_t k) {
+  return __longlong_as_double((long long)((k >> 63) ? (k & 0x7FFFFFFFFFFFFFFFull) : ~k));
+}
+
+// The softmax of a row as exp2(l' log2(e) - ml) * inv, l' = l - first (see
+// exp_row: the rounding of ml is a factor of the whole row).
+struct RowSoftmax {
+  float first, ml, inv;
+  __device__ __forceinline__ float exp_of(float l) const {
+    return __builtin_amdgcn_exp2f(fmaf(l - first, kLog2e, -ml));
+  }
+};
+template <int Lanes, int N>
+__device__ __forceinline__ RowSoftmax row_softmax(const float (&v)[N]) {
+  float m = v[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) m = fmaxf(m, v[i]);
+  m = row_max<Lanes>(m);
+  m = m == -INFINITY ? 0.0f : m;
+  const bool far = fabsf(m) >= 0x1p20f;
+  RowSoftmax r;
+  r.first = far ? m : 0.0f;
+  r.ml = far ? 0.0f : m * kLog2e;
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) s += r.exp_of(v[i]);
+  s = row_sum<Lanes>(s);
+  r.inv = s == 0.0f ? 0.0f : 1.0f / s;
+  return r;
+}
+
+__device__ __forceinline__ float sigmoid_of(float l) {  // to the last bits for any l
+  const float e = expf(-fabsf(l));
+  return l != l ? l : (l >= 0.0f ? 1.0f : e) / (1.0f + e);
+}
+
+struct Candidate {
+  uint32_t key;
+  float l, b;
+  int e;
+};
+
+// One row's choice in fp64 by the whole wave: sel[0..k) gets the experts (-1:
+// none left). keys: E 64-bit words of this wave.
+__device__ void route_row_exact(const ScoredArgs& a, int64_t t, uint64_t* keys, int* sel) {
+  const int lane = threadIdx.x & 63, E = a.E;
+  const float* row = a.logits + t * E;
+  const bool grouped = a.top_groups < a.groups;
+  double m = -INFINITY, sum = 1.0;
+  if (!a.sigmoid) {
+#pragma unroll 1
+    for (int e = lane; e < E; e += 64) m = fmax(m, (double)row[e]);
+#pragma unroll 1
+    for (int d = 32; d; d >>= 1) m = fmax(m, __shfl_xor(m, d, 64));
+    sum = 0.0;
+#pragma unroll 1
+    for (int e = lane; e < E; e += 64) sum += exp((double)row[e] - m);
+#pragma unroll 1
+    for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d, 64);
+  }
+#pragma unroll 1
+  for (int e = lane; e < E; e += 64) {
+    const double l = row[e], b = a.bias ? (double)a.bias[e] : 0.0;
+    uint64_t key = 0;
+    if (l != -INFINITY && b != -INFINITY) {
+      if (!a.bias && !grouped) key = key64(l);
+      else key = key64((a.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - m) / sum) + b);
+    }
+    keys[e] = key;
+  }
+  wave_sync();
+  if (grouped) {
+    const int G = a.groups, gs = E / G;
+    uint64_t mine = 0;  // lane g: the key of group g's score
+#pragma unroll 1
+    for (int g = 0; g < G; ++g) {
+      uint64_t m1 = 0, m2 = 0;
+#pragma unroll 1
+      for (int i = lane; i < gs; i += 64) {
+        const uint64_t x = keys[g * gs + i];
+        m2 = x > m1 ? m1 : (x > m2 ? x : m2);
+        m1 = x > m1 ? x : m1;
+      }
+#pragma unroll 1
+      for (int d = 32; d; d >>= 1) {
+        const uint64_t o1 = __shfl_xor((unsigned long long)m1, d, 64), o2 = __shfl_xor((unsigned long long)m2, d, 64);
+        const uint64_t low = o1 > m1 ? m1 : o1;
+        m2 = m2 > o2 ? m2 : o2;
+        m2 = low > m2 ? low : m2;
+        m1 = o1 > m1 ? o1 : m1;
+      }
+      const uint64_t score = a.group_top == 2 && m2 ? key64((m1 == ~0ull ? NAN : key64_value(m1)) +
+                                                            (m2 == ~0ull ? NAN : key64_value(m2)))
+                                                    : m1;
+      if (lane == g) mine = score;
+    }
+    int rank = 0;
+#pragma unroll 1
+    for (int g = 0; g < G; ++g) {
+      const uint64_t o = __shfl((unsigned long long)mine, g, 64);
+      rank += o > mine || (o == mine && g < lane);
+    }
+    const uint64_t chosen = __ballot(lane < G && mine && rank < a.top_groups);
+#pragma unroll 1
+    for (int e = lane; e < E; e += 64) {
+      uint64_t key = keys[e];
+      if (!((chosen >> (e / gs)) & 1)) key = 0;
+      else if (key && !a.bias) key = key64((double)row[e]);
+      keys[e] = key;
+    }
+  }
+#pragma unroll 1
+  for (int r = 0; r < a.k; ++r) {
+    uint64_t best = 0;
+    int at = E;
+#pragma unroll 1
+    for (int e = lane; e < E; e += 64)
+      if (keys[e] > best) best = keys[e], at = e;
+#pragma unroll 1
+    for (int d = 32; d; d >>= 1) {
+      const uint64_t o = __shfl_xor((unsigned long long)best, d, 64);
+      const int oat = __shfl_xor(at, d, 64);
+      const bool take = o > best || (o == best && oat < at);
+      best = take ? o : best;
+      at = take ? oat : at;
+    }
+    if (lane == 0) sel[r] = best ? at : -1;
+    if (best && (at & 63) == lane) keys[at] = 0;
+  }
+  wave_sync();
+}
+
+// LDS of one wave beside `Candidate`s: the group values of its rows, or the
+// 64-bit keys of one row.
+__host__ __device__ constexpr int64_t row_buffer_bytes(int lanes, bool general, int E) {
+  return (int64_t)E * (general ? (64 / lanes) * 4 : 8);
+}
+
+template <int Lanes>
+struct RouteShared {
+  Candidate cand[kThreads / Lanes][kMaxCand];
+  int sel[kThreads / Lanes][16];
+  float groups[kThreads / Lanes][64];
+};
+
+// Routes the rows t0 + wave * (64 / Lanes) + lane / Lanes of this workgroup.
+// General: with a bias or groups. copy: also gets the ids (LDS), or null.
+template <int Lanes, int NV, bool Vec, bool General>
+__device__ __forceinline__ void route_rows(const ScoredArgs& a, int64_t t0, RouteShared<Lanes>& sh, float* buffer,
+                                           int32_t* copy) {
+  constexpr int N = 4 * NV, kRows = 64 / Lanes;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane % Lanes, sub = lane / Lanes;
+  const int E = a.E, k = a.k;
+  const int64_t t = t0 + wave * kRows + sub;
+  const bool active = t < a.M;
+  const float* row = a.logits + (active ? t : (int64_t)a.M - 1) * E;
+  const int r = wave * kRows + sub;
+  buffer += row_buffer_bytes(Lanes, General, E) / 4 * wave;
+  float v[N];
+  load_row<Lanes, NV, Vec>(row, E, l, v);
+  const bool live = active && (!a.valid || a.valid[t]);
+  RowSoftmax soft{0.0f, 0.0f, 0.0f};
+  if (!a.sigmoid && (General || !a.renorm)) soft = row_softmax<Lanes>(v);
+
+  bool bad = false;
+  uint32_t key[N];
+  float delta = 0.0f;  // twice the error of a score
+  if constexpr (!General) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) key[i] = key32(v[i]);
+  } else {
+    const bool grouped = a.top_groups < a.groups;
+    float c[N];
+    // fp32 errors: a sigmoid is off by some 5 roundings of itself and by
+    // |l| s (1 - s) < 0.23 of them; a softmax value p = pmax e^-x by (1.5 x + 50)
+    // p, at most 50 pmax (x from the exponent, the rest from the row's sum)
+    delta = a.sigmoid ? 0x1p-19f : 0x1p-17f * soft.inv;
+    // scores where they are needed, then c
+    if (a.bias || (grouped && a.group_top == 2)) {
+      if (a.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) c[i] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * v[i]));
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) c[i] = soft.exp_of(v[i]) * soft.inv;
+      }
+      if (a.bias) {
+        float b[N];
+        load_row<Lanes, NV, Vec>(a.bias, E, l, b);
+#pragma unroll
+        for (int i = 0; i < N; ++i) c[i] = c[i] + b[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) c[i] = v[i];
+      delta = 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int e = 4 * Lanes * j + 4 * l + q;
+        bad |= e < E && !(fabsf(v[4 * j + q]) < 1e30f && fabsf(c[4 * j + q]) < 1e30f);
+      }
+    uint64_t chosen = ~0ull;
+    const int gs = E / a.groups;
+    const uint32_t magic = (1u << 20) / (uint32_t)gs + 1u;  // e / gs = e * magic >> 20 for e < 1024
+    if (grouped) {
+      float* mine = buffer + sub * E;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int e = 4 * Lanes * j + 4 * l;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (e + q < E) mine[e + q] = c[4 * j + q];
+      }
+      wave_sync();
+      // P lanes a group
+      const int G = a.groups;
+      int P = 1;
+      while (P < 8 && 2 * P * G <= Lanes) P *= 2;
+      for (int g = l / P; g < G; g += Lanes / P) {
+        float m1 = -INFINITY, m2 = -INFINITY;
+        for (int i = l % P; i < gs; i += P) {
+          const float x = mine[g * gs + i];
+          m2 = fmaxf(m2, fminf(m1, x));
+          m1 = fmaxf(m1, x);
+        }
+        auto join = [&](uint32_t o1b, uint32_t o2b) {
+          const float o1 = __uint_as_float(o1b), o2 = __uint_as_float(o2b);
+          m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
+          m1 = fmaxf(m1, o1);
+        };
+        if (P > 1) join(dpp<kQuadSwap1>(__float_as_uint(m1)), dpp<kQuadSwap1>(__float_as_uint(m2)));
+        if (P > 2) join(dpp<kQuadSwap2>(__float_as_uint(m1)), dpp<kQuadSwap2>(__float_as_uint(m2)));
+        if (P > 4) join(dpp<kRowHalfMirror>(__float_as_uint(m1)), dpp<kRowHalfMirror>(__float_as_uint(m2)));
+        sh.groups[r][g] = a.group_top == 2 ? m1 + m2 : m1;
+      }
+      wave_sync();
+      chosen = 0;
+      float in = INFINITY, out = -INFINITY;
+      for (int g0 = 0; g0 < G; g0 += Lanes) {
+        const int g = g0 + l;
+        const float s = g < G ? sh.groups[r][g] : 0.0f;
+        int rank = 0;
+        for (int h = 0; h < G; ++h) {
+          const float o = sh.groups[r][h];
+          rank += o > s || (o == s && h < g);
+        }
+        const bool take = g < G && rank < a.top_groups;
+        const uint64_t m = __ballot(take) >> (lane & (64 - Lanes));
+        chosen |= (Lanes == 32 ? (m & 0xffffffffu) : (m & 0xffffu)) << g0;
+        in = take ? fminf(in, s) : in;
+        out = g < G && !take ? fmaxf(out, s) : out;
+      }
+      in = -row_max<Lanes>(-in);
+      out = row_max<Lanes>(out);
+      if (delta > 0.0f) bad |= !(in - out > 2.0f * delta + 0x1p-21f * fmaxf(fabsf(in), fabsf(out)));
+    }
+    if (!a.bias) delta = 0.0f;  // the experts are then ordered by their logits
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int e = 4 * Lanes * j + 4 * l + q;
+        const uint32_t kk = key32(a.bias ? c[4 * j + q] : v[4 * j + q]);
+        key[4 * j + q] = e < E && ((chosen >> ((uint32_t)e * magic >> 20)) & 1) ? kk : 0u;
+      }
+  }
+
+  // the threshold
+  uint32_t top = key[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) top = umax(top, key[i]);
+  uint32_t limit = 0;
+#pragma unroll 1
+  for (int i = 0; i < k; ++i) {
+    limit = row_max_u32<Lanes>(top);
+    top = top == limit ? 0u : top;
+  }
+  float near = 0.0f;  // closer than this needs fp64
+  if (General && delta > 0.0f && limit) {
+    const float at = key_value(limit);
+    near = delta + 0x1p-21f * fabsf(at);
+    limit = key32(at - near);
+  }
+  limit = umax(limit, 1u);
+
+  // the candidates
+  if (l < 16) sh.sel[r][l] = -1;
+  int mine = 0, n;
+#pragma unroll
+  for (int i = 0; i < N; ++i) mine += key[i] >= limit;
+  int at = row_before<Lanes>(mine, n);
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (key[4 * j + q] >= limit) {
+        const int e = 4 * Lanes * j + 4 * l + q;
+        if (at < kMaxCand) sh.cand[r][at] = {key[4 * j + q], v[4 * j + q], General && a.bias ? a.bias[e] : 0.0f, e};
+        ++at;
+      }
+  wave_sync();
+  bad |= n > kMaxCand;
+  n = n < kMaxCand ? n : kMaxCand;
+  for (int i = l; i < n; i += Lanes) {
+    const Candidate me = sh.cand[r][i];
+    int rank = 0;
+    bool close = false;
+    for (int h = 0; h < n; ++h) {
+      const Candidate o = sh.cand[r][h];
+      rank += o.key > me.key || (o.key == me.key && o.e < me.e);
+      if (General && delta > 0.0f)
+        close |= h != i && fabsf(key_value(o.key) - key_value(me.key)) <= near && (o.l != me.l || o.b != me.b);
+    }
+    if (rank < k) {
+      sh.sel[r][rank] = me.e;
+      bad |= close;
+    }
+  }
+  const bool again = row_any<Lanes>(bad && live);
+  const uint64_t rows_again = __ballot(again);
+  if (rows_again) {
+    wave_sync();
+    for (int s = 0; s < kRows; ++s)
+      if ((rows_again >> (s * Lanes)) & 1)
+        route_row_exact(a, t0 + wave * kRows + s, (uint64_t*)buffer, sh.sel[wave * kRows + s]);
+  }
+  wave_sync();
+
+  // the weights: lane j of the row has slot j
+  const int e = live && l < k ? sh.sel[r][l] : -1;
+  const bool has = e >= 0;
+  const float lg = has ? row[e] : -INFINITY;
+  float w;
+  if (a.sigmoid) {
+    w = has ? sigmoid_of(lg) : 0.0f;
+    if (a.renorm) w = w / (row_sum<Lanes>(w) + kDenom);
+  } else if (a.renorm) {
+    // (a NaN has to reach the whole row; fmaxf leaves it out)
+    const float top_l = row_max<Lanes>(lg);
+    w = has ? expf(lg - top_l) : 0.0f;
+    const float s = row_sum<Lanes>(w);
+    w = has ? w / s : 0.0f;
+  } else {
+    w = has ? soft.exp_of(lg) * soft.inv : 0.0f;
+  }
+  if (active && l < k) {
+    a.ids[t * k + l] = e;
+    a.weights[t * k + l] = has ? a.scale * w : 0.0f;
+    if (copy) copy[t * k + l] = e;
+  }
+  wave_sync();
+}
+
+template <int Lanes, int NV, bool Vec, bool General>
+__global__ __launch_bounds__(kThreads) void route_scored_kernel(ScoredArgs a) {
+  extern __shared__ __align__(16) float buffer[];
+  __shared__ RouteShared<Lanes> sh;
+  constexpr int kRows = kThreads / Lanes;
+  if (a.sorted_ids) {  // what the grouping kernel does not write
+    const int64_t first = blockIdx.x * (int64_t)kThreads + threadIdx.x, step = gridDim.x * (int64_t)kThreads;
+    for (int64_t i = first; i < a.cap; i += step) a.sorted_ids[i] = a.M * a.k;
+    for (int64_t i = first; i < a.cap / a.block_m; i += step) a.block_expert[i] = -1;
+  }
+  for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < a.M; t0 += (int64_t)gridDim.x * kRows)
+    route_rows<Lanes, NV, Vec, General>(a, t0, sh, buffer, nullptr);
+}
+
+// Up to 16 rows: routing and grouping in one workgroup and one launch.
+template <int Lanes, int NV, bool Vec, bool General>
+__global__ __launch_bounds__(kThreads) void route_scored_small_kernel(ScoredArgs a) {
+  extern __shared__ __align__(16) float buffer[];
+  __shared__ RouteShared<Lanes> sh;
+  __shared__ SmallRoute small;
+  constexpr int kRows = kThreads / Lanes;
+  const int tid = threadIdx.x, MK = a.M * a.k;
+  if (tid < (a.E + 31) / 32) small.bits[tid] = 0u;
+  for (int64_t t0 = 0; t0 < a.M; t0 += kRows) route_rows<Lanes, NV, Vec, General>(a, t0, sh, buffer, small.ids);
+  const int nd = small_group<kThreads, true>(small, MK, a.E);
+  const int bm = a.block_m;
+  for (int64_t i = tid; i < a.cap; i += kThreads) {
+    const int b = (int)(i / bm), p = (int)(i % bm);
+    a.sorted_ids[i] = b < nd && p < kSmallMaxTokens ? small.blk_rows[b][p] : MK;
+  }
+  for (int64_t b = tid; b < a.cap / bm; b += kThreads) a.block_expert[b] = b < nd ? small.blk_e[b] : -1;
+  for (int x = tid; x <= a.E; x += kThreads) a.offsets[x] = bm * (x < a.E ? small_rank(small, x) : nd);
+  if (tid == 0) *a.npp = bm * nd;
+}
+
+// fn(Lanes, NV, Vec) for the row width
+template <typename F>
+void by_width(int E, bool vec, F fn) {
+  auto go = [&](auto lanes, auto nv) { vec ? fn(lanes, nv, std::true_type{}) : fn(lanes, nv, std::false_type{}); };
+  auto row16 = [&](auto nv) { go(std::integral_constant<int, 16>{}, nv); };
+  if (E <= 64) row16(std::integral_constant<int, 1>{});
+  else if (E <= 128) row16(std::integral_constant<int, 2>{});
+  else if (E <= 256) row16(std::integral_constant<int, 4>{});
+  else if (E <= 384) row16(std::integral_constant<int, 6>{});
+  else if (E <= 512) row16(std::integral_constant<int, 8>{});
+  else go(std::integral_constant<int, 32>{}, std::integral_constant<int, 8>{});
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// ---- backward ---------------------------------------------------------------
+
+// The slots' values lie in lanes 0..k of the row. Full (softmax over all
+// experts): every logit has a gradient. Otherwise only the kept ones have;
+// the rest of the row is grad_base or zeros, and is not touched in place.
+// The slots' values reach the row's order through LDS.
+template <int Lanes, int NV, bool Vec, bool Full>
+__global__ __launch_bounds__(kThreads) void route_scored_backward_kernel(ScoredBackwardArgs a) {
+  extern __shared__ __align__(16) float buffer[];
+  constexpr int N = 4 * NV, kRows = kThreads / Lanes;
+  const int l = threadIdx.x % Lanes, r = threadIdx.x / Lanes;
+  const int E = a.E, k = a.k, pitch = (E + 3) & ~3;
+  float* mine = buffer + r * pitch;
+  const bool in_place = a.base == a.grad;
+  for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < a.M; t0 += (int64_t)gridDim.x * kRows) {
+    const int64_t t = t0 + r;
+    const bool active = t < a.M;
+    const float* row = a.logits + (active ? t : (int64_t)a.M - 1) * E;
+    float v[N];
+    if constexpr (Full) load_row<Lanes, NV, Vec>(row, E, l, v);
+    const int e = active && l < k ? a.ids[t * k + l] : -1;
+    const bool has = (unsigned)e < (unsigned)E;
+    const float g = has ? a.scale * a.dweights[t * k + l] : 0.0f;
+    const float lg = has ? row[e] : -INFINITY;
+    const bool any = row_any<Lanes>(has);
+    RowSoftmax soft{0.0f, 0.0f, 0.0f};
+    float d;  // what goes to the slot's expert
+    float dot = 0.0f;
+    if constexpr (Full) {
+      soft = row_softmax<Lanes>(v);
+      dot = row_sum<Lanes>(has ? g * (soft.exp_of(lg) * soft.inv) : 0.0f);
+      d = g;
+    } else if (!a.sigmoid) {
+      const float top = row_max<Lanes>(lg);
+      const float x = has ? expf(lg - top) : 0.0f;
+      const float s = row_sum<Lanes>(x);
+      const float w = has ? x / s : 0.0f;
+      d = w * (g - row_sum<Lanes>(g * w));
+    } else {
+      const float x = expf(-fabsf(lg)), y = 1.0f + x;
+      const float s = has ? (lg >= 0.0f ? 1.0f : x) / y : 0.0f;
+      const float slope = has ? x / (y * y) : 0.0f;
+      if (a.renorm) {
+        const float total = row_sum<Lanes>(s) + kDenom;
+        d = slope / total * (g - row_sum<Lanes>(g * (s / total)));
+      } else {
+        d = slope * g;
+      }
+    }
+    if (!Full && in_place) {
+      if (has) a.grad[t * E + e] += d;
+      continue;
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = 4 * Lanes * j + 4 * l;
+      if (c < E) *(float4*)(mine + c) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+    wave_sync();
+    if (has) mine[e] = d;
+    wave_sync();
+    if (active) {
+      const float* base = a.base ? a.base + t * E : nullptr;
+      float* grad = a.grad + t * E;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = 4 * Lanes * j + 4 * l;
+        float o[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          o[q] = c < E ? mine[c + q] : 0.0f;
+          if constexpr (Full) o[q] = any ? soft.exp_of(v[4 * j + q]) * soft.inv * (o[q] - dot) : 0.0f;
+        }
+        if constexpr (Vec) {
+          if (c < E) {
+            float4 b = base ? *(const float4*)(base + c) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            *(float4*)(grad + c) = make_float4(o[0] + b.x, o[1] + b.y, o[2] + b.z, o[3] + b.w);
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (c + q < E) grad[c + q] = o[q] + (base ? base[c + q] : 0.0f);
+        }
+      }
+    }
+    wave_sync();
+  }
+}
+
+// Workgroups: enough for the rows, at most 2^20 (a grid has fewer than 2^32 threads).
+unsigned grid_for(int64_t M, int rows) {
+  const int64_t n = ceil_div(M, rows);
+  return (unsigned)(n < (1 << 20) ? n : (1 << 20));
+}
+
+}  // namespace
+
+hipError_t launch_route_scored(const ScoredArgs& a, hipStream_t stream) {
+  const bool grouping = a.sorted_ids != nullptr;
+  const bool small = grouping && a.M <= kSmallMaxTokens;
+  const bool general = a.bias || a.top_groups < a.groups;
+  by_width(a.E, a.E % 4 == 0 && aligned16(a.logits) && (!a.bias || aligned16(a.bias)), [&](auto lanes, auto nv, auto vec) {
+    constexpr int L = decltype(lanes)::value, NV = decltype(nv)::value;
+    constexpr bool V = decltype(vec)::value;
+    const unsigned lds = (unsigned)(row_buffer_bytes(L, general, a.E) * kWaves);
+    const unsigned grid = small ? 1u : grid_for(a.M, kThreads / L);
+    if (small) {
+      general ? route_scored_small_kernel<L, NV, V, true><<<grid, kThreads, lds, stream>>>(a)
+              : route_scored_small_kernel<L, NV, V, false><<<grid, kThreads, lds, stream>>>(a);
+    } else {
+      general ? route_scored_kernel<L, NV, V, true><<<grid, kThreads, lds, stream>>>(a)
+              : route_scored_kernel<L, NV, V, false><<<grid, kThreads, lds, stream>>>(a);
+    }
+  });
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess || small || !grouping) return err;
+  return launch_align(a.ids, a.M * a.k, a.E, a.block_m, a.sorted_ids, a.block_expert, a.offsets, a.npp, stream);
+}
+
+hipError_t launch_route_scored_backward(const ScoredBackwardArgs& a, hipStream_t stream) {
+  const bool full = !a.sigmoid && !a.renorm;
+  const bool vec = a.E % 4 == 0 && aligned16(a.logits) && aligned16(a.grad) && (!a.base || aligned16(a.base));
+  by_width(a.E, vec, [&](auto lanes, auto nv, auto v) {
+    constexpr int L = decltype(lanes)::value, NV = decltype(nv)::value;
+    constexpr bool V = decltype(v)::value;
+    const unsigned lds = (unsigned)(((a.E + 3) & ~3) * 4 * (kThreads / L));
+    const unsigned grid = grid_for(a.M, kThreads / L);
+    full ? route_scored_backward_kernel<L, NV, V, true><<<grid, kThreads, lds, stream>>>(a)
+         : route_scored_backward_kernel<L, NV, V, false><<<grid, kThreads, lds, stream>>>(a);
+  });
+  return hipGetLastError();
+}
+
+}  // namespace moe

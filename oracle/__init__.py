@@ -405,3 +405,140 @@ def lora_backward(dout, x, ids, h, a, b, scales, dx_base):
         da[i] = dh.T @ x[rows]
         db[i] = float(scales[i]) * (dout[rows].T @ h[rows])
     return dx, da, db
+
+
+# ------------------------------------------------------------------ between the layer and the rest of a model
+def scores(row, scoring):
+    """Scores of one token's logits in float64; -inf gives 0."""
+    if scoring == "sigmoid":
+        with np.errstate(over="ignore"):
+            return 1.0 / (1.0 + np.exp(-row))
+    return _softmax_or_zero(row)
+
+
+def _rank_key(v):
+    """Sorts the highest value first, NaN before everything."""
+    return (0, 0.0) if np.isnan(v) else (1, -v)
+
+
+def route_scored(logits, k, scoring="softmax", bias=None, n_groups=1, top_groups=1, group_top=1, renormalise=True,
+                 scale=1.0, valid=None):
+    """(ids [M, k], weights [M, k]) in float64: an expert whose logit or bias is
+    -inf is absent, a group's score sums what is present of its group_top
+    highest, slots without an expert are -1 with weight 0."""
+    logits = np.asarray(logits, np.float64)
+    M, E = logits.shape
+    size = E // n_groups
+    ids, w = np.full((M, k), -1, np.int64), np.zeros((M, k))
+    for t in range(M):
+        if valid is not None and not valid[t]:
+            continue
+        row = logits[t]
+        b = np.zeros(E) if bias is None else np.asarray(bias, np.float64)
+        s = scores(row, scoring)
+        c = s + b
+        there = [e for e in range(E) if row[e] != -np.inf and b[e] != -np.inf]
+        if top_groups < n_groups:
+            best = []
+            for g in range(n_groups):
+                inside = sorted((c[e] for e in there if e // size == g), key=_rank_key)
+                if inside:
+                    best.append((_rank_key(sum(inside[:group_top])), g))
+            chosen = {g for _, g in sorted(best)[:top_groups]}
+            there = [e for e in there if e // size in chosen]
+        order = sorted(there, key=lambda e: (_rank_key(row[e] if bias is None else c[e]), e))[:k]
+        n = len(order)
+        ids[t, :n] = order
+        if not n:
+            continue
+        kept = s[order]
+        if renormalise:
+            kept = _softmax_or_zero(row[order]) if scoring == "softmax" else kept / (kept.sum() + 1e-20)
+        w[t, :n] = scale * kept
+    return ids, w
+
+
+def align_dropped(topk_ids, E, block_m):
+    """align of the assignments that have an expert; the sentinel stays M*k."""
+    ids = np.asarray(topk_ids, np.int64).reshape(-1)
+    rows, blocks, offsets = [], [], [0]
+    for e in range(E):
+        mine = np.nonzero(ids == e)[0].tolist()
+        pad = -len(mine) % block_m
+        rows += mine + [ids.size] * pad
+        blocks += [e] * ((len(mine) + pad) // block_m)
+        offsets.append(len(rows))
+    return np.array(rows, np.int64), np.array(blocks, np.int64), np.array(offsets, np.int64)
+
+
+def route_scored_backward(logits, ids, grad_weights, scoring="softmax", renormalise=True, scale=1.0, base=None):
+    """(gradient [M, E], magnitudes of its terms) in float64."""
+    logits = np.asarray(logits, np.float64)
+    M, E = logits.shape
+    grad, mag = np.zeros((M, E)), np.zeros((M, E))
+    for t in range(M):
+        at = [j for j in range(ids.shape[1]) if 0 <= ids[t, j] < E]
+        if not at:
+            continue
+        e = ids[t, at].astype(np.int64)
+        g = scale * np.asarray(grad_weights[t, at], np.float64)
+        if scoring == "softmax":
+            if renormalise:
+                p = np.zeros(E)
+                p[e] = _softmax_or_zero(logits[t, e])
+            else:
+                p = _softmax_or_zero(logits[t])
+            full = np.zeros(E)
+            full[e] = g
+            grad[t] = p * (full - float(full @ p))
+            mag[t] = p * (np.abs(full) + float(np.abs(full) @ p))
+        else:
+            with np.errstate(over="ignore"):
+                s, slope = 1 / (1 + np.exp(-logits[t, e])), 1 / (2 + np.exp(-logits[t, e]) + np.exp(logits[t, e]))
+            if renormalise:
+                total = s.sum() + 1e-20
+                grad[t, e] = slope / total * (g - float(g @ s) / total)
+                mag[t, e] = slope / total * (np.abs(g) + float(np.abs(g) @ s) / total)
+            else:
+                grad[t, e] = slope * g
+                mag[t, e] = slope * np.abs(g)
+    if base is not None:
+        grad = grad + base
+    return grad, mag
+
+
+def e4m3(v):
+    """float64 values rounded to OCP e4m3 (nearest, ties to even, 448 at most), as float64."""
+    v = np.asarray(v, np.float64)
+    a = np.minimum(np.abs(v), 448.0)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        step = np.exp2(np.maximum(np.floor(np.log2(a)), -6.0) - 3.0)
+    step = np.where(a > 0, step, 2.0 ** -9)
+    return np.copysign(np.minimum(np.round(a / step) * step, 448.0), v)
+
+
+def rms_norm(h, w, eps):
+    """(y, r) in float64: y = h * r * w, r = 1 / sqrt(mean(h^2) + eps) of each row."""
+    h, w = np.asarray(h, np.float64), np.asarray(w, np.float64)
+    r = 1.0 / np.sqrt((h * h).mean(1) + eps)
+    return h * r[:, None] * w, r
+
+
+def quantise(y, group):
+    """(e4m3 values, float32 scales) of float64 y, `group` columns a scale."""
+    M, N = y.shape
+    parts = y.reshape(M, N // group, group)
+    s = np.maximum((np.abs(parts).max(2) / 448.0).astype(np.float32), np.float32(2.0 ** -126))
+    return e4m3(parts / s.astype(np.float64)[:, :, None]).reshape(M, N), s
+
+
+def rms_norm_backward(dy, h, r, w, dres=None):
+    """(dh, dw, magnitudes of dh's and of dw's terms) in float64."""
+    dy, h, r, w = (np.asarray(v, np.float64) for v in (dy, h, r, w))
+    n = h * r[:, None]
+    u = dy * w
+    dh = r[:, None] * (u - n * (u * n).mean(1, keepdims=True))
+    mag = r[:, None] * (np.abs(u) + np.abs(n) * np.abs(u * n).mean(1, keepdims=True))
+    if dres is not None:
+        dh, mag = dh + dres, mag + np.abs(dres)
+    return dh, (dy * n).sum(0), mag, np.abs(dy * n).sum(0)
