@@ -6,14 +6,15 @@
 //
 // Finding the k highest without k passes over the row: the k-th highest of the
 // lanes' own maxima (k exchanges within the row) is a threshold that at least k
-// values reach and few others do (for 384 values and k = 8 some 11). These
-// candidates go to LDS, where each is ranked by counting the higher ones.
+// values reach and few others do (for 384 values and k = 8 some 11). The places
+// of these candidates go to LDS, where each is ranked by counting the higher ones.
 //
-// The choice is that of c in fp64, but no row needs fp64 for that: where fp32
-// values that decide the choice are closer than their error bound, and where
-// something is not finite or the candidates are too many, the wave computes
-// the row again in fp64 (route_row_exact). Equal logits with equal biases need
-// no such decision (the lower expert goes first).
+// The choice is that of c in fp64, but hardly a row needs fp64 for that: only
+// where fp32 values that decide the choice are closer than their error bound are
+// the candidates' c computed again in fp64. (Equal logits with equal biases need
+// no such decision: the lower expert goes first.) Where that decides between
+// groups, or something is not finite, or the candidates are too many, the wave
+// computes the whole row again in fp64 (route_row_exact).
 #include <type_traits>
 
 #include "device_common.h"
@@ -75,11 +76,7 @@ __device__ __forceinline__ bool row_any(bool b) {
   return Lanes == 32 ? (uint32_t)m != 0 : (m & 0xffffu) != 0;
 }
 
-// Order-preserving keys: absent (-inf) 0, NaN the highest.
-__device__ __forceinline__ uint32_t key32(float v) {
-  const uint32_t k = order_key(v);
-  return v == -INFINITY ? 0u : v != v ? 0xFFFFFFFFu : k;
-}
+// Order-preserving keys: NaN the highest; 0 is below them all.
 __device__ __forceinline__ uint64_t key64(double v) {
   const uint64_t u = (uint64_t)__double_as_longlong(v + 0.0);
   const uint64_t k = (u >> 63) ? ~u : (u | 0x8000000000000000ull);
@@ -121,20 +118,25 @@ __device__ __forceinline__ float sigmoid_of(float l) {  // to the last bits for 
   return l != l ? l : (l >= 0.0f ? 1.0f : e) / (1.0f + e);
 }
 
-struct Candidate {
-  uint32_t key;
-  float l, b;
-  int e;
+// Scores as the fast path computes them.
+__device__ __forceinline__ float fast_sigmoid(float l) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * l));
+}
+
+struct Chosen {
+  int e;    // -1: none
+  float l;  // its logit
 };
 
-// One row's choice in fp64 by the whole wave: sel[0..k) gets the experts (-1:
-// none left). keys: E 64-bit words of this wave.
-__device__ void route_row_exact(const ScoredArgs& a, int64_t t, uint64_t* keys, int* sel) {
-  const int lane = threadIdx.x & 63, E = a.E;
-  const float* row = a.logits + t * E;
-  const bool grouped = a.top_groups < a.groups;
+// One row's choice in fp64 by the whole wave, to sel[0..k). keys: E 64-bit words
+// of this wave. (Not inlined: its registers would halve the waves of the kernel.)
+__device__ __attribute__((noinline)) void route_row_exact(const float* row, const float* bias, int E, int k,
+                                                          bool sigmoid, int G, int top_groups, int group_top,
+                                                          uint64_t* keys, Chosen* sel) {
+  const int lane = threadIdx.x & 63;
+  const bool grouped = top_groups < G;
   double m = -INFINITY, sum = 1.0;
-  if (!a.sigmoid) {
+  if (!sigmoid) {
 #pragma unroll 1
     for (int e = lane; e < E; e += 64) m = fmax(m, (double)row[e]);
 #pragma unroll 1
@@ -147,93 +149,108 @@ __device__ void route_row_exact(const ScoredArgs& a, int64_t t, uint64_t* keys, 
   }
 #pragma unroll 1
   for (int e = lane; e < E; e += 64) {
-    const double l = row[e], b = a.bias ? (double)a.bias[e] : 0.0;
+    const double l = row[e], b = bias ? (double)bias[e] : 0.0;
     uint64_t key = 0;
     if (l != -INFINITY && b != -INFINITY) {
-      if (!a.bias && !grouped) key = key64(l);
-      else key = key64((a.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - m) / sum) + b);
+      if (!bias && !grouped) key = key64(l);
+      else key = key64((sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - m) / sum) + b);
     }
     keys[e] = key;
   }
   wave_sync();
   if (grouped) {
-    const int G = a.groups, gs = E / G;
-    uint64_t mine = 0;  // lane g: the key of group g's score
-#pragma unroll 1
-    for (int g = 0; g < G; ++g) {
-      uint64_t m1 = 0, m2 = 0;
-#pragma unroll 1
-      for (int i = lane; i < gs; i += 64) {
-        const uint64_t x = keys[g * gs + i];
+    const int gs = E / G;
+    // P lanes a group: lane g P + i takes every P-th of its keys from the i-th on
+    int P = 1;
+    while (2 * P * G <= 64) P *= 2;
+    uint64_t m1 = 0, m2 = 0;
+    if (lane < G * P) {
+#pragma unroll 4
+      for (int i = lane & (P - 1); i < gs; i += P) {
+        const uint64_t x = keys[lane / P * gs + i];
         m2 = x > m1 ? m1 : (x > m2 ? x : m2);
         m1 = x > m1 ? x : m1;
       }
-#pragma unroll 1
-      for (int d = 32; d; d >>= 1) {
-        const uint64_t o1 = __shfl_xor((unsigned long long)m1, d, 64), o2 = __shfl_xor((unsigned long long)m2, d, 64);
-        const uint64_t low = o1 > m1 ? m1 : o1;
-        m2 = m2 > o2 ? m2 : o2;
-        m2 = low > m2 ? low : m2;
-        m1 = o1 > m1 ? o1 : m1;
-      }
-      const uint64_t score = a.group_top == 2 && m2 ? key64((m1 == ~0ull ? NAN : key64_value(m1)) +
-                                                            (m2 == ~0ull ? NAN : key64_value(m2)))
-                                                    : m1;
-      if (lane == g) mine = score;
     }
-    int rank = 0;
 #pragma unroll 1
+    for (int d = 1; d < P; d *= 2) {
+      const uint64_t o1 = __shfl_xor((unsigned long long)m1, d, 64), o2 = __shfl_xor((unsigned long long)m2, d, 64);
+      const uint64_t low = o1 > m1 ? m1 : o1;
+      m2 = m2 > o2 ? m2 : o2;
+      m2 = low > m2 ? low : m2;
+      m1 = o1 > m1 ? o1 : m1;
+    }
+    const uint64_t score = group_top == 2 && m2 ? key64((m1 == ~0ull ? NAN : key64_value(m1)) +
+                                                        (m2 == ~0ull ? NAN : key64_value(m2)))
+                                                : m1;
+    const uint64_t mine = __shfl((unsigned long long)score, lane * P & 63, 64);  // lane g: group g's
+    int rank = 0;
     for (int g = 0; g < G; ++g) {
       const uint64_t o = __shfl((unsigned long long)mine, g, 64);
       rank += o > mine || (o == mine && g < lane);
     }
-    const uint64_t chosen = __ballot(lane < G && mine && rank < a.top_groups);
+    const uint64_t chosen = __ballot(lane < G && mine && rank < top_groups);
 #pragma unroll 1
     for (int e = lane; e < E; e += 64) {
       uint64_t key = keys[e];
       if (!((chosen >> (e / gs)) & 1)) key = 0;
-      else if (key && !a.bias) key = key64((double)row[e]);
+      else if (key && !bias) key = key64((double)row[e]);
       keys[e] = key;
     }
   }
 #pragma unroll 1
-  for (int r = 0; r < a.k; ++r) {
+  for (int r = 0; r < k; ++r) {
     uint64_t best = 0;
     int at = E;
-#pragma unroll 1
-    for (int e = lane; e < E; e += 64)
-      if (keys[e] > best) best = keys[e], at = e;
-#pragma unroll 1
-    for (int d = 32; d; d >>= 1) {
-      const uint64_t o = __shfl_xor((unsigned long long)best, d, 64);
-      const int oat = __shfl_xor(at, d, 64);
-      const bool take = o > best || (o == best && oat < at);
-      best = take ? o : best;
-      at = take ? oat : at;
+#pragma unroll 4
+    for (int e = lane; e < E; e += 64) {
+      const uint64_t x = keys[e];
+      at = x > best ? e : at;
+      best = x > best ? x : best;
     }
-    if (lane == 0) sel[r] = best ? at : -1;
-    if (best && (at & 63) == lane) keys[at] = 0;
+    uint32_t hi = (uint32_t)(best >> 32), lo = (uint32_t)best;
+    wave_max_pair(hi, lo);
+    const bool top = (uint32_t)(best >> 32) == hi && (uint32_t)best == lo;
+    const int e = (int)wave_min_u32(top ? (uint32_t)at : 0xFFFFFFFFu);
+    const bool none = (hi | lo) == 0;
+    if (lane == 0) sel[r] = none ? Chosen{-1, -INFINITY} : Chosen{e, row[e]};
+    if (!none && (e & 63) == lane) keys[e] = 0;
   }
   wave_sync();
 }
 
-// LDS of one wave beside `Candidate`s: the group values of its rows, or the
-// 64-bit keys of one row.
+// Dynamic LDS of one wave: the group values of its rows, or the 64-bit keys of
+// one row.
 __host__ __device__ constexpr int64_t row_buffer_bytes(int lanes, bool general, int E) {
   return (int64_t)E * (general ? (64 / lanes) * 4 : 8);
 }
 
-template <int Lanes>
+// A candidate: its expert and what it is ordered by, in one LDS read; with a
+// bias also what c is computed from.
+struct Candidate {
+  float c;
+  int e;
+};
+struct BiasedCandidate {
+  float c;
+  int e;
+  float l, b;
+};
+
+template <int Lanes, bool General>
 struct RouteShared {
-  Candidate cand[kThreads / Lanes][kMaxCand];
-  int sel[kThreads / Lanes][16];
-  float groups[kThreads / Lanes][64];
+  static constexpr int kRows = kThreads / Lanes;
+  Chosen sel[kRows][16];
+  std::conditional_t<General, BiasedCandidate, Candidate> cand[kRows][kMaxCand];
+  uint64_t c64[General ? kRows : 1][kMaxCand];  // c in fp64
+  float groups[General ? kRows : 1][64];
 };
 
 // Routes the rows t0 + wave * (64 / Lanes) + lane / Lanes of this workgroup.
 // General: with a bias or groups. copy: also gets the ids (LDS), or null.
 template <int Lanes, int NV, bool Vec, bool General>
-__device__ __forceinline__ void route_rows(const ScoredArgs& a, int64_t t0, RouteShared<Lanes>& sh, float* buffer,
+__device__ __forceinline__ void route_rows(const ScoredArgs& a, int64_t t0, RouteShared<Lanes, General>& sh,
+                                           float* buffer,
                                            int32_t* copy) {
   constexpr int N = 4 * NV, kRows = 64 / Lanes;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane % Lanes, sub = lane / Lanes;
@@ -243,71 +260,55 @@ __device__ __forceinline__ void route_rows(const ScoredArgs& a, int64_t t0, Rout
   const float* row = a.logits + (active ? t : (int64_t)a.M - 1) * E;
   const int r = wave * kRows + sub;
   buffer += row_buffer_bytes(Lanes, General, E) / 4 * wave;
-  float v[N];
+  float v[N];  // the logits, then what the experts are ordered by
   load_row<Lanes, NV, Vec>(row, E, l, v);
   const bool live = active && (!a.valid || a.valid[t]);
   RowSoftmax soft{0.0f, 0.0f, 0.0f};
   if (!a.sigmoid && (General || !a.renorm)) soft = row_softmax<Lanes>(v);
+  auto expert_of = [&](int i) { return 4 * Lanes * (i >> 2) + 4 * l + (i & 3); };
+  auto inside = [&](int i) { return expert_of(Vec ? i & ~3 : i) < E; };  // (Vec: E % 4 == 0)
+  auto fast_score = [&](float x) { return a.sigmoid ? fast_sigmoid(x) : soft.exp_of(x) * soft.inv; };
 
+  // rows that need the exact path: NaN, and with scores in the choice whatever is not finite
   bool bad = false;
-  uint32_t key[N];
-  float delta = 0.0f;  // twice the error of a score
-  if constexpr (!General) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) key[i] = key32(v[i]);
-  } else {
+  for (int i = 0; i < N; i += 2) bad |= __builtin_isunordered(v[i], v[i + 1]);
+  float near = 0.0f;     // closer values need fp64
+  float largest = 0.0f;  // of a lane's |l| and |c|
+  if constexpr (General) {
     const bool grouped = a.top_groups < a.groups;
-    float c[N];
-    // fp32 errors: a sigmoid is off by some 5 roundings of itself and by
-    // |l| s (1 - s) < 0.23 of them; a softmax value p = pmax e^-x by (1.5 x + 50)
-    // p, at most 50 pmax (x from the exponent, the rest from the row's sum)
-    delta = a.sigmoid ? 0x1p-19f : 0x1p-17f * soft.inv;
-    // scores where they are needed, then c
-    if (a.bias || (grouped && a.group_top == 2)) {
-      if (a.sigmoid) {
+    // fp32 errors in roundings of 2^-24: a sigmoid's are (1 - s) s (1.3 |l| + 2) + 3 s
+    // < 4; a softmax value's p = pmax e^-x are (1.5 x + 50) p < 50 pmax (x from the
+    // exponent, the rest from the row's sum). c adds |c|. Twice that is `near`.
+    const float score_error = a.sigmoid ? 0x1p-22f : 0x1p-18f * soft.inv;
 #pragma unroll
-        for (int i = 0; i < N; ++i) c[i] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * v[i]));
-      } else {
+    for (int i = 0; i < N; ++i) largest = fmaxf(largest, inside(i) ? fabsf(v[i]) : 0.0f);
+    if (a.bias) {
+      float b[N];
+      load_row<Lanes, NV, Vec>(a.bias, E, l, b);
 #pragma unroll
-        for (int i = 0; i < N; ++i) c[i] = soft.exp_of(v[i]) * soft.inv;
+      for (int i = 0; i < N; ++i) {
+        v[i] = fast_score(v[i]) + b[i];
+        largest = fmaxf(largest, inside(i) ? fabsf(v[i]) : 0.0f);
+        bad |= __builtin_isunordered(b[i], b[i]);
       }
-      if (a.bias) {
-        float b[N];
-        load_row<Lanes, NV, Vec>(a.bias, E, l, b);
-#pragma unroll
-        for (int i = 0; i < N; ++i) c[i] = c[i] + b[i];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) c[i] = v[i];
-      delta = 0.0f;
+      near = 2.0f * score_error;
     }
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int e = 4 * Lanes * j + 4 * l + q;
-        bad |= e < E && !(fabsf(v[4 * j + q]) < 1e30f && fabsf(c[4 * j + q]) < 1e30f);
-      }
-    uint64_t chosen = ~0ull;
-    const int gs = E / a.groups;
-    const uint32_t magic = (1u << 20) / (uint32_t)gs + 1u;  // e / gs = e * magic >> 20 for e < 1024
+    bad |= !(largest < 1e30f);
     if (grouped) {
+      const int gs = E / a.groups, G = a.groups;
       float* mine = buffer + sub * E;
+      const bool raw = a.bias || a.group_top == 1;  // (the highest logit has the highest score)
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int e = 4 * Lanes * j + 4 * l;
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (e + q < E) mine[e + q] = c[4 * j + q];
-      }
+      for (int i = 0; i < N; ++i)
+        if (inside(i)) mine[expert_of(i)] = raw ? v[i] : fast_score(v[i]);
       wave_sync();
       // P lanes a group
-      const int G = a.groups;
       int P = 1;
       while (P < 8 && 2 * P * G <= Lanes) P *= 2;
       for (int g = l / P; g < G; g += Lanes / P) {
         float m1 = -INFINITY, m2 = -INFINITY;
+#pragma unroll 4
         for (int i = l % P; i < gs; i += P) {
           const float x = mine[g * gs + i];
           m2 = fmaxf(m2, fminf(m1, x));
@@ -324,12 +325,13 @@ __device__ __forceinline__ void route_rows(const ScoredArgs& a, int64_t t0, Rout
         sh.groups[r][g] = a.group_top == 2 ? m1 + m2 : m1;
       }
       wave_sync();
-      chosen = 0;
+      uint64_t chosen = 0;
       float in = INFINITY, out = -INFINITY;
       for (int g0 = 0; g0 < G; g0 += Lanes) {
         const int g = g0 + l;
         const float s = g < G ? sh.groups[r][g] : 0.0f;
         int rank = 0;
+#pragma unroll 4
         for (int h = 0; h < G; ++h) {
           const float o = sh.groups[r][h];
           rank += o > s || (o == s && h < g);
@@ -342,68 +344,117 @@ __device__ __forceinline__ void route_rows(const ScoredArgs& a, int64_t t0, Rout
       }
       in = -row_max<Lanes>(-in);
       out = row_max<Lanes>(out);
-      if (delta > 0.0f) bad |= !(in - out > 2.0f * delta + 0x1p-21f * fmaxf(fabsf(in), fabsf(out)));
+      if (a.bias || a.group_top == 2)
+        bad |= !(in - out > 4.0f * score_error + 0x1p-21f * fmaxf(fabsf(in), fabsf(out)));
+      const uint32_t magic = (1u << 20) / (uint32_t)gs + 1u;  // e / gs = e * magic >> 20 for e < 1024
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (!((chosen >> (((uint32_t)expert_of(i) * magic >> 20) & 63)) & 1)) v[i] = -INFINITY;
     }
-    if (!a.bias) delta = 0.0f;  // the experts are then ordered by their logits
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int e = 4 * Lanes * j + 4 * l + q;
-        const uint32_t kk = key32(a.bias ? c[4 * j + q] : v[4 * j + q]);
-        key[4 * j + q] = e < E && ((chosen >> ((uint32_t)e * magic >> 20)) & 1) ? kk : 0u;
-      }
+    for (int i = 0; i < N; ++i)
+      if (!inside(i)) v[i] = -INFINITY;
   }
 
-  // the threshold
-  uint32_t top = key[0];
+  // the threshold (as an integer key: its maxima are one instruction an exchange)
+  float top = v[0];
 #pragma unroll
-  for (int i = 1; i < N; ++i) top = umax(top, key[i]);
-  uint32_t limit = 0;
+  for (int i = 1; i < N; ++i) top = fmaxf(top, v[i]);
+  uint32_t top_key = order_key(top), limit_key = 0;
 #pragma unroll 1
   for (int i = 0; i < k; ++i) {
-    limit = row_max_u32<Lanes>(top);
-    top = top == limit ? 0u : top;
+    limit_key = row_max_u32<Lanes>(top_key);
+    top_key = top_key == limit_key ? 0u : top_key;
   }
-  float near = 0.0f;  // closer than this needs fp64
-  if (General && delta > 0.0f && limit) {
-    const float at = key_value(limit);
-    near = delta + 0x1p-21f * fabsf(at);
-    limit = key32(at - near);
+  float limit = limit_key ? key_value(limit_key) : -INFINITY;
+  if (General && a.bias) {
+    // (no limit: fewer than k lanes have a value, and every value is a candidate)
+    near += 0x1p-22f * (limit == -INFINITY ? row_max<Lanes>(largest) : fabsf(limit));
+    limit -= near;
   }
-  limit = umax(limit, 1u);
+  limit = fmaxf(limit, -3.402823466e38f);
 
   // the candidates
-  if (l < 16) sh.sel[r][l] = -1;
-  int mine = 0, n;
+  if (l < 16) sh.sel[r][l] = {-1, -INFINITY};
+  uint32_t mask = 0;  // bit N - 1 - i: value i
 #pragma unroll
-  for (int i = 0; i < N; ++i) mine += key[i] >= limit;
-  int at = row_before<Lanes>(mine, n);
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (key[4 * j + q] >= limit) {
-        const int e = 4 * Lanes * j + 4 * l + q;
-        if (at < kMaxCand) sh.cand[r][at] = {key[4 * j + q], v[4 * j + q], General && a.bias ? a.bias[e] : 0.0f, e};
-        ++at;
-      }
+  for (int i = 0; i < N; ++i) mask = mask + mask + (v[i] >= limit ? 1u : 0u);
+  int n;
+  int at = row_before<Lanes>(__builtin_popcount(mask), n);
+  while (__any(mask)) {
+    const int bit = mask ? __builtin_ctz(mask) : 0;
+    if (mask && at < kMaxCand) sh.cand[r][at].e = expert_of(N - 1 - bit);
+    ++at;
+    mask &= mask - 1;
+  }
   wave_sync();
   bad |= n > kMaxCand;
   n = n < kMaxCand ? n : kMaxCand;
   for (int i = l; i < n; i += Lanes) {
-    const Candidate me = sh.cand[r][i];
+    auto& me = sh.cand[r][i];
+    const float x = row[me.e];
+    if constexpr (General) {
+      const float b = a.bias ? a.bias[me.e] : 0.0f;
+      me.l = x;
+      me.b = b;
+      me.c = a.bias ? fast_score(x) + b : x;
+    } else {
+      me.c = x;
+    }
+  }
+  wave_sync();
+  bool close = false;
+  for (int i = l; i < n; i += Lanes) {
+    const auto me = sh.cand[r][i];
     int rank = 0;
-    bool close = false;
+    bool beside = false;
+#pragma unroll 4
     for (int h = 0; h < n; ++h) {
-      const Candidate o = sh.cand[r][h];
-      rank += o.key > me.key || (o.key == me.key && o.e < me.e);
-      if (General && delta > 0.0f)
-        close |= h != i && fabsf(key_value(o.key) - key_value(me.key)) <= near && (o.l != me.l || o.b != me.b);
+      const auto o = sh.cand[r][h];
+      rank += (int)(o.c > me.c) | ((int)(o.c == me.c) & (int)(o.e < me.e));
+      if constexpr (General) beside |= (fabsf(o.c - me.c) <= near) & ((o.l != me.l) | (o.b != me.b));
     }
     if (rank < k) {
-      sh.sel[r][rank] = me.e;
-      bad |= close;
+      if constexpr (General) {
+        sh.sel[r][rank] = {me.e, me.l};
+        close |= beside;
+      } else {
+        sh.sel[r][rank] = {me.e, me.c};
+      }
+    }
+  }
+  if constexpr (General) if (a.bias && __any(close && live)) {  // the candidates again, in fp64
+    wave_sync();
+    double m = 0.0, sum = 1.0;
+    if (!a.sigmoid) {
+      float top_l = -INFINITY;
+#pragma unroll 1
+      for (int e = l; e < E; e += Lanes) top_l = fmaxf(top_l, row[e]);
+      m = row_max<Lanes>(top_l);
+      sum = 0.0;
+#pragma unroll 1
+      for (int e = l; e < E; e += Lanes) sum += exp((double)row[e] - m);
+#pragma unroll
+      for (int d = Lanes / 2; d; d >>= 1) sum += __shfl_xor(sum, d, 64);
+    }
+#pragma unroll 1
+    for (int i = l; i < n; i += Lanes) {
+      const int e = sh.cand[r][i].e;
+      const double x = sh.cand[r][i].l;
+      sh.c64[r][i] = key64((a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - m) / sum) + (double)a.bias[e]);
+    }
+    wave_sync();
+#pragma unroll 1
+    for (int i = l; i < n; i += Lanes) {
+      const uint64_t me = sh.c64[r][i];
+      const int e = sh.cand[r][i].e;
+      int rank = 0;
+#pragma unroll 1
+      for (int h = 0; h < n; ++h) {
+        const uint64_t o = sh.c64[r][h];
+        rank += o > me || (o == me && sh.cand[r][h].e < e);
+      }
+      if (rank < k) sh.sel[r][rank] = {e, sh.cand[r][i].l};
     }
   }
   const bool again = row_any<Lanes>(bad && live);
@@ -412,14 +463,16 @@ __device__ __forceinline__ void route_rows(const ScoredArgs& a, int64_t t0, Rout
     wave_sync();
     for (int s = 0; s < kRows; ++s)
       if ((rows_again >> (s * Lanes)) & 1)
-        route_row_exact(a, t0 + wave * kRows + s, (uint64_t*)buffer, sh.sel[wave * kRows + s]);
+        route_row_exact(a.logits + (t0 + wave * kRows + s) * E, a.bias, E, k, a.sigmoid, a.groups, a.top_groups,
+                        a.group_top, (uint64_t*)buffer, sh.sel[wave * kRows + s]);
   }
   wave_sync();
 
   // the weights: lane j of the row has slot j
-  const int e = live && l < k ? sh.sel[r][l] : -1;
+  const Chosen slot = live && l < k ? sh.sel[r][l] : Chosen{-1, -INFINITY};
+  const int e = slot.e;
   const bool has = e >= 0;
-  const float lg = has ? row[e] : -INFINITY;
+  const float lg = slot.l;
   float w;
   if (a.sigmoid) {
     w = has ? sigmoid_of(lg) : 0.0f;
@@ -441,30 +494,36 @@ __device__ __forceinline__ void route_rows(const ScoredArgs& a, int64_t t0, Rout
   wave_sync();
 }
 
+// One pass of rows a workgroup, from row `first` on: in a loop the compiler
+// keeps what does not depend on the row (biases, groups of the experts) in
+// registers, twice as many as fit 4 waves a SIMD.
 template <int Lanes, int NV, bool Vec, bool General>
-__global__ __launch_bounds__(kThreads) void route_scored_kernel(ScoredArgs a) {
+__global__ __launch_bounds__(kThreads) void route_scored_kernel(ScoredArgs a, int64_t first_row) {
   extern __shared__ __align__(16) float buffer[];
-  __shared__ RouteShared<Lanes> sh;
+  __shared__ RouteShared<Lanes, General> sh;
   constexpr int kRows = kThreads / Lanes;
-  if (a.sorted_ids) {  // what the grouping kernel does not write
+  if (a.sorted_ids && first_row == 0) {  // what the grouping kernel does not write
     const int64_t first = blockIdx.x * (int64_t)kThreads + threadIdx.x, step = gridDim.x * (int64_t)kThreads;
     for (int64_t i = first; i < a.cap; i += step) a.sorted_ids[i] = a.M * a.k;
     for (int64_t i = first; i < a.cap / a.block_m; i += step) a.block_expert[i] = -1;
   }
-  for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < a.M; t0 += (int64_t)gridDim.x * kRows)
-    route_rows<Lanes, NV, Vec, General>(a, t0, sh, buffer, nullptr);
+  route_rows<Lanes, NV, Vec, General>(a, first_row + (int64_t)blockIdx.x * kRows, sh, buffer, nullptr);
 }
 
 // Up to 16 rows: routing and grouping in one workgroup and one launch.
 template <int Lanes, int NV, bool Vec, bool General>
 __global__ __launch_bounds__(kThreads) void route_scored_small_kernel(ScoredArgs a) {
   extern __shared__ __align__(16) float buffer[];
-  __shared__ RouteShared<Lanes> sh;
+  __shared__ RouteShared<Lanes, General> sh;
   __shared__ SmallRoute small;
   constexpr int kRows = kThreads / Lanes;
   const int tid = threadIdx.x, MK = a.M * a.k;
   if (tid < (a.E + 31) / 32) small.bits[tid] = 0u;
-  for (int64_t t0 = 0; t0 < a.M; t0 += kRows) route_rows<Lanes, NV, Vec, General>(a, t0, sh, buffer, small.ids);
+  if constexpr (kRows >= kSmallMaxTokens) {
+    route_rows<Lanes, NV, Vec, General>(a, 0, sh, buffer, small.ids);
+  } else {
+    for (int64_t t0 = 0; t0 < a.M; t0 += kRows) route_rows<Lanes, NV, Vec, General>(a, t0, sh, buffer, small.ids);
+  }
   const int nd = small_group<kThreads, true>(small, MK, a.E);
   const int bm = a.block_m;
   for (int64_t i = tid; i < a.cap; i += kThreads) {
@@ -498,92 +557,91 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 // the rest of the row is grad_base or zeros, and is not touched in place.
 // The slots' values reach the row's order through LDS.
 template <int Lanes, int NV, bool Vec, bool Full>
-__global__ __launch_bounds__(kThreads) void route_scored_backward_kernel(ScoredBackwardArgs a) {
+__global__ __launch_bounds__(kThreads) void route_scored_backward_kernel(ScoredBackwardArgs a, int64_t first_row) {
   extern __shared__ __align__(16) float buffer[];
   constexpr int N = 4 * NV, kRows = kThreads / Lanes;
   const int l = threadIdx.x % Lanes, r = threadIdx.x / Lanes;
   const int E = a.E, k = a.k, pitch = (E + 3) & ~3;
   float* mine = buffer + r * pitch;
   const bool in_place = a.base == a.grad;
-  for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < a.M; t0 += (int64_t)gridDim.x * kRows) {
-    const int64_t t = t0 + r;
-    const bool active = t < a.M;
-    const float* row = a.logits + (active ? t : (int64_t)a.M - 1) * E;
-    float v[N];
-    if constexpr (Full) load_row<Lanes, NV, Vec>(row, E, l, v);
-    const int e = active && l < k ? a.ids[t * k + l] : -1;
-    const bool has = (unsigned)e < (unsigned)E;
-    const float g = has ? a.scale * a.dweights[t * k + l] : 0.0f;
-    const float lg = has ? row[e] : -INFINITY;
-    const bool any = row_any<Lanes>(has);
-    RowSoftmax soft{0.0f, 0.0f, 0.0f};
-    float d;  // what goes to the slot's expert
-    float dot = 0.0f;
-    if constexpr (Full) {
-      soft = row_softmax<Lanes>(v);
-      dot = row_sum<Lanes>(has ? g * (soft.exp_of(lg) * soft.inv) : 0.0f);
-      d = g;
-    } else if (!a.sigmoid) {
-      const float top = row_max<Lanes>(lg);
-      const float x = has ? expf(lg - top) : 0.0f;
-      const float s = row_sum<Lanes>(x);
-      const float w = has ? x / s : 0.0f;
-      d = w * (g - row_sum<Lanes>(g * w));
+  const int64_t t = first_row + (int64_t)blockIdx.x * kRows + r;
+  const bool active = t < a.M;
+  const float* row = a.logits + (active ? t : (int64_t)a.M - 1) * E;
+  float v[N];
+  if constexpr (Full) load_row<Lanes, NV, Vec>(row, E, l, v);
+  const int e = active && l < k ? a.ids[t * k + l] : -1;
+  const bool has = (unsigned)e < (unsigned)E;
+  const float g = has ? a.scale * a.dweights[t * k + l] : 0.0f;
+  const float lg = has ? row[e] : -INFINITY;
+  const bool any = row_any<Lanes>(has);
+  RowSoftmax soft{0.0f, 0.0f, 0.0f};
+  float d;  // what goes to the slot's expert
+  float dot = 0.0f;
+  if constexpr (Full) {
+    soft = row_softmax<Lanes>(v);
+    dot = row_sum<Lanes>(has ? g * (soft.exp_of(lg) * soft.inv) : 0.0f);
+    d = g;
+  } else if (!a.sigmoid) {
+    const float top = row_max<Lanes>(lg);
+    const float x = has ? expf(lg - top) : 0.0f;
+    const float s = row_sum<Lanes>(x);
+    const float w = has ? x / s : 0.0f;
+    d = w * (g - row_sum<Lanes>(g * w));
+  } else {
+    const float x = expf(-fabsf(lg)), y = 1.0f + x;
+    const float s = has ? (lg >= 0.0f ? 1.0f : x) / y : 0.0f;
+    const float slope = has ? x / (y * y) : 0.0f;
+    if (a.renorm) {
+      const float total = row_sum<Lanes>(s) + kDenom;
+      d = slope / total * (g - row_sum<Lanes>(g * s / total));
     } else {
-      const float x = expf(-fabsf(lg)), y = 1.0f + x;
-      const float s = has ? (lg >= 0.0f ? 1.0f : x) / y : 0.0f;
-      const float slope = has ? x / (y * y) : 0.0f;
-      if (a.renorm) {
-        const float total = row_sum<Lanes>(s) + kDenom;
-        d = slope / total * (g - row_sum<Lanes>(g * (s / total)));
-      } else {
-        d = slope * g;
-      }
+      d = slope * g;
     }
-    if (!Full && in_place) {
-      if (has) a.grad[t * E + e] += d;
-      continue;
-    }
+  }
+  if (!Full && in_place) {
+    if (has) a.grad[t * E + e] += d;
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = 4 * Lanes * j + 4 * l;
+    if (c < E) *(float4*)(mine + c) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  }
+  wave_sync();
+  if (has) mine[e] = d;
+  wave_sync();
+  if (active) {
+    const float* base = a.base ? a.base + t * E : nullptr;
+    float* grad = a.grad + t * E;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = 4 * Lanes * j + 4 * l;
-      if (c < E) *(float4*)(mine + c) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    }
-    wave_sync();
-    if (has) mine[e] = d;
-    wave_sync();
-    if (active) {
-      const float* base = a.base ? a.base + t * E : nullptr;
-      float* grad = a.grad + t * E;
+      float o[4];
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int c = 4 * Lanes * j + 4 * l;
-        float o[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          o[q] = c < E ? mine[c + q] : 0.0f;
-          if constexpr (Full) o[q] = any ? soft.exp_of(v[4 * j + q]) * soft.inv * (o[q] - dot) : 0.0f;
+      for (int q = 0; q < 4; ++q) {
+        o[q] = c < E ? mine[c + q] : 0.0f;
+        if constexpr (Full) o[q] = any ? soft.exp_of(v[4 * j + q]) * soft.inv * (o[q] - dot) : 0.0f;
+      }
+      if constexpr (Vec) {
+        if (c < E) {
+          float4 b = base ? *(const float4*)(base + c) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          *(float4*)(grad + c) = make_float4(o[0] + b.x, o[1] + b.y, o[2] + b.z, o[3] + b.w);
         }
-        if constexpr (Vec) {
-          if (c < E) {
-            float4 b = base ? *(const float4*)(base + c) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            *(float4*)(grad + c) = make_float4(o[0] + b.x, o[1] + b.y, o[2] + b.z, o[3] + b.w);
-          }
-        } else {
+      } else {
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (c + q < E) grad[c + q] = o[q] + (base ? base[c + q] : 0.0f);
-        }
+        for (int q = 0; q < 4; ++q)
+          if (c + q < E) grad[c + q] = o[q] + (base ? base[c + q] : 0.0f);
       }
     }
-    wave_sync();
   }
 }
 
-// Workgroups: enough for the rows, at most 2^20 (a grid has fewer than 2^32 threads).
+// Workgroups of a launch: enough for the rows, at most 2^23 (a grid has fewer
+// than 2^32 threads).
+constexpr int kMaxGrid = 1 << 23;
 unsigned grid_for(int64_t M, int rows) {
   const int64_t n = ceil_div(M, rows);
-  return (unsigned)(n < (1 << 20) ? n : (1 << 20));
+  return (unsigned)(n < kMaxGrid ? n : kMaxGrid);
 }
 
 }  // namespace
@@ -596,13 +654,16 @@ hipError_t launch_route_scored(const ScoredArgs& a, hipStream_t stream) {
     constexpr int L = decltype(lanes)::value, NV = decltype(nv)::value;
     constexpr bool V = decltype(vec)::value;
     const unsigned lds = (unsigned)(row_buffer_bytes(L, general, a.E) * kWaves);
-    const unsigned grid = small ? 1u : grid_for(a.M, kThreads / L);
+    constexpr int kRows = kThreads / L;
     if (small) {
-      general ? route_scored_small_kernel<L, NV, V, true><<<grid, kThreads, lds, stream>>>(a)
-              : route_scored_small_kernel<L, NV, V, false><<<grid, kThreads, lds, stream>>>(a);
-    } else {
-      general ? route_scored_kernel<L, NV, V, true><<<grid, kThreads, lds, stream>>>(a)
-              : route_scored_kernel<L, NV, V, false><<<grid, kThreads, lds, stream>>>(a);
+      general ? route_scored_small_kernel<L, NV, V, true><<<1, kThreads, lds, stream>>>(a)
+              : route_scored_small_kernel<L, NV, V, false><<<1, kThreads, lds, stream>>>(a);
+      return;
+    }
+    for (int64_t first = 0; first < a.M; first += (int64_t)kMaxGrid * kRows) {
+      const unsigned grid = grid_for(a.M - first, kRows);
+      general ? route_scored_kernel<L, NV, V, true><<<grid, kThreads, lds, stream>>>(a, first)
+              : route_scored_kernel<L, NV, V, false><<<grid, kThreads, lds, stream>>>(a, first);
     }
   });
   const hipError_t err = hipGetLastError();
@@ -617,9 +678,12 @@ hipError_t launch_route_scored_backward(const ScoredBackwardArgs& a, hipStream_t
     constexpr int L = decltype(lanes)::value, NV = decltype(nv)::value;
     constexpr bool V = decltype(v)::value;
     const unsigned lds = (unsigned)(((a.E + 3) & ~3) * 4 * (kThreads / L));
-    const unsigned grid = grid_for(a.M, kThreads / L);
-    full ? route_scored_backward_kernel<L, NV, V, true><<<grid, kThreads, lds, stream>>>(a)
-         : route_scored_backward_kernel<L, NV, V, false><<<grid, kThreads, lds, stream>>>(a);
+    constexpr int kRows = kThreads / L;
+    for (int64_t first = 0; first < a.M; first += (int64_t)kMaxGrid * kRows) {
+      const unsigned grid = grid_for(a.M - first, kRows);
+      full ? route_scored_backward_kernel<L, NV, V, true><<<grid, kThreads, lds, stream>>>(a, first)
+           : route_scored_backward_kernel<L, NV, V, false><<<grid, kThreads, lds, stream>>>(a, first);
+    }
   });
   return hipGetLastError();
 }
