@@ -219,31 +219,31 @@ __device__ __attribute__((noinline)) void route_row_exact(const float* row, cons
   wave_sync();
 }
 
-// Dynamic LDS of one wave: the group values of its rows, or the 64-bit keys of
-// one row.
-__host__ __device__ constexpr int64_t row_buffer_bytes(int lanes, bool general, int E) {
-  return (int64_t)E * (general ? (64 / lanes) * 4 : 8);
-}
+constexpr int kStep = 8;  // keys compared in a step of the ranking
 
-// A candidate: its expert and what it is ordered by, in one LDS read; with a
-// bias also what c is computed from.
-struct Candidate {
-  float c;
-  int e;
-};
-struct BiasedCandidate {
-  float c;
-  int e;
-  float l, b;
-};
+// Dynamic LDS of one wave: with groups the values of its rows, padded so that
+// the groups of a row and the rows start in different banks; then the
+// candidates' c in fp64; then the 64-bit keys of one row (exact path).
+__host__ __device__ constexpr int row_pitch(int E, int groups) { return (E + groups + 63) / 64 * 64 + 16; }
+__host__ __device__ constexpr int row_buffer_bytes(int lanes, bool biased, bool grouped, int E, int groups) {
+  int bytes = E * 8;
+  if (grouped) bytes = row_pitch(E, groups) * (64 / lanes) * 4;
+  if (biased && bytes < 64 / lanes * kMaxCand * 8) bytes = 64 / lanes * kMaxCand * 8;
+  return bytes;
+}
 
 template <int Lanes, bool General>
 struct RouteShared {
   static constexpr int kRows = kThreads / Lanes;
   Chosen sel[kRows][16];
-  std::conditional_t<General, BiasedCandidate, Candidate> cand[kRows][kMaxCand];
-  uint64_t c64[General ? kRows : 1][kMaxCand];  // c in fp64
-  float groups[General ? kRows : 1][64];
+  union {
+    // the candidates: (order key of c) << 32 | ~expert, zeros behind them
+    __align__(16) uint64_t key[kMaxCand + kStep];
+    float groups[64];  // before that, the groups' scores
+  } row[kRows];
+  // with a bias: what c is computed from, and the candidates by rank
+  float l[General ? kRows : 1][kMaxCand], b[General ? kRows : 1][kMaxCand];
+  uint8_t by_rank[General ? kRows : 1][kMaxCand];
 };
 
 // Routes the rows t0 + wave * (64 / Lanes) + lane / Lanes of this workgroup.
@@ -259,7 +259,8 @@ __device__ __forceinline__ void route_rows(const ScoredArgs& a, int64_t t0, Rout
   const bool active = t < a.M;
   const float* row = a.logits + (active ? t : (int64_t)a.M - 1) * E;
   const int r = wave * kRows + sub;
-  buffer += row_buffer_bytes(Lanes, General, E) / 4 * wave;
+  const bool grouped = General && a.top_groups < a.groups;
+  buffer += row_buffer_bytes(Lanes, a.bias != nullptr, grouped, E, a.groups) / 4 * wave;
   float v[N];  // the logits, then what the experts are ordered by
   load_row<Lanes, NV, Vec>(row, E, l, v);
   const bool live = active && (!a.valid || a.valid[t]);
@@ -276,7 +277,6 @@ __device__ __forceinline__ void route_rows(const ScoredArgs& a, int64_t t0, Rout
   float near = 0.0f;     // closer values need fp64
   float largest = 0.0f;  // of a lane's |l| and |c|
   if constexpr (General) {
-    const bool grouped = a.top_groups < a.groups;
     // fp32 errors in roundings of 2^-24: a sigmoid's are (1 - s) s (1.3 |l| + 2) + 3 s
     // < 4; a softmax value's p = pmax e^-x are (1.5 x + 50) p < 50 pmax (x from the
     // exponent, the rest from the row's sum). c adds |c|. Twice that is `near`.
@@ -296,21 +296,25 @@ __device__ __forceinline__ void route_rows(const ScoredArgs& a, int64_t t0, Rout
     }
     bad |= !(largest < 1e30f);
     if (grouped) {
-      const int gs = E / a.groups, G = a.groups;
-      float* mine = buffer + sub * E;
-      const bool raw = a.bias || a.group_top == 1;  // (the highest logit has the highest score)
+      const int G = a.groups, gs = E / G;
+      const uint32_t magic = (1u << 20) / (uint32_t)gs + 1u;  // e / gs = e * magic >> 20 for e < 1024
+      auto group_of = [&](int e) { return (int)((uint32_t)e * magic >> 20); };
+      float* mine = buffer + sub * row_pitch(E, G);  // expert e of group g at e + g
+      const bool raw = a.bias || a.group_top == 1;   // (the highest logit has the highest score)
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (inside(i)) mine[expert_of(i)] = raw ? v[i] : fast_score(v[i]);
+      for (int i = 0; i < N; ++i) {
+        const int e = expert_of(i);
+        if (inside(i)) mine[e + group_of(e)] = raw ? v[i] : fast_score(v[i]);
+      }
       wave_sync();
       // P lanes a group
       int P = 1;
       while (P < 8 && 2 * P * G <= Lanes) P *= 2;
       for (int g = l / P; g < G; g += Lanes / P) {
         float m1 = -INFINITY, m2 = -INFINITY;
-#pragma unroll 4
+#pragma unroll 8
         for (int i = l % P; i < gs; i += P) {
-          const float x = mine[g * gs + i];
+          const float x = mine[g * (gs + 1) + i];
           m2 = fmaxf(m2, fminf(m1, x));
           m1 = fmaxf(m1, x);
         }
@@ -322,19 +326,19 @@ __device__ __forceinline__ void route_rows(const ScoredArgs& a, int64_t t0, Rout
         if (P > 1) join(dpp<kQuadSwap1>(__float_as_uint(m1)), dpp<kQuadSwap1>(__float_as_uint(m2)));
         if (P > 2) join(dpp<kQuadSwap2>(__float_as_uint(m1)), dpp<kQuadSwap2>(__float_as_uint(m2)));
         if (P > 4) join(dpp<kRowHalfMirror>(__float_as_uint(m1)), dpp<kRowHalfMirror>(__float_as_uint(m2)));
-        sh.groups[r][g] = a.group_top == 2 ? m1 + m2 : m1;
+        sh.row[r].groups[g] = a.group_top == 2 ? m1 + m2 : m1;
       }
       wave_sync();
       uint64_t chosen = 0;
       float in = INFINITY, out = -INFINITY;
       for (int g0 = 0; g0 < G; g0 += Lanes) {
         const int g = g0 + l;
-        const float s = g < G ? sh.groups[r][g] : 0.0f;
+        const float s = g < G ? sh.row[r].groups[g] : 0.0f;
         int rank = 0;
-#pragma unroll 4
+#pragma unroll 8
         for (int h = 0; h < G; ++h) {
-          const float o = sh.groups[r][h];
-          rank += o > s || (o == s && h < g);
+          const float o = sh.row[r].groups[h];
+          rank += (int)(o > s) | ((int)(o == s) & (int)(h < g));
         }
         const bool take = g < G && rank < a.top_groups;
         const uint64_t m = __ballot(take) >> (lane & (64 - Lanes));
@@ -346,14 +350,30 @@ __device__ __forceinline__ void route_rows(const ScoredArgs& a, int64_t t0, Rout
       out = row_max<Lanes>(out);
       if (a.bias || a.group_top == 2)
         bad |= !(in - out > 4.0f * score_error + 0x1p-21f * fmaxf(fabsf(in), fabsf(out)));
-      const uint32_t magic = (1u << 20) / (uint32_t)gs + 1u;  // e / gs = e * magic >> 20 for e < 1024
+      // The values in another order: a lane's experts lie `Lanes` apart, so that
+      // a group's are spread over all lanes. (Neighbours of 4 a lane leave lanes
+      // empty, the threshold is then low and the candidates are many: ranking
+      // them took 8 of 15 us for [4096, 256] in 8 groups.)
+      const bool logits = !a.bias && a.group_top == 2;  // scores were written: the order is the logits'
+      if (logits) {
+        wave_sync();
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int e = expert_of(i);
+          if (inside(i)) mine[e + group_of(e)] = v[i];
+        }
+        wave_sync();
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int e = l + Lanes * i, g = group_of(e);
+        v[i] = e < E && ((chosen >> (g & 63)) & 1) ? mine[e + g] : -INFINITY;
+      }
+    } else {
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        if (!((chosen >> (((uint32_t)expert_of(i) * magic >> 20) & 63)) & 1)) v[i] = -INFINITY;
+        if (!inside(i)) v[i] = -INFINITY;
     }
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (!inside(i)) v[i] = -INFINITY;
   }
 
   // the threshold (as an integer key: its maxima are one instruction an exchange)
@@ -382,79 +402,90 @@ __device__ __forceinline__ void route_rows(const ScoredArgs& a, int64_t t0, Rout
   int n;
   int at = row_before<Lanes>(__builtin_popcount(mask), n);
   while (__any(mask)) {
-    const int bit = mask ? __builtin_ctz(mask) : 0;
-    if (mask && at < kMaxCand) sh.cand[r][at].e = expert_of(N - 1 - bit);
+    const int i = N - 1 - (mask ? __builtin_ctz(mask) : 0);
+    if (mask && at < kMaxCand) sh.row[r].key[at] = (uint32_t)(grouped ? l + Lanes * i : expert_of(i));
     ++at;
     mask &= mask - 1;
   }
   wave_sync();
   bad |= n > kMaxCand;
   n = n < kMaxCand ? n : kMaxCand;
+  if (l < kStep) sh.row[r].key[n + l] = 0;
   for (int i = l; i < n; i += Lanes) {
-    auto& me = sh.cand[r][i];
-    const float x = row[me.e];
+    const int e = (int)sh.row[r].key[i];
+    const float x = row[e];
+    float c = x;
     if constexpr (General) {
-      const float b = a.bias ? a.bias[me.e] : 0.0f;
-      me.l = x;
-      me.b = b;
-      me.c = a.bias ? fast_score(x) + b : x;
-    } else {
-      me.c = x;
+      const float b = a.bias ? a.bias[e] : 0.0f;
+      sh.l[r][i] = x;
+      sh.b[r][i] = b;
+      c = a.bias ? fast_score(x) + b : x;
     }
+    sh.row[r].key[i] = (uint64_t)order_key(c) << 32 | (uint32_t)~e;
   }
   wave_sync();
-  bool close = false;
-  for (int i = l; i < n; i += Lanes) {
-    const auto me = sh.cand[r][i];
-    int rank = 0;
-    bool beside = false;
-#pragma unroll 4
-    for (int h = 0; h < n; ++h) {
-      const auto o = sh.cand[r][h];
-      rank += (int)(o.c > me.c) | ((int)(o.c == me.c) & (int)(o.e < me.e));
-      if constexpr (General) beside |= (fabsf(o.c - me.c) <= near) & ((o.l != me.l) | (o.b != me.b));
-    }
-    if (rank < k) {
-      if constexpr (General) {
-        sh.sel[r][rank] = {me.e, me.l};
-        close |= beside;
-      } else {
-        sh.sel[r][rank] = {me.e, me.c};
-      }
-    }
-  }
-  if constexpr (General) if (a.bias && __any(close && live)) {  // the candidates again, in fp64
-    wave_sync();
-    double m = 0.0, sum = 1.0;
-    if (!a.sigmoid) {
-      float top_l = -INFINITY;
-#pragma unroll 1
-      for (int e = l; e < E; e += Lanes) top_l = fmaxf(top_l, row[e]);
-      m = row_max<Lanes>(top_l);
-      sum = 0.0;
-#pragma unroll 1
-      for (int e = l; e < E; e += Lanes) sum += exp((double)row[e] - m);
+  for (int i = l; i < n; i += 2 * Lanes) {  // two candidates of a lane against all
+    const int j = i + Lanes;
+    const uint64_t me = sh.row[r].key[i], other = j < n ? sh.row[r].key[j] : 0;
+    int rank = 0, other_rank = 0;
+    for (int h = 0; h < n; h += kStep) {
 #pragma unroll
-      for (int d = Lanes / 2; d; d >>= 1) sum += __shfl_xor(sum, d, 64);
-    }
-#pragma unroll 1
-    for (int i = l; i < n; i += Lanes) {
-      const int e = sh.cand[r][i].e;
-      const double x = sh.cand[r][i].l;
-      sh.c64[r][i] = key64((a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - m) / sum) + (double)a.bias[e]);
-    }
-    wave_sync();
-#pragma unroll 1
-    for (int i = l; i < n; i += Lanes) {
-      const uint64_t me = sh.c64[r][i];
-      const int e = sh.cand[r][i].e;
-      int rank = 0;
-#pragma unroll 1
-      for (int h = 0; h < n; ++h) {
-        const uint64_t o = sh.c64[r][h];
-        rank += o > me || (o == me && sh.cand[r][h].e < e);
+      for (int q = 0; q < kStep; ++q) {
+        const uint64_t o = sh.row[r].key[h + q];
+        rank += o > me;
+        other_rank += o > other;
       }
-      if (rank < k) sh.sel[r][rank] = {e, sh.cand[r][i].l};
+    }
+    auto place = [&](int at, uint64_t k64, int to) {
+      if (to < k) sh.sel[r][to] = {(int)~(uint32_t)k64, General ? sh.l[r][at] : key_value((uint32_t)(k64 >> 32))};
+      if constexpr (General) sh.by_rank[r][to] = (uint8_t)at;
+    };
+    place(i, me, rank);
+    if (j < n) place(j, other, other_rank);
+  }
+  if constexpr (General) {
+    if (a.bias) {
+      // neighbours in this order that are closer than fp32 tells and not equal in
+      // all: of such a pair further apart some neighbours between are one too
+      wave_sync();
+      bool close = false;
+      for (int i = l; i + 1 < n; i += Lanes) {
+        const int u = sh.by_rank[r][i], w = sh.by_rank[r][i + 1];
+        const float apart = key_value((uint32_t)(sh.row[r].key[u] >> 32)) - key_value((uint32_t)(sh.row[r].key[w] >> 32));
+        close |= (apart <= near) & ((sh.l[r][u] != sh.l[r][w]) | (sh.b[r][u] != sh.b[r][w]));
+      }
+      if (__any(close && live)) {  // the candidates again, in fp64
+        uint64_t* c64 = (uint64_t*)buffer + sub * kMaxCand;
+        double m = 0.0, sum = 1.0;
+        if (!a.sigmoid) {
+          float top_l = -INFINITY;
+#pragma unroll 1
+          for (int e = l; e < E; e += Lanes) top_l = fmaxf(top_l, row[e]);
+          m = row_max<Lanes>(top_l);
+          sum = 0.0;
+#pragma unroll 1
+          for (int e = l; e < E; e += Lanes) sum += exp((double)row[e] - m);
+#pragma unroll
+          for (int d = Lanes / 2; d; d >>= 1) sum += __shfl_xor(sum, d, 64);
+        }
+#pragma unroll 1
+        for (int i = l; i < n; i += Lanes) {
+          const double x = sh.l[r][i];
+          c64[i] = key64((a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - m) / sum) + (double)sh.b[r][i]);
+        }
+        wave_sync();
+#pragma unroll 1
+        for (int i = l; i < n; i += Lanes) {
+          const uint64_t me = c64[i];
+          const uint32_t e = (uint32_t)sh.row[r].key[i];  // (its complement: the lower expert is the higher)
+          int rank = 0;
+          for (int h = 0; h < n; ++h) {
+            const uint64_t o = c64[h];
+            rank += (int)(o > me) | ((int)(o == me) & (int)((uint32_t)sh.row[r].key[h] > e));
+          }
+          if (rank < k) sh.sel[r][rank] = {(int)~e, sh.l[r][i]};
+        }
+      }
     }
   }
   const bool again = row_any<Lanes>(bad && live);
@@ -510,20 +541,24 @@ __global__ __launch_bounds__(kThreads) void route_scored_kernel(ScoredArgs a, in
   route_rows<Lanes, NV, Vec, General>(a, first_row + (int64_t)blockIdx.x * kRows, sh, buffer, nullptr);
 }
 
-// Up to 16 rows: routing and grouping in one workgroup and one launch.
+// Up to 16 rows: routing and grouping in one workgroup and one launch. The
+// grouping's tables take the dynamic LDS after the routing.
 template <int Lanes, int NV, bool Vec, bool General>
 __global__ __launch_bounds__(kThreads) void route_scored_small_kernel(ScoredArgs a) {
   extern __shared__ __align__(16) float buffer[];
   __shared__ RouteShared<Lanes, General> sh;
-  __shared__ SmallRoute small;
+  __shared__ int32_t ids[kSmallMaxAssign];
   constexpr int kRows = kThreads / Lanes;
   const int tid = threadIdx.x, MK = a.M * a.k;
-  if (tid < (a.E + 31) / 32) small.bits[tid] = 0u;
   if constexpr (kRows >= kSmallMaxTokens) {
-    route_rows<Lanes, NV, Vec, General>(a, 0, sh, buffer, small.ids);
+    route_rows<Lanes, NV, Vec, General>(a, 0, sh, buffer, ids);
   } else {
-    for (int64_t t0 = 0; t0 < a.M; t0 += kRows) route_rows<Lanes, NV, Vec, General>(a, t0, sh, buffer, small.ids);
+    for (int64_t t0 = 0; t0 < a.M; t0 += kRows) route_rows<Lanes, NV, Vec, General>(a, t0, sh, buffer, ids);
   }
+  __syncthreads();
+  SmallRoute& small = *(SmallRoute*)buffer;
+  if (tid < MK) small.ids[tid] = ids[tid];  // (MK <= kThreads)
+  if (tid < (a.E + 31) / 32) small.bits[tid] = 0u;
   const int nd = small_group<kThreads, true>(small, MK, a.E);
   const int bm = a.block_m;
   for (int64_t i = tid; i < a.cap; i += kThreads) {
@@ -534,6 +569,7 @@ __global__ __launch_bounds__(kThreads) void route_scored_small_kernel(ScoredArgs
   for (int x = tid; x <= a.E; x += kThreads) a.offsets[x] = bm * (x < a.E ? small_rank(small, x) : nd);
   if (tid == 0) *a.npp = bm * nd;
 }
+static_assert(kSmallMaxAssign <= kThreads, "one id a thread");
 
 // fn(Lanes, NV, Vec) for the row width
 template <typename F>
@@ -653,7 +689,8 @@ hipError_t launch_route_scored(const ScoredArgs& a, hipStream_t stream) {
   by_width(a.E, a.E % 4 == 0 && aligned16(a.logits) && (!a.bias || aligned16(a.bias)), [&](auto lanes, auto nv, auto vec) {
     constexpr int L = decltype(lanes)::value, NV = decltype(nv)::value;
     constexpr bool V = decltype(vec)::value;
-    const unsigned lds = (unsigned)(row_buffer_bytes(L, general, a.E) * kWaves);
+    unsigned lds = (unsigned)row_buffer_bytes(L, a.bias != nullptr, a.top_groups < a.groups, a.E, a.groups) * kWaves;
+    if (small && lds < sizeof(SmallRoute)) lds = sizeof(SmallRoute);
     constexpr int kRows = kThreads / L;
     if (small) {
       general ? route_scored_small_kernel<L, NV, V, true><<<1, kThreads, lds, stream>>>(a)
