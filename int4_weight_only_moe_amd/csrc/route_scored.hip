@@ -224,7 +224,12 @@ constexpr int kStep = 8;  // keys compared in a step of the ranking
 // Dynamic LDS of one wave: with groups the values of its rows, padded so that
 // the groups of a row and the rows start in different banks; then the
 // candidates' c in fp64; then the 64-bit keys of one row (exact path).
-__host__ __device__ constexpr int row_pitch(int E, int groups) { return (E + groups + 63) / 64 * 64 + 16; }
+// Groups of 4 n >= 16 experts are 4 words apart, so that 4 neighbours of a lane
+// are one 16-byte access; others 1 word.
+__host__ __device__ constexpr int group_pad(int size) { return size % 4 == 0 && size >= 16 ? 4 : 1; }
+__host__ __device__ constexpr int row_pitch(int E, int groups) {
+  return (E + groups * group_pad(E / groups) + 63) / 64 * 64 + 16;
+}
 __host__ __device__ constexpr int row_buffer_bytes(int lanes, bool biased, bool grouped, int E, int groups) {
   int bytes = E * 8;
   if (grouped) bytes = row_pitch(E, groups) * (64 / lanes) * 4;
@@ -299,24 +304,53 @@ __device__ __forceinline__ void route_rows(const ScoredArgs& a, int64_t t0, Rout
       const int G = a.groups, gs = E / G;
       const uint32_t magic = (1u << 20) / (uint32_t)gs + 1u;  // e / gs = e * magic >> 20 for e < 1024
       auto group_of = [&](int e) { return (int)((uint32_t)e * magic >> 20); };
-      float* mine = buffer + sub * row_pitch(E, G);  // expert e of group g at e + g
+      const int pad = group_pad(gs);
+      const bool quads = Vec && pad == 4;
+      float* mine = buffer + sub * row_pitch(E, G);  // expert e of group g at e + pad g
       const bool raw = a.bias || a.group_top == 1;   // (the highest logit has the highest score)
+      auto write_row = [&](auto value) {
+        if (quads) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int e = expert_of(i);
-        if (inside(i)) mine[e + group_of(e)] = raw ? v[i] : fast_score(v[i]);
-      }
+          for (int j = 0; j < NV; ++j) {
+            const int e = expert_of(4 * j);
+            if (e < E)
+              *(float4*)(mine + e + 4 * group_of(e)) =
+                  make_float4(value(4 * j), value(4 * j + 1), value(4 * j + 2), value(4 * j + 3));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const int e = expert_of(i);
+            if (inside(i)) mine[e + pad * group_of(e)] = value(i);
+          }
+        }
+      };
+      if (raw) write_row([&](int i) { return v[i]; });
+      else write_row([&](int i) { return fast_score(v[i]); });
       wave_sync();
       // P lanes a group
       int P = 1;
       while (P < 8 && 2 * P * G <= Lanes) P *= 2;
+      const bool quad_scan = pad == 4 && gs % (4 * P) == 0;
       for (int g = l / P; g < G; g += Lanes / P) {
         float m1 = -INFINITY, m2 = -INFINITY;
-#pragma unroll 8
-        for (int i = l % P; i < gs; i += P) {
-          const float x = mine[g * (gs + 1) + i];
+        auto take = [&](float x) {
           m2 = fmaxf(m2, fminf(m1, x));
           m1 = fmaxf(m1, x);
+        };
+        const float* from = mine + g * (gs + pad);
+        if (quad_scan) {
+#pragma unroll 4
+          for (int i = 4 * (l % P); i < gs; i += 4 * P) {
+            const float4 x = *(const float4*)(from + i);
+            take(x.x);
+            take(x.y);
+            take(x.z);
+            take(x.w);
+          }
+        } else {
+#pragma unroll 4
+          for (int i = l % P; i < gs; i += P) take(from[i]);
         }
         auto join = [&](uint32_t o1b, uint32_t o2b) {
           const float o1 = __uint_as_float(o1b), o2 = __uint_as_float(o2b);
@@ -353,21 +387,27 @@ __device__ __forceinline__ void route_rows(const ScoredArgs& a, int64_t t0, Rout
       // The values in another order: a lane's experts lie `Lanes` apart, so that
       // a group's are spread over all lanes. (Neighbours of 4 a lane leave lanes
       // empty, the threshold is then low and the candidates are many: ranking
-      // them took 8 of 15 us for [4096, 256] in 8 groups.)
-      const bool logits = !a.bias && a.group_top == 2;  // scores were written: the order is the logits'
-      if (logits) {
-        wave_sync();
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int e = expert_of(i);
-          if (inside(i)) mine[e + group_of(e)] = v[i];
-        }
+      // them took 8 of 15 us for [4096, 256] in 8 groups.) Those of groups that
+      // are not chosen are taken out by the groups' lanes first.
+      if (!raw) {
+        write_row([&](int i) { return v[i]; });
         wave_sync();
       }
+      for (int g = l / P; g < G; g += Lanes / P) {
+        if ((chosen >> g) & 1) continue;
+        float* from = mine + g * (gs + pad);
+        if (quad_scan) {
+          for (int i = 4 * (l % P); i < gs; i += 4 * P)
+            *(float4*)(from + i) = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        } else {
+          for (int i = l % P; i < gs; i += P) from[i] = -INFINITY;
+        }
+      }
+      wave_sync();
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const int e = l + Lanes * i, g = group_of(e);
-        v[i] = e < E && ((chosen >> (g & 63)) & 1) ? mine[e + g] : -INFINITY;
+        const int e = l + Lanes * i;
+        v[i] = e < E ? mine[e + pad * group_of(e)] : -INFINITY;
       }
     } else {
 #pragma unroll
