@@ -301,7 +301,7 @@ int moe_add_rms_norm(const uint16_t* x_bf16, int64_t ldx, const void* residual, 
 
 int64_t moe_add_rms_norm_workspace_bytes(int32_t M, int32_t N) {
   if (check_norm(M, N, MOE_DTYPE_BF16) != MOE_OK) return -1;
-  return (int64_t)moe::norm_backward_parts(M) * N * 4;
+  return (int64_t)moe::norm_backward_parts(M, N) * N * 4;
 }
 
 int moe_add_rms_norm_backward(const uint16_t* grad_out_bf16, int64_t ld_grad_out, const void* h, int64_t ld_h,

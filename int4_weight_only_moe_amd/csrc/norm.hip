@@ -5,50 +5,66 @@
 //   backward, n = h r, u = w g:  dh = dres + r (u - n mean(u n)),  dw = sum_t g n
 //
 // Both are bound by HBM traffic: a row is read once and stays in registers
-// between its sum and its outputs. Rows of up to 2048 columns take one wave,
-// wider ones a workgroup of 4 or 16 waves; a lane holds up to 4 chunks of 8
-// columns.
+// between its sum and its outputs. Rows of up to 1024 columns take one wave,
+// wider ones a workgroup; a lane holds 1, 2 or (from 16385 columns on) 4 chunks
+// of 8 columns. Outputs go through the cache, where what reads them next finds
+// them: with non-temporal stores [4096, 4096] took 20 us instead of 25, but with a
+// reader of both outputs behind it 53 instead of 50.
 #include <type_traits>
 
 #include "device_common.h"
 #include "operators.h"
+#include "route_common.h"
 
 namespace moe {
 namespace {
 
-constexpr float kE4m3Max = 448.0f;
+constexpr double kE4m3Max = 448.0;
 
-// Sums over a wave, every lane gets the same bits.
+// Sum over a wave, every lane gets the same bits (wave_sum for fp32).
+template <int kCtrl>
+__device__ __forceinline__ double add_dpp(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint64_t o = (uint64_t)dpp<kCtrl>((uint32_t)(u >> 32)) << 32 | dpp<kCtrl>((uint32_t)u);
+  return v + __builtin_bit_cast(double, o);
+}
 __device__ __forceinline__ double wave_sum64(double v) {
-#pragma unroll
-  for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d, 64);
-  return v;
-}
-__device__ __forceinline__ float wave_sum32(float v) {
-#pragma unroll
-  for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d, 64);
-  return v;
+  v = add_dpp<kQuadSwap1>(v);
+  v = add_dpp<kQuadSwap2>(v);
+  v = add_dpp<kRowHalfMirror>(v);
+  v = add_dpp<kRowMirror>(v);
+  {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const auto lo = __builtin_amdgcn_permlane16_swap((uint32_t)u, (uint32_t)u, false, false);
+    const auto hi = __builtin_amdgcn_permlane16_swap((uint32_t)(u >> 32), (uint32_t)(u >> 32), false, false);
+    v = __builtin_bit_cast(double, (uint64_t)hi[0] << 32 | lo[0]) + __builtin_bit_cast(double, (uint64_t)hi[1] << 32 | lo[1]);
+  }
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const auto lo = __builtin_amdgcn_permlane32_swap((uint32_t)u, (uint32_t)u, false, false);
+  const auto hi = __builtin_amdgcn_permlane32_swap((uint32_t)(u >> 32), (uint32_t)(u >> 32), false, false);
+  return __builtin_bit_cast(double, (uint64_t)hi[0] << 32 | lo[0]) + __builtin_bit_cast(double, (uint64_t)hi[1] << 32 | lo[1]);
 }
 
-// The lanes that share a row: a wave, or W waves that exchange through LDS.
-template <int W>
+// The lanes that share a row: a wave (4 rows a workgroup), or with Wide all
+// waves of the workgroup, which exchange through LDS.
+constexpr int kMaxWaves = 16;
+template <bool Wide>
 struct Team {
-  static constexpr int kLanes = 64 * W;
-  static constexpr int kThreads = W == 1 ? 256 : 64 * W;
-  static constexpr int kRows = W == 1 ? 4 : 1;
-  static __device__ __forceinline__ int lane() { return threadIdx.x % kLanes; }
-  static __device__ __forceinline__ int row() { return threadIdx.x / kLanes; }
+  static constexpr int kRows = Wide ? 1 : 4;
+  static __device__ __forceinline__ int lanes() { return Wide ? (int)blockDim.x : 64; }
+  static __device__ __forceinline__ int lane() { return Wide ? threadIdx.x : threadIdx.x & 63; }
+  static __device__ __forceinline__ int row() { return Wide ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
   // (two barriers, so that `room` may be used again)
   template <typename T>
   static __device__ __forceinline__ T sum(T v, T* room) {
     if constexpr (sizeof(T) == 8) v = wave_sum64(v);
-    else v = wave_sum32(v);
-    if constexpr (W > 1) {
+    else v = wave_sum(v);
+    if constexpr (Wide) {
+      const int waves = blockDim.x >> 6;
       if ((threadIdx.x & 63) == 0) room[threadIdx.x >> 6] = v;
       __syncthreads();
       v = room[0];
-#pragma unroll
-      for (int i = 1; i < W; ++i) v += room[i];
+      for (int i = 1; i < waves; ++i) v += room[i];
       __syncthreads();
     }
     return v;
@@ -57,9 +73,9 @@ struct Team {
 
 // Element q of a lane's chunk i. Vec: chunks of 8 neighbours (16-byte loads);
 // else neighbours lie in neighbouring lanes.
-template <int Lanes, bool Vec>
-__device__ __forceinline__ int column(int i, int q, int lane) {
-  return Vec ? (i * Lanes + lane) * 8 + q : (i * 8 + q) * Lanes + lane;
+template <bool Vec>
+__device__ __forceinline__ int column(int i, int q, int lane, int lanes) {
+  return Vec ? (i * lanes + lane) * 8 + q : (i * 8 + q) * lanes + lane;
 }
 
 __device__ __forceinline__ float from_bf16(uint32_t bits) { return __uint_as_float(bits << 16); }
@@ -80,14 +96,22 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
   return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
+// `columns` further in a row: the row's address is the same in all lanes, and a
+// 32-bit byte offset beside it takes half the registers of whole addresses.
+template <typename T>
+__device__ __forceinline__ T* beside(T* row, int columns) {
+  using Byte = std::conditional_t<std::is_const_v<T>, const char, char>;
+  return (T*)((Byte*)row + (uint32_t)(columns * (int)sizeof(T)));
+}
+
 // Chunk i of a row of bf16 or fp32 values (columns past N: what column 0
 // holds; the caller drops them). Loads are unconditional, so that those of
 // all chunks go out together.
-template <int Lanes, bool Vec, typename T>
-__device__ __forceinline__ void load_chunk(const T* row, int i, int lane, int N, float (&v)[8]) {
+template <bool Vec, typename T>
+__device__ __forceinline__ void load_chunk(const T* row, int i, int lane, int lanes, int N, float (&v)[8]) {
   if constexpr (Vec) {
-    const int c = column<Lanes, true>(i, 0, lane);
-    const T* p = row + (c < N ? c : 0);
+    const int c = column<true>(i, 0, lane, lanes);
+    const T* p = beside(row, c < N ? c : 0);
     if constexpr (sizeof(T) == 2) {
       unpack8(*(const uint4*)p, v);
     } else {
@@ -98,32 +122,32 @@ __device__ __forceinline__ void load_chunk(const T* row, int i, int lane, int N,
   } else {
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      const int c = column<Lanes, false>(i, q, lane);
-      const T x = row[c < N ? c : 0];
+      const int c = column<false>(i, q, lane, lanes);
+      const T x = *beside(row, c < N ? c : 0);
       if constexpr (sizeof(T) == 2) v[q] = from_bf16(x);
       else v[q] = x;
     }
   }
 }
 
-template <int Lanes, bool Vec, typename T>
-__device__ __forceinline__ void store_chunk(T* row, int i, int lane, int N, const float (&v)[8]) {
+template <bool Vec, typename T>
+__device__ __forceinline__ void store_chunk(T* row, int i, int lane, int lanes, int N, const float (&v)[8]) {
   if constexpr (Vec) {
-    const int c = column<Lanes, true>(i, 0, lane);
+    const int c = column<true>(i, 0, lane, lanes);
     if (c >= N) return;
     if constexpr (sizeof(T) == 2) {
-      *(uint4*)(row + c) = pack8(v);
+      *(uint4*)beside(row, c) = pack8(v);
     } else {
-      ((float4*)(row + c))[0] = make_float4(v[0], v[1], v[2], v[3]);
-      ((float4*)(row + c))[1] = make_float4(v[4], v[5], v[6], v[7]);
+      ((float4*)beside(row, c))[0] = make_float4(v[0], v[1], v[2], v[3]);
+      ((float4*)beside(row, c))[1] = make_float4(v[4], v[5], v[6], v[7]);
     }
   } else {
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      const int c = column<Lanes, false>(i, q, lane);
+      const int c = column<false>(i, q, lane, lanes);
       if (c < N) {
-        if constexpr (sizeof(T) == 2) row[c] = to_bf16(v[q]);
-        else row[c] = v[q];
+        if constexpr (sizeof(T) == 2) *beside(row, c) = to_bf16(v[q]);
+        else *beside(row, c) = v[q];
       }
     }
   }
@@ -140,18 +164,78 @@ __device__ __forceinline__ float to_odd(double t) {
   return __uint_as_float(u);
 }
 
-__device__ __forceinline__ uint64_t magnitude(double v) {  // ordered like |v|, NaN the highest
-  return (uint64_t)__double_as_longlong(v) & 0x7FFFFFFFFFFFFFFFull;
+// Ordered like |v|, NaN the highest.
+template <typename F>
+using Bits = std::conditional_t<sizeof(F) == 4, uint32_t, unsigned long long>;
+template <typename F>
+__device__ __forceinline__ Bits<F> magnitude(F v) {
+  return __builtin_bit_cast(Bits<F>, v) & (~(Bits<F>)0 >> 1);
 }
-__device__ __forceinline__ uint64_t larger(uint64_t a, uint64_t b) { return a > b ? a : b; }
+template <typename B>
+__device__ __forceinline__ B larger(B a, B b) { return a > b ? a : b; }
 
-template <int W, int C, bool Vec, typename S, bool Quant>
-__global__ __launch_bounds__(Team<W>::kThreads) void norm_kernel(NormArgs a) {
-  using T = Team<W>;
-  constexpr int L = T::kLanes;
-  __shared__ double room[W];
+// The largest over `lanes` neighbouring lanes: 4, 8 or 16.
+template <int kCtrl>
+__device__ __forceinline__ uint32_t larger_dpp(uint32_t m) { return larger(m, dpp<kCtrl>(m)); }
+template <int kCtrl>
+__device__ __forceinline__ unsigned long long larger_dpp(unsigned long long m) {
+  return larger(m, (unsigned long long)dpp<kCtrl>((uint32_t)(m >> 32)) << 32 | dpp<kCtrl>((uint32_t)m));
+}
+template <typename B>
+__device__ __forceinline__ B largest_of(B m, int lanes) {
+  m = larger_dpp<kQuadSwap1>(m);
+  m = larger_dpp<kQuadSwap2>(m);
+  if (lanes > 4) m = larger_dpp<kRowHalfMirror>(m);
+  if (lanes > 8) m = larger_dpp<kRowMirror>(m);
+  return m;
+}
+
+// The largest |h w| of a chunk. F = float: exact for bf16 h and w unless it over-
+// or underflows, which fp32_top finds.
+template <typename F>
+__device__ __forceinline__ Bits<F> top_of(const float (&h)[8], const float (&w)[8]) {
+  Bits<F> m = 0;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) m = larger(m, magnitude((F)h[q] * (F)w[q]));
+  return m;
+}
+__device__ __forceinline__ bool fp32_top(uint32_t m) {
+  const float v = __uint_as_float(m);
+  return v >= 0x1p-100f && v < 0x1p120f;
+}
+
+// e4m3 of h w rr / s, as 4 bytes a word. In fp32 that is off by at most 6
+// roundings: where it is nowhere near the middle between two e4m3 values (bits 0 to
+// 19 of a normal one) it rounds like the exact value. The other chunks (one in a
+// hundred) take fp64.
+__device__ __forceinline__ void to_e4m3(const float (&h)[8], const float (&w)[8], double rr, float s, uint32_t (&out)[2]) {
+  const float f = (float)rr * __builtin_amdgcn_rcpf(s);
+  float y[8];
+  bool close = !(f >= 0x1p-100f && f < 0x1p100f && s < 0x1p100f);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    y[q] = h[q] * w[q] * f;
+    const uint32_t u = __float_as_uint(y[q]);
+    close |= ((u & 0xFFFFFu) - (0x80000u - 16u) <= 32u) | !(fabsf(y[q]) >= 0x1p-6f && fabsf(y[q]) < 449.0f);
+  }
+  if (__any(close)) {
+    const double f64 = rr / (double)s;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) y[q] = to_odd((double)h[q] * (double)w[q] * f64);
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int u = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * k], y[4 * k + 1], 0, false);
+    out[k] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[4 * k + 2], y[4 * k + 3], u, true);
+  }
+}
+
+template <bool Wide, int C, bool Vec, typename S, bool Quant>
+__global__ __launch_bounds__(Wide ? 64 * kMaxWaves : 256) void norm_kernel(NormArgs a) {
+  using T = Team<Wide>;
+  __shared__ double room[kMaxWaves];
   extern __shared__ unsigned long long maxima[];  // Quant without Vec: of the rows' groups
-  const int lane = T::lane(), N = a.N;
+  const int lane = T::lane(), lanes = T::lanes(), N = a.N;
   const int64_t at = (int64_t)blockIdx.x * T::kRows + T::row();
   const bool active = at < a.M;
   const int64_t t = active ? at : a.M - 1;
@@ -161,8 +245,8 @@ __global__ __launch_bounds__(Team<W>::kThreads) void norm_kernel(NormArgs a) {
     float y[C][8];
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      load_chunk<L, Vec>(a.x + t * a.ldx, i, lane, N, h[i]);
-      load_chunk<L, Vec>(res + t * a.ld_res, i, lane, N, y[i]);
+      load_chunk<Vec>(a.x + t * a.ldx, i, lane, lanes, N, h[i]);
+      load_chunk<Vec>(res + t * a.ld_res, i, lane, lanes, N, y[i]);
     }
 #pragma unroll
     for (int i = 0; i < C; ++i)
@@ -173,121 +257,121 @@ __global__ __launch_bounds__(Team<W>::kThreads) void norm_kernel(NormArgs a) {
       }
   } else if (a.x) {
 #pragma unroll
-    for (int i = 0; i < C; ++i) load_chunk<L, Vec>(a.x + t * a.ldx, i, lane, N, h[i]);
+    for (int i = 0; i < C; ++i) load_chunk<Vec>(a.x + t * a.ldx, i, lane, lanes, N, h[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < C; ++i) load_chunk<L, Vec>(res + t * a.ld_res, i, lane, N, h[i]);
+    for (int i = 0; i < C; ++i) load_chunk<Vec>(res + t * a.ld_res, i, lane, lanes, N, h[i]);
   }
-  float w[C][8];
-#pragma unroll
-  for (int i = 0; i < C; ++i) load_chunk<L, Vec>(a.w, i, lane, N, w[i]);
   double ss = 0.0;
 #pragma unroll
   for (int i = 0; i < C; ++i)
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      if (column<L, Vec>(i, q, lane) >= N) h[i][q] = 0.0f;
+      if (column<Vec>(i, Vec ? 0 : q, lane, lanes) >= N) h[i][q] = 0.0f;  // (Vec: N % 8 == 0)
       ss = fma((double)h[i][q], (double)h[i][q], ss);
     }
+  if (a.res_out && active) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) store_chunk<Vec>((S*)a.res_out + t * a.ld_res_out, i, lane, lanes, N, h[i]);
+  }
   ss = T::sum(ss, room);
   const double rr = 1.0 / sqrt(ss / N + a.eps);
   const float r = (float)rr;
-  if (a.res_out && active) {
-#pragma unroll
-    for (int i = 0; i < C; ++i) store_chunk<L, Vec>((S*)a.res_out + t * a.ld_res_out, i, lane, N, h[i]);
-  }
   if (a.out && active) {
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       float y[8];
+      load_chunk<Vec>(a.w, i, lane, lanes, N, y);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) y[q] = h[i][q] * r * w[i][q];
-      store_chunk<L, Vec>(a.out + t * a.ld_out, i, lane, N, y);
+      for (int q = 0; q < 8; ++q) y[q] *= h[i][q] * r;
+      store_chunk<Vec>(a.out + t * a.ld_out, i, lane, lanes, N, y);
     }
   }
   if (a.rstd && active && lane == 0) a.rstd[t] = r;
   if constexpr (Quant) {
     const int group = a.group, groups = N / group;
-    unsigned long long* mine = maxima + T::row() * groups;
-    uint64_t top[C], all = 0;
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-      top[i] = 0;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) top[i] = larger(top[i], magnitude((double)h[i][q] * (double)w[i][q]));
-      all = larger(all, top[i]);
-    }
-    auto scale_of = [&](uint64_t m) {
-      const float s = (float)(__longlong_as_double((long long)m) * rr / kE4m3Max);
+    auto weights = [&](int i, float (&w)[8]) { load_chunk<Vec>(a.w, i, lane, lanes, N, w); };
+    const double unit = rr / kE4m3Max;
+    auto scale_of = [&](double top) {
+      const float s = (float)(top * unit);
       return s < 0x1p-126f ? 0x1p-126f : s;
     };
-    float s[C][Vec ? 1 : 8];
-    if (Vec && group < N) {  // group / 8 neighbouring lanes
+    auto value_of = [](unsigned long long m) { return __builtin_bit_cast(double, m); };
+    uint8_t* row8 = a.out8 + t * a.ld_out8;
+    float one = 0.0f;  // the row's scale
+    if (group == N) {
+      unsigned long long all = 0;
 #pragma unroll
       for (int i = 0; i < C; ++i) {
-        uint64_t m = top[i];
-        for (int d = 1; d < group / 8; d *= 2) m = larger(m, (uint64_t)__shfl_xor((unsigned long long)m, d, 64));
-        s[i][0] = scale_of(m);
-        const int c = column<L, true>(i, 0, lane);
-        if (active && c < N && c % group == 0) a.scales[t * groups + c / group] = s[i][0];
+        float w[8];
+        weights(i, w);
+        all = larger(all, top_of<double>(h[i], w));
       }
-    } else if (group == N) {
 #pragma unroll
-      for (int d = 32; d; d >>= 1) all = larger(all, (uint64_t)__shfl_xor((unsigned long long)all, d, 64));
-      if constexpr (W > 1) {
-        if ((threadIdx.x & 63) == 0) room[threadIdx.x >> 6] = __longlong_as_double((long long)all);
+      for (int d = 32; d; d >>= 1) all = larger(all, __shfl_xor(all, d, 64));
+      if constexpr (Wide) {
+        const int waves = blockDim.x >> 6;
+        unsigned long long* tops = (unsigned long long*)room;
+        if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = all;
+        __syncthreads();
+        for (int i = 0; i < waves; ++i) all = larger(all, tops[i]);
+      }
+      one = scale_of(value_of(all));
+      if (active && lane == 0) a.scales[t] = one;
+    }
+    if constexpr (Vec) {
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        float w[8], s = one;
+        weights(i, w);
+        const int c = column<true>(i, 0, lane, lanes);
+        if (group < N) {  // group / 8 neighbouring lanes
+          double top;
+          bool small = false;
+          if constexpr (sizeof(S) == 2) {
+            uint32_t m = top_of<float>(h[i], w);
+            m = largest_of(m, group / 8);
+            small = __all(fp32_top(m) || c >= N);
+            top = __uint_as_float(m);
+          }
+          if (!small) {
+            top = value_of(largest_of(top_of<double>(h[i], w), group / 8));
+          }
+          s = scale_of(top);
+          if (active && c < N && c % group == 0) a.scales[t * groups + c / group] = s;
+        }
+        uint32_t p[2];
+        to_e4m3(h[i], w, rr, s, p);
+        if (active && c < N) *(uint2*)(row8 + c) = make_uint2(p[0], p[1]);
+      }
+    } else {
+      unsigned long long* mine = maxima + T::row() * groups;
+      if (group < N) {
+        for (int g = lane; g < groups; g += lanes) mine[g] = 0;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < W; ++i) all = larger(all, (uint64_t)__double_as_longlong(room[i]));
+        for (int i = 0; i < C; ++i) {
+          float w[8];
+          weights(i, w);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const int c = column<false>(i, q, lane, lanes);
+            if (c < N) atomicMax(mine + c / group, magnitude((double)h[i][q] * (double)w[q]));
+          }
+        }
+        __syncthreads();
+        for (int g = lane; g < groups && active; g += lanes) a.scales[t * groups + g] = scale_of(value_of(mine[g]));
       }
-      const float one = scale_of(all);
 #pragma unroll
-      for (int i = 0; i < C; ++i)
-#pragma unroll
-        for (int q = 0; q < (Vec ? 1 : 8); ++q) s[i][q] = one;
-      if (active && lane == 0) a.scales[t] = one;
-    } else {
-      for (int g = lane; g < groups; g += L) mine[g] = 0;
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < C; ++i)
+      for (int i = 0; i < C; ++i) {
+        float w[8];
+        weights(i, w);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          const int c = column<L, Vec>(i, q, lane);
-          if (c < N) atomicMax(mine + c / group, (unsigned long long)magnitude((double)h[i][q] * (double)w[i][q]));
-        }
-      __syncthreads();
-      for (int g = lane; g < groups && active; g += L) a.scales[t * groups + g] = scale_of(mine[g]);
-#pragma unroll
-      for (int i = 0; i < C; ++i)
-#pragma unroll
-        for (int q = 0; q < (Vec ? 1 : 8); ++q) {
-          const int c = column<L, Vec>(i, q, lane);
-          s[i][q] = scale_of(mine[c < N ? c / group : 0]);
-        }
-    }
-    if (!active) return;
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-      float y[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        y[q] = to_odd((double)h[i][q] * (double)w[i][q] * (rr / (double)s[i][Vec ? 0 : q]));
-      uint32_t p[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        int u = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * k], y[4 * k + 1], 0, false);
-        p[k] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[4 * k + 2], y[4 * k + 3], u, true);
-      }
-      uint8_t* row8 = a.out8 + t * a.ld_out8;
-      if constexpr (Vec) {
-        const int c = column<L, true>(i, 0, lane);
-        if (c < N) *(uint2*)(row8 + c) = make_uint2(p[0], p[1]);
-      } else {
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const int c = column<L, false>(i, q, lane);
-          if (c < N) row8[c] = (uint8_t)(p[q / 4] >> (8 * (q % 4)));
+          const int c = column<false>(i, q, lane, lanes);
+          const float s = group == N ? one : scale_of(value_of(mine[c < N ? c / group : 0]));
+          const float y = to_odd((double)h[i][q] * (double)w[q] * (rr / (double)s));
+          if (active && c < N) row8[c] = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(y, y, 0, false);
         }
       }
     }
@@ -296,61 +380,158 @@ __global__ __launch_bounds__(Team<W>::kThreads) void norm_kernel(NormArgs a) {
 
 // ---- backward ---------------------------------------------------------------
 
-// Team i takes the rows i, i + teams, ...; each leaves its sum for dw in parts[i].
-template <int W, int C, bool Vec, typename S>
-__global__ __launch_bounds__(Team<W>::kThreads) void norm_backward_kernel(NormBackwardArgs a, int teams) {
-  using T = Team<W>;
-  constexpr int L = T::kLanes;
-  __shared__ float room[W];
-  const int lane = T::lane(), N = a.N;
-  const int team = blockIdx.x * T::kRows + T::row();
-  float w[C][8], acc[C][8];
-#pragma unroll
-  for (int i = 0; i < C; ++i) {
-    load_chunk<L, Vec>(a.w, i, lane, N, w[i]);
-#pragma unroll
-    for (int q = 0; q < 8; ++q) acc[i][q] = 0.0f;
+// A chunk as it was loaded: 16 or 32 bytes of neighbours, else 8 values.
+template <bool Vec, typename T>
+struct Raw {
+  std::conditional_t<Vec, uint4, float> v[Vec ? (sizeof(T) == 2 ? 1 : 2) : 8];
+  __device__ __forceinline__ void load(const T* row, int i, int lane, int lanes, int N) {
+    if constexpr (Vec) {
+      const int c = column<true>(i, 0, lane, lanes);
+      const uint4* p = (const uint4*)beside(row, c < N ? c : 0);
+      v[0] = p[0];
+      if constexpr (sizeof(T) == 4) v[1] = p[1];
+    } else {
+      load_chunk<false>(row, i, lane, lanes, N, v);
+    }
   }
-  if (team >= teams) return;  // (a whole wave of a one-wave team)
-  const float inv_n = 1.0f / (float)N;
-  for (int64_t t = team; t < a.M; t += teams) {
-    float g[C][8], n[C][8], d[C][8];
+  // What follows does not see that it is the value from before: else the compiler
+  // keeps the unpacked values in twice the registers.
+  __device__ __forceinline__ void forget() {
+    if constexpr (Vec) {
+#pragma unroll
+      for (auto& x : v) asm volatile("" : "+v"(x.x), "+v"(x.y), "+v"(x.z), "+v"(x.w));
+    }
+  }
+  __device__ __forceinline__ void values(float (&o)[8]) const {
+    if constexpr (!Vec) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) o[q] = v[q];
+    } else if constexpr (sizeof(T) == 2) {
+      unpack8(v[0], o);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        o[4 * q] = __uint_as_float(v[q].x);
+        o[4 * q + 1] = __uint_as_float(v[q].y);
+        o[4 * q + 2] = __uint_as_float(v[q].z);
+        o[4 * q + 3] = __uint_as_float(v[q].w);
+      }
+    }
+  }
+};
+
+// The rows of a team's turn, one in flight while another is computed where the
+// registers allow it (16-byte chunks of bf16, at most 2 a lane).
+template <int C, bool Vec, typename S>
+struct BackwardRow {
+  Raw<Vec, uint16_t> g[C];
+  Raw<Vec, S> h[C], d[C];
+  float r;
+  __device__ __forceinline__ void load(const NormBackwardArgs& a, int64_t t, int lane, int lanes) {
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      load_chunk<L, Vec>(a.dout + t * a.ld_dout, i, lane, N, g[i]);
-      load_chunk<L, Vec>((const S*)a.h + t * a.ld_h, i, lane, N, n[i]);
-      if (a.dres) load_chunk<L, Vec>((const S*)a.dres + t * a.ld_dres, i, lane, N, d[i]);
+      g[i].load(a.dout + t * a.ld_dout, i, lane, lanes, a.N);
+      h[i].load((const S*)a.h + t * a.ld_h, i, lane, lanes, a.N);
+      if (C <= 2 && a.dres) d[i].load((const S*)a.dres + t * a.ld_dres, i, lane, lanes, a.N);
     }
-    const float r = a.rstd[t];
+    r = a.rstd[t];
+  }
+};
+
+// A workgroup takes the rows kRows (blockIdx.x + n gridDim.x) + 0 .. kRows - 1
+// and leaves their sums for dw in parts[blockIdx.x].
+template <bool Wide, int C, bool Vec, typename S>
+__global__ __launch_bounds__(Wide ? 64 * kMaxWaves : 256) void norm_backward_kernel(NormBackwardArgs a) {
+  using T = Team<Wide>;
+  constexpr bool kAhead = Vec && C <= 2 && sizeof(S) == 2;
+  __shared__ float room[kMaxWaves];
+  extern __shared__ __align__(16) float sums[];  // not Wide: [kRows][N]
+  const int lane = T::lane(), lanes = T::lanes(), N = a.N;
+  const int64_t step = (int64_t)gridDim.x * T::kRows;
+  float acc[C][8];
+#pragma unroll
+  for (int i = 0; i < C; ++i)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) acc[i][q] = 0.0f;
+  Raw<Vec, uint16_t> w[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i)
+    if (C <= 2) w[i].load(a.w, i, lane, lanes, N);
+  const float inv_n = 1.0f / (float)N;
+  int64_t t = (int64_t)blockIdx.x * T::kRows + T::row();
+  BackwardRow<C, Vec, S> next;
+  if (kAhead && t < a.M) next.load(a, t, lane, lanes);
+  for (; t < a.M; t += step) {
+    BackwardRow<C, Vec, S> row;
+    if constexpr (kAhead) {
+      row = next;
+      next.load(a, t + step < a.M ? t + step : t, lane, lanes);
+    } else {
+      row.load(a, t, lane, lanes);
+    }
     float dot = 0.0f;
 #pragma unroll
-    for (int i = 0; i < C; ++i)
+    for (int i = 0; i < C; ++i) {
+      float g[8], n[8], wv[8];
+      row.g[i].values(g);
+      row.h[i].values(n);
+      if (C > 2) w[i].load(a.w, i, lane, lanes, N);
+      w[i].values(wv);
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        if (column<L, Vec>(i, q, lane) >= N) g[i][q] = n[i][q] = 0.0f;
-        n[i][q] *= r;
-        acc[i][q] = fmaf(g[i][q], n[i][q], acc[i][q]);
-        g[i][q] *= w[i][q];
-        dot = fmaf(g[i][q], n[i][q], dot);
+        if (column<Vec>(i, Vec ? 0 : q, lane, lanes) >= N) g[q] = n[q] = 0.0f;  // (Vec: N % 8 == 0)
+        n[q] *= row.r;
+        acc[i][q] = fmaf(g[q], n[q], acc[i][q]);
+        dot = fmaf(g[q] * wv[q], n[q], dot);
+        // now, not behind the row's sum: that would keep g and n unpacked over it
+        asm volatile("" : "+v"(acc[i][q]));
       }
+    }
     dot = T::sum(dot, room) * inv_n;
     if (a.dh) {
 #pragma unroll
       for (int i = 0; i < C; ++i) {
-        float y[8];
+        float y[8], n[8], wv[8];
+        row.g[i].forget();
+        row.h[i].forget();
+        w[i].forget();
+        row.g[i].values(y);
+        row.h[i].values(n);
+        if (C > 2) w[i].load(a.w, i, lane, lanes, N);
+        w[i].values(wv);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) y[q] = r * (g[i][q] - n[i][q] * dot) + (a.dres ? d[i][q] : 0.0f);
-        store_chunk<L, Vec>((S*)a.dh + t * a.ld_dh, i, lane, N, y);
+        for (int q = 0; q < 8; ++q) y[q] = row.r * (y[q] * wv[q] - n[q] * row.r * dot);
+        if (a.dres) {
+          float d[8];
+          if (C > 2) row.d[i].load((const S*)a.dres + t * a.ld_dres, i, lane, lanes, N);
+          row.d[i].values(d);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) y[q] += d[q];
+        }
+        store_chunk<Vec>((S*)a.dh + t * a.ld_dh, i, lane, lanes, N, y);
       }
     }
   }
-  if (a.dw) {
+  if (!a.dw) return;
+  float* part = a.parts + (int64_t)blockIdx.x * N;
+  if constexpr (Wide) {
 #pragma unroll
-    for (int i = 0; i < C; ++i) store_chunk<L, Vec>(a.parts + (int64_t)team * N, i, lane, N, acc[i]);
+    for (int i = 0; i < C; ++i) store_chunk<Vec>(part, i, lane, lanes, N, acc[i]);
+  } else {  // the waves' sums, in order
+    float* mine = sums + T::row() * N;
+#pragma unroll
+    for (int i = 0; i < C; ++i) store_chunk<Vec>(mine, i, lane, lanes, N, acc[i]);
+    __syncthreads();
+    for (int c = threadIdx.x; c < N; c += 256) {
+      float s = sums[c];
+#pragma unroll
+      for (int k = 1; k < T::kRows; ++k) s += sums[k * N + c];
+      part[c] = s;
+    }
   }
 }
 
-// dw = the teams' sums, added in order by 16 rows of lanes, in fp64.
+// dw = the workgroups' sums, added in order by 16 rows of lanes, in fp64.
 constexpr int kJoinRows = 16;
 __global__ __launch_bounds__(64 * kJoinRows) void norm_join_kernel(const float* parts, int teams, int N, float* dw) {
   __shared__ double sums[kJoinRows][64];
@@ -377,18 +558,18 @@ __global__ __launch_bounds__(64 * kJoinRows) void norm_join_kernel(const float* 
   }
 }
 
-// fn(W, C) for the row width
+// fn(Wide, C, threads) for the row width. 2 chunks a lane: with 1 or 4 of them
+// [16384, 7168] bf16 took 182 and 167 us instead of 163. From 1025 columns on the
+// waves of a workgroup share a row ([8192, 2048]: 25.9 us, 28.5 with a wave a row).
 template <typename F>
 void by_width(int N, F fn) {
-  auto go = [&](auto w, auto c) { fn(w, c); };
   using std::integral_constant;
-  if (N <= 512) go(integral_constant<int, 1>{}, integral_constant<int, 1>{});
-  else if (N <= 1024) go(integral_constant<int, 1>{}, integral_constant<int, 2>{});
-  else if (N <= 2048) go(integral_constant<int, 1>{}, integral_constant<int, 4>{});
-  else if (N <= 4096) go(integral_constant<int, 4>{}, integral_constant<int, 2>{});
-  else if (N <= 8192) go(integral_constant<int, 4>{}, integral_constant<int, 4>{});
-  else if (N <= 16384) go(integral_constant<int, 16>{}, integral_constant<int, 2>{});
-  else go(integral_constant<int, 16>{}, integral_constant<int, 4>{});
+  auto one = [&](auto c) { fn(std::false_type{}, c, 256u); };
+  auto all = [&](auto c) { fn(std::true_type{}, c, 64u * (unsigned)ceil_div(N, 512 * decltype(c)::value)); };
+  if (N <= 512) one(integral_constant<int, 1>{});
+  else if (N <= 1024) one(integral_constant<int, 2>{});
+  else if (N <= 16384) all(integral_constant<int, 2>{});
+  else all(integral_constant<int, 4>{});
 }
 
 // 16-byte chunks of 8 columns in every row of a matrix of `size`-byte elements
@@ -403,14 +584,15 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
   const bool vec = a.N % 8 == 0 && chunks_ok(a.x, a.ldx, 2) && chunks_ok(a.res, a.ld_res, size) &&
                    chunks_ok(a.res_out, a.ld_res_out, size) && chunks_ok(a.w, 8, 2) && chunks_ok(a.out, a.ld_out, 2) &&
                    chunks_ok(a.out8, a.ld_out8, 1);
-  by_width(a.N, [&](auto w, auto c) {
-    constexpr int W = decltype(w)::value, C = decltype(c)::value;
+  by_width(a.N, [&](auto wide, auto c, unsigned threads) {
+    constexpr bool W = decltype(wide)::value;
+    constexpr int C = decltype(c)::value;
     const unsigned grid = (unsigned)ceil_div(a.M, Team<W>::kRows);
     auto go = [&](auto v, auto s, auto quant) {
       constexpr bool V = decltype(v)::value, Q = decltype(quant)::value;
       using S = decltype(s);
       const unsigned lds = Q && !V && a.group < a.N ? (unsigned)(a.N / a.group * 8 * Team<W>::kRows) : 0;
-      norm_kernel<W, C, V, S, Q><<<grid, Team<W>::kThreads, lds, stream>>>(a);
+      norm_kernel<W, C, V, S, Q><<<grid, threads, lds, stream>>>(a);
     };
     auto typed = [&](auto v, auto quant) { a.f32 ? go(v, float{}, quant) : go(v, uint16_t{}, quant); };
     auto quanted = [&](auto v) { a.out8 ? typed(v, std::true_type{}) : typed(v, std::false_type{}); };
@@ -419,21 +601,27 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Teams of a backward pass: enough loads in flight for the memory, few enough
-// that the sums they leave are small beside the rows.
-int norm_backward_parts(int64_t M) { return (int)(M < 512 ? (M < 1 ? 1 : M) : 512); }
+// Workgroups of a backward pass. A CU's one workgroup of wide rows keeps a row
+// in flight while it computes another; more of them only leave more sums and
+// spread the rows in flight ([16384, 7168] bf16: 173 us with 256, 189 with 512, 196
+// with 1024; of 2048 columns 76, 58 and 58).
+int norm_backward_parts(int64_t M, int64_t N) {
+  const int64_t most = N > 2048 ? 256 : N > 1024 ? 512 : 1024, n = N > 1024 ? M : ceil_div(M, 4);
+  return (int)(n < 1 ? 1 : n < most ? n : most);
+}
 
 hipError_t launch_norm_backward(const NormBackwardArgs& a, hipStream_t stream) {
   const int size = a.f32 ? 4 : 2;
-  const int teams = norm_backward_parts(a.M);
+  const int teams = norm_backward_parts(a.M, a.N);
   if (a.M > 0 && (a.dh || a.dw)) {
     const bool vec = a.N % 8 == 0 && chunks_ok(a.dout, a.ld_dout, 2) && chunks_ok(a.h, a.ld_h, size) &&
                      chunks_ok(a.w, 8, 2) && chunks_ok(a.dres, a.ld_dres, size) && chunks_ok(a.dh, a.ld_dh, size);
-    by_width(a.N, [&](auto w, auto c) {
-      constexpr int W = decltype(w)::value, C = decltype(c)::value;
-      const unsigned grid = (unsigned)ceil_div(teams, Team<W>::kRows);
+    by_width(a.N, [&](auto wide, auto c, unsigned threads) {
+      constexpr bool W = decltype(wide)::value;
+      constexpr int C = decltype(c)::value;
+      const unsigned lds = W ? 0u : (unsigned)(Team<W>::kRows * a.N * 4);
       auto go = [&](auto v, auto s) {
-        norm_backward_kernel<W, C, decltype(v)::value, decltype(s)><<<grid, Team<W>::kThreads, 0, stream>>>(a, teams);
+        norm_backward_kernel<W, C, decltype(v)::value, decltype(s)><<<teams, threads, lds, stream>>>(a);
       };
       auto typed = [&](auto v) { a.f32 ? go(v, float{}) : go(v, uint16_t{}); };
       vec ? typed(std::true_type{}) : typed(std::false_type{});

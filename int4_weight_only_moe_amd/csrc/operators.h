@@ -165,9 +165,9 @@ struct NormBackwardArgs {
   void* dh;                  // [M, N] or null
   int64_t ld_dh;
   float* dw;                 // [N] or null
-  float* parts;              // [norm_backward_parts(M), N]
+  float* parts;              // [norm_backward_parts(M, N), N]
 };
-int norm_backward_parts(int64_t M);  // rows of partial weight gradients
+int norm_backward_parts(int64_t M, int64_t N);  // rows of partial weight gradients
 hipError_t launch_norm_backward(const NormBackwardArgs& a, hipStream_t stream);
 
 // ---- gradient norm and clipping ----------------------------------------------

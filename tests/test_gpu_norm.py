@@ -6,7 +6,8 @@ off by half a step (2^-8 relative) and the roundings of 2^-24 that come before
 it: r carries 1, two products 1 each. Gradients count, per term: n = h r 1 (r is
 given), u = w g exact, their product and the running sum over the lane's columns
 (at most 32) and 6 + 4 + 15 to join lanes and waves, the mean 2, three more
-steps; dw: its rows of one team (M / 512, rounded up) and 3, the rest is fp64."""
+steps; dw: the rows that one lane adds (at most M / 256, rounded up: of workgroups of
+wide rows), 3 to join the waves of narrow rows, the rest is fp64."""
 import itertools
 
 import numpy as np
@@ -196,7 +197,7 @@ def check_backward(M, N, dtype, seed, passed=True, gap=0, shift=0, in_place=None
     else:
         assert got is None
     err = np.abs(f64(gw) - dw)
-    assert (err <= (-(-M // 512) + 3 + 1) * U * wmag + U * np.abs(dw) + 2.0 ** -149).all()
+    assert (err <= (-(-M // 256) + 3 + 1) * U * wmag + U * np.abs(dw) + 2.0 ** -149).all()
     return got, gw
 
 
