@@ -574,8 +574,9 @@ int moe_add_rms_norm_backward(const uint16_t* grad_out_bf16, int64_t ld_grad_out
  *   sumsq = sum of the squares of all elements, fp64
  *   norm = sqrt(sumsq);  out_i = grad_i * (norm > max_norm ? max_norm / norm : 1)
  * moe_grad_sumsq writes sumsq; a data-parallel job may sum it over its ranks
- * before moe_grad_clip scales. A sum that is not finite scales nothing (norm
- * says so: leave the step out).
+ * before moe_grad_clip scales. moe_clip_grad_norm does both (a launch less for
+ * up to 192 tensors). A sum that is not finite scales nothing (norm says so:
+ * leave the step out).
  *
  *   grads, outs, sizes, dtypes: host arrays of n entries, read during the call:
  *               contiguous device tensors (outs_i may be grads_i: in place),
@@ -596,6 +597,9 @@ int moe_grad_sumsq(const void* const* grads, const int64_t* sizes, const int32_t
                    void* workspace, int64_t workspace_bytes, void* stream);
 int moe_grad_clip(const void* const* grads, void* const* outs, const int64_t* sizes, const int32_t* dtypes, int32_t n,
                   const double* sumsq, float max_norm, float* norm, void* stream);
+int moe_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* sizes, const int32_t* dtypes,
+                       int32_t n, float max_norm, double* sumsq, float* norm, void* workspace, int64_t workspace_bytes,
+                       void* stream);
 
 /* Measurement helpers (not part of the layer). They measure what this GPU
  * sustains, so that a layer kernel's rate can be stated as a fraction of the

@@ -32,7 +32,7 @@ from ._binding import (  # noqa: F401
     moe_lora_backward, moe_lora_forward, moe_lora_workspace_bytes,
     MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX, moe_route_scored, moe_route_scored_backward, moe_add_rms_norm,
     moe_add_rms_norm_backward, moe_add_rms_norm_workspace_bytes, moe_grad_clip, moe_grad_norm_workspace_bytes,
-    moe_grad_sumsq,
+    moe_grad_sumsq, moe_clip_grad_norm,
 )
 
 FORMATS = ("int4", "mxfp4")  # weight formats: INT4 g32 + fp16 scales, MXFP4 (e2m1 + E8M0 per 32)
@@ -388,7 +388,17 @@ def grad_clip(grads, sumsq: torch.Tensor, max_norm: float, out=None, norm: torch
     return norm
 
 
-def clip_grad_norm(grads, max_norm: float, out=None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """grad_sumsq and grad_clip: clips the gradients by their global norm, in
-    place or into the tensors of out; returns the norm before, float32 [1]."""
-    return grad_clip(grads, grad_sumsq(grads, workspace=workspace, stream=stream), max_norm, out=out, stream=stream)
+def clip_grad_norm(grads, max_norm: float, out=None, workspace: torch.Tensor | None = None,
+                   norm: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """grad_sumsq and grad_clip in one call: clips the gradients by their global
+    norm, in place or into the tensors of out; returns the norm before, float32 [1]."""
+    if not grads:
+        raise ValueError("no gradients")
+    device = grads[0].device
+    workspace = _grads_workspace(grads, device, workspace, stream)
+    with _memory_of(stream, device):
+        sumsq = torch.empty(1, dtype=torch.float64, device=device)
+        if norm is None:
+            norm = torch.empty(1, dtype=torch.float32, device=device)
+    moe_clip_grad_norm(grads, grads if out is None else out, max_norm, sumsq, workspace, norm=norm, stream=stream)
+    return norm

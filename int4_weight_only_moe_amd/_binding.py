@@ -85,6 +85,7 @@ _SIGNATURES["moe_add_rms_norm_backward"] = (ctypes.c_int, [_vp, _i64, _vp, _i64,
 _SIGNATURES["moe_grad_norm_workspace_bytes"] = (_i64, [_i32])
 _SIGNATURES["moe_grad_sumsq"] = (ctypes.c_int, [_vp, _vp, _vp, _i32, _vp, _vp, _i64, _vp])
 _SIGNATURES["moe_grad_clip"] = (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _vp, _f32, _vp, _vp])
+_SIGNATURES["moe_clip_grad_norm"] = (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _f32, _vp, _vp, _vp, _i64, _vp])
 _SIGNATURES["moe_calib_read_granule"] = (_i64, [])
 _SIGNATURES["moe_calib_hbm_read"] = (ctypes.c_int, [_vp, _i64, _i32, _vp, _vp])
 _SIGNATURES["moe_calib_mfma_f16"] = (ctypes.c_int, [_i64, _i32, _vp, _vp])
@@ -621,12 +622,11 @@ def moe_grad_norm_workspace_bytes(n: int) -> int:
 
 def _grad_arrays(grads, device: torch.device) -> tuple:
     """(pointers, sizes, types) of contiguous bf16 or fp32 tensors, as host arrays."""
-    for t in grads:
-        if t.dtype not in _SIDE_DTYPES or t.device != device or not t.is_contiguous():
-            raise ValueError(f"gradients must be contiguous bfloat16 or float32 tensors on {device}")
     n = len(grads)
-    return ((ctypes.c_void_p * n)(*[t.data_ptr() for t in grads]), (_i64 * n)(*[t.numel() for t in grads]),
-            (_i32 * n)(*[_SIDE_DTYPES[t.dtype] for t in grads]))
+    kinds = [_SIDE_DTYPES.get(t.dtype, -1) if t.device == device and t.is_contiguous() else -1 for t in grads]
+    if -1 in kinds:
+        raise ValueError(f"gradients must be contiguous bfloat16 or float32 tensors on {device}")
+    return ((_vp * n)(*[t.data_ptr() for t in grads]), (_i64 * n)(*[t.numel() for t in grads]), (_i32 * n)(*kinds))
 
 
 def moe_grad_sumsq(grads, sumsq: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
@@ -637,21 +637,35 @@ def moe_grad_sumsq(grads, sumsq: torch.Tensor, workspace: torch.Tensor, stream=N
                _shaped(sumsq, torch.float64, (1,), "sumsq", dev), *_buffer(workspace, "workspace", dev))
 
 
-def moe_grad_clip(grads, outs, sumsq: torch.Tensor, max_norm: float, norm: torch.Tensor | None = None,
-                  stream=None) -> None:
-    """outs: a sequence of tensors like grads (the same ones: in place)."""
-    dev = sumsq.device
+def _clip_arrays(grads, outs, device: torch.device) -> tuple:
+    """(gradients' pointers, results' pointers, sizes, types) as host arrays."""
+    ptrs, sizes, kinds = _grad_arrays(grads, device)
+    if outs is grads:
+        return ptrs, ptrs, sizes, kinds
     if len(outs) != len(grads):
         raise ValueError("outs must have as many tensors as grads")
-    ptrs, sizes, kinds = _grad_arrays(grads, dev)
-    to = ptrs
-    if outs is not grads:
-        to, osizes, okinds = _grad_arrays(outs, dev)
-        if list(osizes) != list(sizes) or list(okinds) != list(kinds):
-            raise ValueError("outs must have the sizes and types of grads")
-    _on_device(dev, "moe_grad_clip", stream, ptrs, to, sizes, kinds, len(grads),
+    to, osizes, okinds = _grad_arrays(outs, device)
+    if bytes(osizes) != bytes(sizes) or bytes(okinds) != bytes(kinds):
+        raise ValueError("outs must have the sizes and types of grads")
+    return ptrs, to, sizes, kinds
+
+
+def moe_grad_clip(grads, outs, sumsq: torch.Tensor, max_norm: float, norm: torch.Tensor | None = None,
+                  stream=None) -> None:
+    """outs: a sequence of tensors like grads (the same one: in place)."""
+    dev = sumsq.device
+    _on_device(dev, "moe_grad_clip", stream, *_clip_arrays(grads, outs, dev), len(grads),
                _shaped(sumsq, torch.float64, (1,), "sumsq", dev), max_norm,
                _shaped(norm, torch.float32, (1,), "norm", dev))
+
+
+def moe_clip_grad_norm(grads, outs, max_norm: float, sumsq: torch.Tensor, workspace: torch.Tensor,
+                       norm: torch.Tensor | None = None, stream=None) -> None:
+    """moe_grad_sumsq and moe_grad_clip in one call."""
+    dev = sumsq.device
+    _on_device(dev, "moe_clip_grad_norm", stream, *_clip_arrays(grads, outs, dev), len(grads), max_norm,
+               _shaped(sumsq, torch.float64, (1,), "sumsq", dev), _shaped(norm, torch.float32, (1,), "norm", dev),
+               *_buffer(workspace, "workspace", dev))
 
 
 # ------------------------------------------------------------------ measurement helpers

@@ -104,6 +104,15 @@ bool outs_apart(const void* const* grads, void* const* outs, const int64_t* size
   return true;
 }
 
+int check_outs(const void* const* grads, void* const* outs, const int64_t* sizes, const int32_t* dtypes, int32_t n,
+               const double* sumsq, float max_norm, const float* norm) {
+  if (!(max_norm >= 0.0f) || !sumsq || !aligned(sumsq, 8) || !aligned(norm, 4) || (n > 0 && !outs))
+    return MOE_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < n; ++i)
+    if ((sizes[i] > 0 && !outs[i]) || !aligned(outs[i], dtypes[i] == MOE_DTYPE_F32 ? 4 : 2)) return MOE_ERR_INVALID_ARG;
+  return outs_apart(grads, outs, sizes, dtypes, n) ? MOE_OK : MOE_ERR_INVALID_ARG;
+}
+
 }  // namespace
 
 extern "C" {
@@ -354,17 +363,29 @@ int moe_grad_sumsq(const void* const* grads, const int64_t* sizes, const int32_t
 
 int moe_grad_clip(const void* const* grads, void* const* outs, const int64_t* sizes, const int32_t* dtypes, int32_t n,
                   const double* sumsq, float max_norm, float* norm, void* stream) {
-  const int st = check_grads(grads, sizes, dtypes, n);
+  int st = check_grads(grads, sizes, dtypes, n);
   if (st != MOE_OK) return st;
-  if (!(max_norm >= 0.0f) || !sumsq || !aligned(sumsq, 8) || !aligned(norm, 4) || (n > 0 && !outs))
-    return MOE_ERR_INVALID_ARG;
-  for (int32_t i = 0; i < n; ++i)
-    if ((sizes[i] > 0 && !outs[i]) || !aligned(outs[i], dtypes[i] == MOE_DTYPE_F32 ? 4 : 2)) return MOE_ERR_INVALID_ARG;
-  if (!outs_apart(grads, outs, sizes, dtypes, n)) return MOE_ERR_INVALID_ARG;
+  st = check_outs(grads, outs, sizes, dtypes, n, sumsq, max_norm, norm);
+  if (st != MOE_OK) return st;
   moe::ClipArgs a{};
   a.grads = grads; a.outs = outs; a.sizes = sizes; a.dtypes = dtypes; a.n = n;
   a.sumsq = const_cast<double*>(sumsq); a.max_norm = max_norm; a.norm = norm;
   return hip_status(moe::launch_grad_clip(a, (hipStream_t)stream));
+}
+
+int moe_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* sizes, const int32_t* dtypes,
+                       int32_t n, float max_norm, double* sumsq, float* norm, void* workspace, int64_t workspace_bytes,
+                       void* stream) {
+  int st = check_grads(grads, sizes, dtypes, n);
+  if (st != MOE_OK) return st;
+  st = check_outs(grads, outs, sizes, dtypes, n, sumsq, max_norm, norm);
+  if (st != MOE_OK) return st;
+  if (!workspace || !aligned(workspace, 16)) return MOE_ERR_INVALID_ARG;
+  if (workspace_bytes < moe_grad_norm_workspace_bytes(n)) return MOE_ERR_WORKSPACE;
+  moe::ClipArgs a{};
+  a.grads = grads; a.outs = outs; a.sizes = sizes; a.dtypes = dtypes; a.n = n; a.sumsq = sumsq;
+  a.max_norm = max_norm; a.norm = norm; a.parts = (double*)workspace;
+  return hip_status(moe::launch_clip_grad_norm(a, (hipStream_t)stream));
 }
 
 }  // extern "C"

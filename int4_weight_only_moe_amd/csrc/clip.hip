@@ -2,11 +2,12 @@
 //
 //   sumsq = sum of g^2 over all elements (fp64);  out = g * min(1, max_norm / sqrt(sumsq))
 //
-// Both passes are bound by the tensors' traffic. The tensors of a launch lie
-// end to end in units of 2048 elements (each tensor's last unit may be short);
-// every workgroup takes an equal run of units, so the work is even however
-// large the tensors are. Squares are summed in fp64: no gradient over- or
-// underflows, and the conversions hide behind the loads.
+// Both passes are bound by the tensors' traffic. The tensors of a launch are cut
+// into units of 4096 elements (each tensor's last one may be short), workgroup b
+// takes the units b, b + blocks, ...: the work is even however large the tensors
+// are, and what is in flight lies together in memory (with a run of units a
+// workgroup the squares of 705 MB took 157 us). Squares are summed in fp64: no
+// gradient over- or underflows, and the conversions hide behind the loads.
 #include "../../include/moe_w4a16.h"
 #include "device_common.h"
 #include "operators.h"
@@ -15,7 +16,8 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnit = 8 * kThreads;
+constexpr int kPasses = 2;  // of 8 elements a thread
+constexpr int kUnit = 8 * kThreads * kPasses;
 constexpr int kTensors = kClipTensorsPerLaunch;
 
 struct Table {
@@ -56,31 +58,27 @@ __device__ __forceinline__ void unpack8(uint4 p, float (&v)[8]) {
 }
 __device__ __forceinline__ uint16_t to_bf16(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
 
-// Eight elements of a thread in a whole unit. fp32: two runs of 4, each
-// instruction a contiguous 4 KB of the workgroup's.
-__device__ __forceinline__ void load_unit(const void* p, bool f32, int64_t first, float (&v)[8]) {
-  const int tid = threadIdx.x;
-  if (f32) {
-    const float4* q = (const float4*)((const float*)p + first);
-    const float4 a = q[tid], b = q[kThreads + tid];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    unpack8(((const uint4*)((const uint16_t*)p + first))[tid], v);
-  }
-}
-__device__ __forceinline__ void store_unit(void* p, bool f32, int64_t first, const float (&v)[8]) {
-  const int tid = threadIdx.x;
-  if (f32) {
-    float4* q = (float4*)((float*)p + first);
-    q[tid] = make_float4(v[0], v[1], v[2], v[3]);
-    q[kThreads + tid] = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-    uint32_t u[4];
+// The elements of a thread in a whole unit, as they lie in memory: in each pass 8,
+// fp32 as two runs of 4, each instruction a contiguous 4 KB of the workgroup's.
+struct Unit {
+  uint4 v[2 * kPasses];
+  __device__ __forceinline__ void load(const void* p, bool f32, int64_t first) {
+    if (f32) {
+      const uint4* q = (const uint4*)((const float*)p + first) + threadIdx.x;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = (uint32_t)to_bf16(v[2 * i]) | ((uint32_t)to_bf16(v[2 * i + 1]) << 16);
-    ((uint4*)((uint16_t*)p + first))[tid] = make_uint4(u[0], u[1], u[2], u[3]);
+      for (int j = 0; j < 2 * kPasses; ++j) v[j] = q[j * kThreads];
+    } else {
+      const uint4* q = (const uint4*)((const uint16_t*)p + first) + threadIdx.x;
+#pragma unroll
+      for (int j = 0; j < kPasses; ++j) v[j] = q[j * kThreads];
+    }
   }
+};
+__device__ __forceinline__ void four(uint4 u, float (&o)[4]) {
+  o[0] = __uint_as_float(u.x);
+  o[1] = __uint_as_float(u.y);
+  o[2] = __uint_as_float(u.z);
+  o[3] = __uint_as_float(u.w);
 }
 __device__ __forceinline__ float load_one(const void* p, bool f32, int64_t i) {
   return f32 ? ((const float*)p)[i] : __uint_as_float((uint32_t)((const uint16_t*)p)[i] << 16);
@@ -90,54 +88,61 @@ __device__ __forceinline__ void store_one(void* p, bool f32, int64_t i, float v)
   else ((uint16_t*)p)[i] = to_bf16(v);
 }
 
-// Workgroup b's run of the launch's units, one tensor after another: whole(i,
-// first, count) for `count` whole units of tensor i from element `first` on,
-// part(i, first, last) for elements that are to be taken one by one.
-template <typename Whole, typename Part>
+// Workgroup b's units, with `blocks` of them, one after another: whole(i, first)
+// for a unit of tensor i from element `first` on, part(i, first, last) for
+// elements that are to be taken one by one. Back: from the last unit to the first.
+template <bool kBack, typename Whole, typename Part>
 __device__ __forceinline__ void walk(const Table& tab, int64_t b, int64_t blocks, Whole whole, Part part) {
   const int64_t units = tab.end[tab.n - 1];
-  int64_t u = units * b / blocks;
-  const int64_t last = units * (b + 1) / blocks;
-  for (int i = tensor_of(tab, u); u < last; ++i) {
-    const int64_t start = i ? tab.end[i - 1] : 0;
-    const int64_t to = tab.end[i] < last ? tab.end[i] : last;
-    const int64_t first = (u - start) * kUnit;
-    int64_t stop = (to - start) * kUnit;
-    stop = stop < tab.size[i] ? stop : tab.size[i];
-    const int64_t count = aligned16(tab.grad[i]) && aligned16(tab.out[i]) ? (stop - first) / kUnit : 0;
-    if (count) whole(i, first, count);
-    if (first + count * kUnit < stop) part(i, first + count * kUnit, stop);
-    u = to;
+  int i = kBack ? tab.n - 1 : 0;
+  for (int64_t k = b; k < units; k += blocks) {
+    const int64_t u = kBack ? units - 1 - k : k;
+    if (kBack ? (i > 0 && tab.end[i - 1] > u) : tab.end[i] <= u) i = tensor_of(tab, u);
+    const int64_t first = (u - (i ? tab.end[i - 1] : 0)) * kUnit;
+    const int64_t size = tab.size[i];
+    if (first + kUnit <= size && aligned16(tab.grad[i]) && aligned16(tab.out[i])) whole(i, first);
+    else part(i, first, first + kUnit < size ? first + kUnit : size);
   }
 }
 
-constexpr int kAhead = 4;  // units in flight
+// The sum of a workgroup's threads' values, in every thread.
+template <int kWaves>
+__device__ __forceinline__ double block_sum(double s, double (&room)[kWaves]) {
+  s = wave_sum64(s);
+  if ((threadIdx.x & 63) == 0) room[threadIdx.x >> 6] = s;
+  __syncthreads();
+  s = room[0];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) s += room[w];
+  return s;
+}
 
 __global__ __launch_bounds__(kThreads) void grad_sumsq_kernel(Table tab, double* parts, double* direct) {
   __shared__ double room[kThreads / 64];
   double s = 0.0;
-  auto add = [&](const float (&v)[8]) {
-#pragma unroll
-    for (int q = 0; q < 8; ++q) s = fma((double)v[q], (double)v[q], s);
-  };
   if (tab.n) {
-    walk(
+    walk<false>(
         tab, blockIdx.x, gridDim.x,
-        [&](int i, int64_t first, int64_t count) {
-          const void* p = tab.grad[i];
+        [&](int i, int64_t first) {
           const bool f32 = tab.f32[i];
-          int64_t c = 0;
-          for (; c + kAhead <= count; c += kAhead) {
-            float v[kAhead][8];
+          Unit unit;
+          unit.load(tab.grad[i], f32, first);
+          if (f32) {
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) load_unit(p, f32, first + (c + j) * kUnit, v[j]);
+            for (int j = 0; j < 2 * kPasses; ++j) {
+              float v[4];
+              four(unit.v[j], v);
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) add(v[j]);
-          }
-          for (; c < count; ++c) {
-            float v[8];
-            load_unit(p, f32, first + c * kUnit, v);
-            add(v);
+              for (int q = 0; q < 4; ++q) s = fma((double)v[q], (double)v[q], s);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < kPasses; ++j) {
+              float v[8];
+              unpack8(unit.v[j], v);
+#pragma unroll
+              for (int q = 0; q < 8; ++q) s = fma((double)v[q], (double)v[q], s);
+            }
           }
         },
         [&](int i, int64_t first, int64_t stop) {
@@ -147,67 +152,85 @@ __global__ __launch_bounds__(kThreads) void grad_sumsq_kernel(Table tab, double*
           }
         });
   }
-  s = wave_sum64(s);
-  if ((threadIdx.x & 63) == 0) room[threadIdx.x >> 6] = s;
-  __syncthreads();
+  s = block_sum(s, room);
   if (threadIdx.x == 0) {
-    for (int w = 1; w < kThreads / 64; ++w) s += room[w];
     if (direct) *direct = s;
     else parts[blockIdx.x] = s;
   }
-  if (!direct && blockIdx.x == 0)  // the places of workgroups that this launch does not have
-    for (int b = gridDim.x + threadIdx.x; b < kSumsqBlocks; b += kThreads) parts[b] = 0.0;
 }
 
-// The launches' parts, in order.
+// The parts of all launches, in order.
 constexpr int kJoinThreads = 1024;
 __global__ __launch_bounds__(kJoinThreads) void grad_join_kernel(const double* parts, int64_t n, double* sumsq) {
   __shared__ double room[kJoinThreads / 64];
   double s = 0.0;
   for (int64_t i = threadIdx.x; i < n; i += kJoinThreads) s += parts[i];
-  s = wave_sum64(s);
-  if ((threadIdx.x & 63) == 0) room[threadIdx.x >> 6] = s;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < kJoinThreads / 64; ++w) s += room[w];
-    *sumsq = s;
-  }
+  s = block_sum(s, room);
+  if (threadIdx.x == 0) *sumsq = s;
+}
+
+// Results go around the cache: the gradients are then found there, and what reads
+// the results next takes no longer (squares, clipping and a reader of 705 MB of
+// results: 490 us, 518 with ordinary stores; of 88 MB 72 and 78; of 44 MB the same).
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ void put(uint4* p, uint4 v) {
+  __builtin_nontemporal_store(__builtin_bit_cast(u32x4_t, v), (u32x4_t*)p);
 }
 
 // The workgroups go through the tensors from the last to the first: what the
 // pass over the squares read last is still in the cache.
-__global__ __launch_bounds__(kThreads) void grad_clip_kernel(Table tab, const double* sumsq, float max_norm,
-                                                             float* norm) {
-  const double total = *sumsq, root = sqrt(total);
-  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)root;
+//
+// n_parts > 0: sumsq is still in that many parts, which every workgroup adds
+// itself, in the same order: one launch less, and up to kJoinParts of them cost less
+// than that.
+__global__ __launch_bounds__(kThreads) void grad_clip_kernel(Table tab, const double* parts, int n_parts,
+                                                             double* sumsq, float max_norm, float* norm) {
+  __shared__ double room[kThreads / 64];
+  double total;
+  if (n_parts > 0) {
+    double s = 0.0;
+#pragma unroll 8
+    for (int i = threadIdx.x; i < n_parts; i += kThreads) s += parts[i];
+    total = block_sum(s, room);
+  } else {
+    total = *sumsq;
+  }
+  const double root = sqrt(total);
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    if (norm) *norm = (float)root;
+    if (n_parts > 0 && sumsq) *sumsq = total;
+  }
   const bool over = root > (double)max_norm && root < INFINITY;
   const float factor = over ? (float)((double)max_norm / root) : 1.0f;
   if (!tab.n) return;
-  walk(
-      tab, gridDim.x - 1 - blockIdx.x, gridDim.x,
-      [&](int i, int64_t first, int64_t count) {
-        const void* p = tab.grad[i];
-        void* o = tab.out[i];
+  walk<true>(
+      tab, blockIdx.x, gridDim.x,
+      [&](int i, int64_t first) {
+        if (!over && tab.grad[i] == tab.out[i]) return;
         const bool f32 = tab.f32[i];
-        if (!over && p == o) return;
-        int64_t c = 0;
-        for (; c + kAhead <= count; c += kAhead) {
-          float v[kAhead][8];
+        Unit unit;
+        unit.load(tab.grad[i], f32, first);
+        if (f32) {
+          uint4* q = (uint4*)((float*)tab.out[i] + first) + threadIdx.x;
 #pragma unroll
-          for (int j = 0; j < kAhead; ++j) load_unit(p, f32, first + (c + j) * kUnit, v[j]);
-#pragma unroll
-          for (int j = 0; j < kAhead; ++j) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) v[j][q] *= factor;
-            store_unit(o, f32, first + (c + j) * kUnit, v[j]);
+          for (int j = 0; j < 2 * kPasses; ++j) {
+            float v[4];
+            four(unit.v[j], v);
+            put(q + j * kThreads, make_uint4(__float_as_uint(v[0] * factor), __float_as_uint(v[1] * factor),
+                                         __float_as_uint(v[2] * factor), __float_as_uint(v[3] * factor)));
           }
-        }
-        for (; c < count; ++c) {
-          float v[8];
-          load_unit(p, f32, first + c * kUnit, v);
+        } else {
+          uint4* q = (uint4*)((uint16_t*)tab.out[i] + first) + threadIdx.x;
 #pragma unroll
-          for (int q = 0; q < 8; ++q) v[q] *= factor;
-          store_unit(o, f32, first + c * kUnit, v);
+          for (int j = 0; j < kPasses; ++j) {
+            float v[8];
+            unpack8(unit.v[j], v);
+            uint32_t u[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              u[k] = (uint32_t)to_bf16(v[2 * k] * factor) | ((uint32_t)to_bf16(v[2 * k + 1] * factor) << 16);
+            put(q + j * kThreads, make_uint4(u[0], u[1], u[2], u[3]));
+          }
         }
       },
       [&](int i, int64_t first, int64_t stop) {
@@ -233,36 +256,65 @@ Table table_of(const ClipArgs& a, int64_t from, int64_t& units) {
   return tab;
 }
 
+constexpr int64_t kJoinParts = 2 * kSumsqBlocks;
+
 // Workgroups of a launch: a unit each, at most kSumsqBlocks (8 a CU).
 unsigned blocks_for(int64_t units) { return (unsigned)(units < 1 ? 1 : units < kSumsqBlocks ? units : kSumsqBlocks); }
 
 }  // namespace
 
-hipError_t launch_grad_sumsq(const ClipArgs& a, hipStream_t stream) {
+// The squares of all tensors, in `parts` pieces; a call of one workgroup writes
+// them to `direct` instead (if that is not null; 0 pieces).
+static hipError_t launch_squares(const ClipArgs& a, double* direct, int64_t& parts, hipStream_t stream) {
   const int64_t launches = clip_launches(a.n);
+  parts = 0;
   for (int64_t i = 0; i < (launches ? launches : 1); ++i) {
     int64_t units;
     const Table tab = table_of(a, i * kTensors, units);
     const unsigned blocks = blocks_for(units);
-    const bool only = launches <= 1 && blocks == 1;
-    grad_sumsq_kernel<<<blocks, kThreads, 0, stream>>>(tab, a.parts + i * kSumsqBlocks, only ? a.sumsq : nullptr);
+    const bool only = direct && launches <= 1 && blocks == 1;
+    grad_sumsq_kernel<<<blocks, kThreads, 0, stream>>>(tab, a.parts + parts, only ? direct : nullptr);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess || only) return err;
+    parts += blocks;
   }
-  grad_join_kernel<<<1, kJoinThreads, 0, stream>>>(a.parts, launches * kSumsqBlocks, a.sumsq);
+  return hipSuccess;
+}
+
+static hipError_t launch_join(const double* parts, int64_t n, double* sumsq, hipStream_t stream) {
+  grad_join_kernel<<<1, kJoinThreads, 0, stream>>>(parts, n, sumsq);
   return hipGetLastError();
 }
 
-hipError_t launch_grad_clip(const ClipArgs& a, hipStream_t stream) {
+static hipError_t launch_scale(const ClipArgs& a, int n_parts, hipStream_t stream) {
   const int64_t launches = clip_launches(a.n);
   for (int64_t i = (launches ? launches : 1) - 1; i >= 0; --i) {
     int64_t units;
     const Table tab = table_of(a, i * kTensors, units);
-    grad_clip_kernel<<<blocks_for(units), kThreads, 0, stream>>>(tab, a.sumsq, a.max_norm, i == 0 ? a.norm : nullptr);
+    // (sumsq is written by one launch, and by none that others read it in)
+    grad_clip_kernel<<<blocks_for(units), kThreads, 0, stream>>>(
+        tab, a.parts, n_parts, n_parts == 0 || i == 0 ? a.sumsq : nullptr, a.max_norm, i == 0 ? a.norm : nullptr);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
   }
   return hipSuccess;
+}
+
+hipError_t launch_grad_sumsq(const ClipArgs& a, hipStream_t stream) {
+  int64_t parts;
+  const hipError_t err = launch_squares(a, a.sumsq, parts, stream);
+  return err != hipSuccess || parts == 0 ? err : launch_join(a.parts, parts, a.sumsq, stream);
+}
+
+hipError_t launch_grad_clip(const ClipArgs& a, hipStream_t stream) { return launch_scale(a, 0, stream); }
+
+hipError_t launch_clip_grad_norm(const ClipArgs& a, hipStream_t stream) {
+  int64_t parts;
+  hipError_t err = launch_squares(a, nullptr, parts, stream);
+  if (err != hipSuccess) return err;
+  if (parts <= kJoinParts) return launch_scale(a, (int)parts, stream);
+  err = launch_join(a.parts, parts, a.sumsq, stream);
+  return err != hipSuccess ? err : launch_scale(a, 0, stream);
 }
 
 }  // namespace moe

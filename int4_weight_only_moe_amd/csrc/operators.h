@@ -183,10 +183,11 @@ struct ClipArgs {
   double* sumsq;
   float max_norm;            // clip only
   float* norm;               // clip only, or null
-  double* parts;             // sumsq only: [launches, kSumsqBlocks]
+  double* parts;             // sumsq only: up to kSumsqBlocks a launch
 };
 inline int64_t clip_launches(int64_t n) { return ceil_div(n, kClipTensorsPerLaunch); }
 hipError_t launch_grad_sumsq(const ClipArgs& a, hipStream_t stream);
 hipError_t launch_grad_clip(const ClipArgs& a, hipStream_t stream);
+hipError_t launch_clip_grad_norm(const ClipArgs& a, hipStream_t stream);
 
 }  // namespace moe

@@ -142,6 +142,19 @@ def test_grad_clip_validation():
         assert call(ptrs, outs, sizes) == ARG, (ptrs, outs)
 
 
+def test_clip_grad_norm_validation():
+    def call(ptrs=(P,), outs=(P,), sizes=(4,), most=1.0, sumsq=P, norm=P, ws=P, nbytes=1 << 30):
+        a, s, k = arrays(ptrs, sizes, [1] * len(ptrs))
+        return moe.lib().moe_clip_grad_norm(a, (ctypes.c_void_p * len(outs))(*outs), s, k, len(ptrs), most, sumsq, norm, ws,
+                                            nbytes, None)
+
+    for bad in (dict(most=-1.0), dict(most=float("nan")), dict(sumsq=None), dict(ws=None), dict(ws=P + 8), dict(norm=P + 2),
+                dict(outs=(P + 4,)), dict(outs=(None,)), dict(ptrs=(None,)), dict(sizes=(-1,)),
+                dict(ptrs=(P, P), outs=(P, P), sizes=(4, 4))):
+        assert call(**bad) == ARG, bad
+    assert call(nbytes=moe.moe_grad_norm_workspace_bytes(1) - 1) == WS
+
+
 @pytest.fixture(scope="module")
 def checker():
     import torch

@@ -36,6 +36,11 @@ def check(grads, ratio, in_place=False):
     assert abs(s.item() - want) <= (total / 2**19 + 2**13 + 40) * 2.0 ** -53 * want
     norm = moe.grad_clip(grads, s, most, out=None if in_place else out)
     root = s.item() ** 0.5
+    whole = [t.clone() for t in keep]  # both in one call: the same sum in another order
+    norm1 = moe.clip_grad_norm(whole, most)
+    assert abs(norm1.item() - root) <= 1.01 * U * root + 2.0 ** -149
+    assert all((a.double() - b.double()).abs().le((2.0 ** -7 if b.dtype == BF16 else 2.1 * U) * b.double().abs() + 2.0 ** -133).all()
+               for a, b in zip(whole, out))
     assert norm.dtype == F32 and abs(norm.item() - root) <= U * root + 2.0 ** -149
     factor = most / root if root > most else 1.0
     for a, b in zip(keep, out):
@@ -130,8 +135,9 @@ def test_clip_the_same_gradient_twice():
     out = [torch.empty_like(g), torch.empty_like(g)]
     moe.grad_clip([g, g], s, 0.1, out=out)
     assert torch.equal(out[0], out[1])
-    with pytest.raises(moe.MoeError):
-        moe.grad_clip([g, g], s, 0.1)
+    for call in (lambda: moe.grad_clip([g, g], s, 0.1), lambda: moe.clip_grad_norm([g, g], 0.1)):
+        with pytest.raises(moe.MoeError):
+            call()
 
 
 def test_clip_offsets_past_32_bits():
@@ -152,11 +158,13 @@ def test_clip_same_bits_streams_and_replays():
     out = [torch.empty_like(t) for t in grads]
     ws = torch.empty(moe.moe_grad_norm_workspace_bytes(len(sizes)), dtype=torch.uint8, device="cuda")
     s, norm = torch.empty(1, dtype=torch.float64, device="cuda"), torch.empty(1, device="cuda")
+    few, few_s, few_norm = [torch.empty_like(t) for t in grads[:60]], s.clone(), norm.clone()
 
     def call(stream=None):
         moe.grad_sumsq(grads, sumsq=s, workspace=ws, stream=stream)
         moe.grad_clip(grads, s, 0.5, out=out, norm=norm, stream=stream)
-        return [s, norm, *out]
+        moe.moe_clip_grad_norm(grads[:60], few, 0.4, few_s, ws, norm=few_norm, stream=stream)
+        return [s, norm, *out, *few, few_s, few_norm]
 
     first = [t.clone() for t in call()]
     side = torch.cuda.Stream()
@@ -170,11 +178,11 @@ def test_clip_same_bits_streams_and_replays():
     for rep in range(4):
         for a, b in zip(grads, keep):
             a.copy_(b * (1 + rep % 2))
-        for t in [s, norm, ws, *out]:
+        for t in [s, norm, ws, *out, *few, few_s, few_norm]:
             t.zero_()
         g.replay()
         torch.cuda.synchronize()
-        replayed = [t.clone() for t in (s, norm, *out)]
+        replayed = [t.clone() for t in (s, norm, *out, *few, few_s, few_norm)]
         assert all(torch.equal(a, b) for a, b in zip(replayed, call()))
         if rep % 2 == 0:
             assert all(torch.equal(a, b) for a, b in zip(replayed, first))
@@ -185,12 +193,14 @@ def test_clip_wrapper_refusals():
     s = moe.grad_sumsq(g)
     for bad in (lambda: moe.grad_sumsq([g[0].half()]), lambda: moe.grad_sumsq([g[0], g[1].cpu()]),
                 lambda: moe.grad_sumsq([torch.zeros((4, 4), device="cuda").t()]), lambda: moe.grad_sumsq([]),
-                lambda: moe.grad_clip(g, s.float(), 1.0), lambda: moe.grad_clip(g, s, 1.0, out=g[:1]),
+                lambda: moe.grad_clip(g, s.float(), 1.0), lambda: moe.clip_grad_norm([], 1.0),
+                lambda: moe.clip_grad_norm(g, 1.0, out=g[:1]), lambda: moe.grad_clip(g, s, 1.0, out=g[:1]),
                 lambda: moe.grad_clip(g, s, 1.0, out=[g[1], g[0]]),
                 lambda: moe.grad_clip(g, s, 1.0, out=[g[0], g[1].bfloat16()])):
         with pytest.raises(ValueError):
             bad()
-    for bad in (lambda: moe.grad_clip(g, s, -1.0), lambda: moe.grad_clip([g[0], g[0][:4]], s, 1.0)):
+    for bad in (lambda: moe.grad_clip(g, s, -1.0), lambda: moe.grad_clip([g[0], g[0][:4]], s, 1.0),
+                lambda: moe.clip_grad_norm(g, float("nan"))):
         with pytest.raises(moe.MoeError):
             bad()
     with pytest.raises(moe.MoeError) as e:
