@@ -215,8 +215,8 @@ __device__ __forceinline__ void align_body(AlignShared& sh, const int32_t* __res
 // ballot ranks among equal experts, running positions in LDS. The outputs
 // are identical to the one-workgroup kernel's.
 struct AlignGridShared {
-  int total[kMaxExperts];
-  int before[kMaxExperts];
+  int before[kMaxExperts];  // ids before the segment
+  int rest[kMaxExperts];    // and from it on
   int wave_tot[kAlignWaves];
   int wcnt[kAlignWaves][kMaxExperts];
 };
@@ -229,8 +229,8 @@ __global__ __launch_bounds__(kAlignThreads) void align_grid_kernel(
   const int s0 = blockIdx.x * seg;
   const int s1 = s0 + seg < MK ? s0 + seg : MK;
   if (tid < E) {
-    sh.total[tid] = 0;
     sh.before[tid] = 0;
+    sh.rest[tid] = 0;
 #pragma unroll
     for (int w = 0; w < kAlignWaves; ++w) sh.wcnt[w][tid] = 0;
   }
@@ -248,7 +248,7 @@ __global__ __launch_bounds__(kAlignThreads) void align_grid_kernel(
     const int f = f0 + 64 * r + lane;
     wv[r] = ids[f < MK ? f : MK - 1];
   }
-  // histograms of all ids and of the ids before the segment; the loads of a
+  // histograms of the ids before the segment and of the others; the loads of a
   // batch are unconditional (index clamped) so they go out together
   for (int fb = 0; fb < MK; fb += kAlignThreads * kHistIdsPerLane) {
     int ev[kHistIdsPerLane];
@@ -261,10 +261,7 @@ __global__ __launch_bounds__(kAlignThreads) void align_grid_kernel(
     for (int i = 0; i < kHistIdsPerLane; ++i) {
       const int f = fb + i * kAlignThreads + tid;
       const int e = ev[i];
-      if (f < MK && e >= 0 && e < E) {
-        atomicAdd(&sh.total[e], 1);
-        if (f < s0) atomicAdd(&sh.before[e], 1);
-      }
+      if (f < MK && e >= 0 && e < E) atomicAdd(f < s0 ? &sh.before[e] : &sh.rest[e], 1);
     }
   }
   // the wave's per-expert counts
@@ -284,7 +281,8 @@ __global__ __launch_bounds__(kAlignThreads) void align_grid_kernel(
 
   // exclusive scan of the padded totals (one expert per thread)
   int padded = 0;
-  if (tid < E) padded = (sh.total[tid] + block_m - 1) / block_m * block_m;
+  const int total = tid < E ? sh.before[tid] + sh.rest[tid] : 0;
+  if (tid < E) padded = (total + block_m - 1) / block_m * block_m;
   int incl = padded;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -300,7 +298,7 @@ __global__ __launch_bounds__(kAlignThreads) void align_grid_kernel(
   // offsets, the block -> expert map and the sentinel padding: expert e is
   // written by workgroup e % gridDim.x
   if (tid < E && tid % gridDim.x == blockIdx.x) {
-    const int o0 = excl, o1 = excl + padded, c = sh.total[tid];
+    const int o0 = excl, o1 = excl + padded, c = total;
     offsets[tid] = o0;
     for (int bb = o0 / block_m; bb < o1 / block_m; ++bb) block_expert[bb] = tid;
     for (int p = o0 + c; p < o1; ++p) sorted_ids[p] = MK;
