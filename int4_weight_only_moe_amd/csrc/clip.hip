@@ -201,7 +201,10 @@ __global__ __launch_bounds__(kThreads) void grad_clip_kernel(Table tab, const do
     if (n_parts > 0 && sumsq) *sumsq = total;
   }
   const bool over = root > (double)max_norm && root < INFINITY;
-  const float factor = over ? (float)((double)max_norm / root) : 1.0f;
+  // the factor in two steps where it is too small for a normal fp32 number
+  const double ratio = over ? (double)max_norm / root : 1.0;
+  const float step = ratio < 0x1p-100 ? 0x1p-64f : 1.0f;
+  const float factor = (float)(ratio / (double)step);
   if (!tab.n) return;
   walk<true>(
       tab, blockIdx.x, gridDim.x,
@@ -216,8 +219,8 @@ __global__ __launch_bounds__(kThreads) void grad_clip_kernel(Table tab, const do
           for (int j = 0; j < 2 * kPasses; ++j) {
             float v[4];
             four(unit.v[j], v);
-            put(q + j * kThreads, make_uint4(__float_as_uint(v[0] * factor), __float_as_uint(v[1] * factor),
-                                         __float_as_uint(v[2] * factor), __float_as_uint(v[3] * factor)));
+            put(q + j * kThreads, make_uint4(__float_as_uint(v[0] * step * factor), __float_as_uint(v[1] * step * factor),
+                                         __float_as_uint(v[2] * step * factor), __float_as_uint(v[3] * step * factor)));
           }
         } else {
           uint4* q = (uint4*)((uint16_t*)tab.out[i] + first) + threadIdx.x;
@@ -228,7 +231,7 @@ __global__ __launch_bounds__(kThreads) void grad_clip_kernel(Table tab, const do
             uint32_t u[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              u[k] = (uint32_t)to_bf16(v[2 * k] * factor) | ((uint32_t)to_bf16(v[2 * k + 1] * factor) << 16);
+              u[k] = (uint32_t)to_bf16(v[2 * k] * step * factor) | ((uint32_t)to_bf16(v[2 * k + 1] * step * factor) << 16);
             put(q + j * kThreads, make_uint4(u[0], u[1], u[2], u[3]));
           }
         }
@@ -236,7 +239,7 @@ __global__ __launch_bounds__(kThreads) void grad_clip_kernel(Table tab, const do
       [&](int i, int64_t first, int64_t stop) {
         if (!over && tab.grad[i] == tab.out[i]) return;
         for (int64_t e = first + threadIdx.x; e < stop; e += kThreads)
-          store_one(tab.out[i], tab.f32[i], e, load_one(tab.grad[i], tab.f32[i], e) * factor);
+          store_one(tab.out[i], tab.f32[i], e, load_one(tab.grad[i], tab.f32[i], e) * step * factor);
       });
 }
 

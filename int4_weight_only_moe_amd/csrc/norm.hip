@@ -539,7 +539,7 @@ __global__ __launch_bounds__(64 * kJoinRows) void norm_join_kernel(const float* 
   const int c = blockIdx.x * 64 + lane;
   const float* p = parts + (c < N ? c : N - 1);
   double s = 0.0;
-  constexpr int kAhead = 8;
+  constexpr int kAhead = 16;  // (a sum of 256 workgroups in one turn of loads)
   for (int i = wave; i < teams; i += kJoinRows * kAhead) {
     float v[kAhead];
 #pragma unroll
@@ -579,7 +579,10 @@ bool chunks_ok(const void* p, int64_t ld, int size) {
 
 }  // namespace
 
-hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
+// Rows of a launch: a grid has fewer than 2^32 threads.
+constexpr int kSlabRows = 1 << 21;
+
+static hipError_t launch_norm_slab(const NormArgs& a, hipStream_t stream) {
   const int size = a.f32 ? 4 : 2;
   const bool vec = a.N % 8 == 0 && chunks_ok(a.x, a.ldx, 2) && chunks_ok(a.res, a.ld_res, size) &&
                    chunks_ok(a.res_out, a.ld_res_out, size) && chunks_ok(a.w, 8, 2) && chunks_ok(a.out, a.ld_out, 2) &&
@@ -599,6 +602,26 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
     vec ? quanted(std::true_type{}) : quanted(std::false_type{});
   });
   return hipGetLastError();
+}
+
+hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
+  const int64_t size = a.f32 ? 4 : 2;
+  for (int64_t first = 0; first < a.M; first += kSlabRows) {
+    NormArgs slab = a;
+    slab.M = (int)(a.M - first < kSlabRows ? a.M - first : kSlabRows);
+    if (a.x) slab.x += first * a.ldx;
+    if (a.res) slab.res = (const uint8_t*)a.res + first * a.ld_res * size;
+    if (a.res_out) slab.res_out = (uint8_t*)a.res_out + first * a.ld_res_out * size;
+    if (a.out) slab.out += first * a.ld_out;
+    if (a.out8) {
+      slab.out8 += first * a.ld_out8;
+      slab.scales += first * (a.N / a.group);
+    }
+    if (a.rstd) slab.rstd += first;
+    const hipError_t err = launch_norm_slab(slab, stream);
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
 }
 
 // Workgroups of a backward pass. A CU's one workgroup of wide rows keeps a row

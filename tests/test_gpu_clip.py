@@ -92,6 +92,17 @@ def test_clip_magnitudes():
     """Squares beyond fp32's range, subnormal gradients, a norm of zero."""
     for scale in (1e30, 1e-30, 1e-40):
         check(make((5000, 300), (F32, BF16), 7, scale=scale), 0.5)
+    # a factor below the smallest normal fp32 number: results of ordinary size keep their bits
+    big = make((5000, 300), (F32, BF16), 7, scale=1e30)
+    keep = [t.double() for t in big]
+    root = sum(float(t.square().sum()) for t in keep) ** 0.5
+    for most in (1e-10, 1e-13):
+        out = [torch.empty_like(t) for t in big]
+        moe.clip_grad_norm(big, most, out=out)
+        for a, b in zip(keep, out):
+            exact = a * (float(np.float32(most)) / root)
+            half = HALF_BF16 if b.dtype == BF16 else U
+            assert (b.double() - exact).abs().le((half + 2.1 * U) * exact.abs() + 2.0 ** -133 * (b.dtype == BF16) + 2.0 ** -148).all()
     zero = [torch.zeros(100, device="cuda")]
     assert moe.clip_grad_norm(zero, 0.0).item() == 0 and not zero[0].any()
     g = make((100,), (F32,), 8)

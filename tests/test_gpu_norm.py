@@ -302,6 +302,24 @@ def test_norm_same_bits_streams_and_replays():
             assert all(torch.equal(a, b) for a, b in zip(replayed, first))
 
 
+def test_norm_more_rows_than_a_launch():
+    """2^21 rows a launch; every output of the rows behind."""
+    M, N = 2**21 + 70, 64
+    x = torch.ones((M, N + 8), dtype=BF16, device="cuda")[:, :N]
+    res = torch.zeros((M, N), device="cuda")
+    g = torch.Generator().manual_seed(4)
+    tail = slice(2**21 - 10, M)
+    x[tail] = torch.randn(80, N, generator=g).to(BF16).cuda()
+    res[tail] = torch.randn(80, N, generator=g).cuda()
+    w = (1 + 0.3 * torch.randn(N, generator=g)).to(BF16).cuda()
+    bufs = moe.add_rms_norm(x, w, moe.alloc_norm_buffers(M, N, F32, rstd=True, quant_group=32), residual=res)
+    small = moe.add_rms_norm(x[tail], w, moe.alloc_norm_buffers(80, N, F32, rstd=True, quant_group=32), residual=res[tail])
+    for name in ("residual_out", "out", "rstd", "scales"):
+        assert torch.equal(getattr(bufs, name)[tail], getattr(small, name)), name
+    assert torch.equal(bufs.out8[tail].view(torch.uint8), small.out8.view(torch.uint8))
+    assert (bufs.residual_out[:2**21 - 10] == 1).all() and (bufs.rstd[:2**21 - 10] == bufs.rstd[0]).all()
+
+
 def test_norm_workspace_of_a_larger_batch_and_offsets_past_32_bits():
     N = 1024
     M = 2**21 + 2**20 + 5  # M * N > 2^31 elements

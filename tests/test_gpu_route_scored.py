@@ -89,7 +89,8 @@ def normal(M, E, seed):
     (5, 100, 7, (50, 20, 2)), (64, 128, 8, (64, 8, 1)), (40, 160, 6, (8, 3, 1)), (130, 256, 8, (8, 4, 2)),
     (9, 257, 16, (257 // 257, 1, 1)), (48, 384, 8, (16, 1, 2)), (31, 512, 8, (2, 1, 2)), (20, 513, 5, (27, 9, 2)),
     (50, 1024, 16, (32, 32, 1)), (37, 1023, 11, (33, 2, 2)), (16, 1000, 16, (4, 4, 2)), (300, 7, 7, (1, 1, 1)),
-    (12, 512, 16, (64, 2, 2)), (21, 62, 9, (2, 2, 2)),
+    (12, 512, 16, (64, 2, 2)), (21, 62, 9, (2, 2, 2)), (19, 512, 8, (32, 4, 2)), (33, 1024, 8, (64, 5, 2)), (70, 384, 8, (24, 4, 2)),
+    (15, 96, 6, (3, 2, 2)),
 ])
 def test_route_scored_shapes(M, E, k, groups):
     logits = normal(M, E, M + E)
@@ -168,6 +169,44 @@ def test_route_scored_masked_experts(scoring, biased, groups):
                 x = normal(4, E, 9)
                 x[1, 17], x[2, 95], x[2, 4] = np.nan, np.nan, np.nan
                 check(x, k, scoring, bias, groups, renormalise)
+
+
+def test_route_scored_nan_bias_and_infinite_logits():
+    """A NaN bias or logit counts as the highest c; +inf saturates a sigmoid and makes a softmax NaN."""
+    M, E, k = 12, 80, 4
+    logits = normal(M, E, 60)
+    bias = (0.1 * normal(1, E, 61))[0]
+    bias[[70, 3]] = np.nan
+    logits[3, 50], logits[4, [9, 11]] = np.inf, np.inf
+    logits[5, 20] = -np.inf
+    with np.errstate(invalid="ignore", over="ignore"):
+        for groups in ((1, 1, 1), (8, 2, 2)):
+            want, w = oracle.route_scored(logits, k, "sigmoid", bias, *groups, True)
+            rb = moe.alloc_route_buffers(M, E, k, 16)
+            moe.route_scored(dev(logits), rb, "sigmoid", dev(bias), *groups)
+            np.testing.assert_array_equal(rb.topk_ids.cpu().numpy(), want)
+            np.testing.assert_allclose(rb.topk_weights.cpu().numpy(), w, rtol=14 * U)
+        check(logits, k, "sigmoid", None, (8, 2, 2))
+        rb = moe.route_scored(dev(logits), moe.alloc_route_buffers(M, E, k, 16), renormalise=False)
+        got = rb.topk_weights.cpu().numpy()
+        assert np.isnan(got[[3, 4]]).all() and np.isfinite(got[[0, 1, 2, 5]]).all()
+        assert rb.topk_ids[3, 0] == 50 and rb.topk_ids[4, :2].tolist() == [9, 11]
+
+
+def test_route_scored_more_rows_than_a_grid():
+    """More rows than one launch's workgroups take (2^23 of 16 rows)."""
+    M, E = 2**27 + 21, 2
+    logits = torch.zeros((M, E), device="cuda")
+    logits[::3, 1] = 1.0
+    rb = moe.alloc_route_buffers(M, E, 1, 16)
+    moe.route_scored(logits, rb, "sigmoid", renormalise=False, grouping=False)
+    want = torch.zeros(M, dtype=torch.int32, device="cuda")
+    want[::3] = 1
+    assert torch.equal(rb.topk_ids[:, 0], want)
+    assert (rb.topk_weights[:, 0] - torch.where(want == 1, 1 / (1 + np.exp(-1.0)), 0.5)).abs().max() <= 4 * U
+    grad = moe.route_scored_backward(logits, rb.topk_ids, torch.ones((M, 1), device="cuda"), "sigmoid", False)
+    other = grad.gather(1, 1 - want[:, None].long())
+    assert not other.any() and (grad[:, 0][1::3] - 0.25).abs().max() <= 4 * U
 
 
 def test_route_scored_large_values():
