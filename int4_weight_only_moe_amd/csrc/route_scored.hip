@@ -2,7 +2,7 @@
 //
 // s = softmax(l) or sigmoid(l) of a token's logits, c = s + bias; the groups of
 // the highest scores, the k experts of the highest c in them, weights from s.
-// A row of logits lies in the registers of 16 lanes (32 from 513 experts on).
+// A row of logits lies in the registers of 16 or 32 lanes.
 //
 // Finding the k highest without k passes over the row: the k-th highest of the
 // lanes' own maxima (k exchanges within the row) is a threshold that at least k
@@ -611,17 +611,27 @@ __global__ __launch_bounds__(kThreads) void route_scored_small_kernel(ScoredArgs
 }
 static_assert(kSmallMaxAssign <= kThreads, "one id a thread");
 
-// fn(Lanes, NV, Vec) for the row width
+// fn(Lanes, NV, Vec) for the row width. Few rows (kFewRows: below that 16 lanes a
+// row are less than two waves a SIMD) take 32 lanes from 65 experts on: the work of
+// a row is then done sooner ([64, 384] 4.5 us instead of 5.4, [4096, 256] in groups
+// 12.3 instead of 13.0), while a full device takes longer ([16384, 384] 10.3 instead
+// of 8.6).
+constexpr int kFewRows = 8192;
 template <typename F>
-void by_width(int E, bool vec, F fn) {
+void by_width(int E, bool vec, bool few, F fn) {
   auto go = [&](auto lanes, auto nv) { vec ? fn(lanes, nv, std::true_type{}) : fn(lanes, nv, std::false_type{}); };
   auto row16 = [&](auto nv) { go(std::integral_constant<int, 16>{}, nv); };
+  auto row32 = [&](auto nv) { go(std::integral_constant<int, 32>{}, nv); };
   if (E <= 64) row16(std::integral_constant<int, 1>{});
+  else if (E > 512) row32(std::integral_constant<int, 8>{});
+  else if (few && E <= 128) row32(std::integral_constant<int, 1>{});
+  else if (few && E <= 256) row32(std::integral_constant<int, 2>{});
+  else if (few && E <= 384) row32(std::integral_constant<int, 3>{});
+  else if (few) row32(std::integral_constant<int, 4>{});
   else if (E <= 128) row16(std::integral_constant<int, 2>{});
   else if (E <= 256) row16(std::integral_constant<int, 4>{});
   else if (E <= 384) row16(std::integral_constant<int, 6>{});
-  else if (E <= 512) row16(std::integral_constant<int, 8>{});
-  else go(std::integral_constant<int, 32>{}, std::integral_constant<int, 8>{});
+  else row16(std::integral_constant<int, 8>{});
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -726,16 +736,19 @@ hipError_t launch_route_scored(const ScoredArgs& a, hipStream_t stream) {
   const bool grouping = a.sorted_ids != nullptr;
   const bool small = grouping && a.M <= kSmallMaxTokens;
   const bool general = a.bias || a.top_groups < a.groups;
-  by_width(a.E, a.E % 4 == 0 && aligned16(a.logits) && (!a.bias || aligned16(a.bias)), [&](auto lanes, auto nv, auto vec) {
+  const bool vec = a.E % 4 == 0 && aligned16(a.logits) && (!a.bias || aligned16(a.bias));
+  by_width(a.E, vec, a.M < kFewRows, [&](auto lanes, auto nv, auto v) {
     constexpr int L = decltype(lanes)::value, NV = decltype(nv)::value;
-    constexpr bool V = decltype(vec)::value;
+    constexpr bool V = decltype(v)::value;
     unsigned lds = (unsigned)row_buffer_bytes(L, a.bias != nullptr, a.top_groups < a.groups, a.E, a.groups) * kWaves;
     if (small && lds < sizeof(SmallRoute)) lds = sizeof(SmallRoute);
     constexpr int kRows = kThreads / L;
-    if (small) {
-      general ? route_scored_small_kernel<L, NV, V, true><<<1, kThreads, lds, stream>>>(a)
-              : route_scored_small_kernel<L, NV, V, false><<<1, kThreads, lds, stream>>>(a);
-      return;
+    if constexpr (L == 32 || NV == 1) {  // (up to 16 rows are few)
+      if (small) {
+        general ? route_scored_small_kernel<L, NV, V, true><<<1, kThreads, lds, stream>>>(a)
+                : route_scored_small_kernel<L, NV, V, false><<<1, kThreads, lds, stream>>>(a);
+        return;
+      }
     }
     for (int64_t first = 0; first < a.M; first += (int64_t)kMaxGrid * kRows) {
       const unsigned grid = grid_for(a.M - first, kRows);
@@ -751,7 +764,7 @@ hipError_t launch_route_scored(const ScoredArgs& a, hipStream_t stream) {
 hipError_t launch_route_scored_backward(const ScoredBackwardArgs& a, hipStream_t stream) {
   const bool full = !a.sigmoid && !a.renorm;
   const bool vec = a.E % 4 == 0 && aligned16(a.logits) && aligned16(a.grad) && (!a.base || aligned16(a.base));
-  by_width(a.E, vec, [&](auto lanes, auto nv, auto v) {
+  by_width(a.E, vec, false, [&](auto lanes, auto nv, auto v) {
     constexpr int L = decltype(lanes)::value, NV = decltype(nv)::value;
     constexpr bool V = decltype(v)::value;
     const unsigned lds = (unsigned)(((a.E + 3) & ~3) * 4 * (kThreads / L));

@@ -104,6 +104,35 @@ def test_route_scored_shapes(M, E, k, groups):
         check(lg, k, scoring, bias, groups, renormalise, 1.0 + i % 3, valid, (16, 32, 64, 128)[i % 4], grouping=i != 5)
 
 
+@pytest.mark.parametrize("E,k,groups", [(65, 5, (5, 2, 2)), (100, 7, (50, 20, 2)), (128, 16, (8, 4, 2)), (160, 6, (8, 3, 1)),
+                                        (256, 8, (8, 4, 2)), (257, 16, (1, 1, 1)), (384, 8, (16, 3, 2)), (384, 8, (24, 4, 2)),
+                                        (500, 9, (4, 2, 2)), (512, 16, (64, 9, 2)), (512, 8, (32, 4, 2)), (1000, 8, (8, 4, 2))])
+def test_route_scored_many_rows(E, k, groups):
+    """From 8192 rows on a row has 16 lanes: 96 rows (ties, absent experts and padding among them), each
+    86 times over, in another order of rows for each."""
+    logits = normal(96, E, E + k)
+    rng = np.random.default_rng(E)
+    logits[3] = 0.0
+    logits[4] = np.round(logits[4] * 4) / 4
+    logits[5, rng.permutation(E)[3:]] = -np.inf
+    logits[6] = -np.inf
+    logits[7] = torch.from_numpy(logits[7]).to(torch.bfloat16).float().numpy()
+    logits[8] = logits[8, 0] + np.arange(E, dtype=np.float32) * np.float32(2.0 ** -22)
+    valid = rng.random(96) > 0.1
+    logits[~valid] = np.nan
+    order = np.concatenate([rng.permutation(96) for _ in range(86)])
+    bias = (0.05 * rng.standard_normal(E)).astype(np.float32)
+    for scoring, b, renormalise in itertools.product(("softmax", "sigmoid"), (None, bias), (False, True)):
+        ids, w = oracle.route_scored(logits, k, scoring, b, *groups, renormalise, 1.5, valid)
+        rb = moe.alloc_route_buffers(len(order), E, k, 32)
+        moe.route_scored(dev(logits[order]), rb, scoring, dev(b), *groups, renormalise=renormalise, scale=1.5,
+                         row_valid=dev(valid[order]))
+        np.testing.assert_array_equal(rb.topk_ids.cpu().numpy(), ids[order])
+        n = weight_roundings(logits, scoring, renormalise)
+        np.testing.assert_allclose(rb.topk_weights.cpu().numpy(), w[order], rtol=n * U, atol=2.0 ** -126)
+    check_grouping(rb, ids[order], E)
+
+
 @pytest.mark.parametrize("scoring", ("softmax", "sigmoid"))
 @pytest.mark.parametrize("groups", ((1, 1, 1), (8, 3, 2)))
 def test_route_scored_ties_and_neighbours(scoring, groups):
