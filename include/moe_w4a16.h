@@ -584,7 +584,7 @@ int moe_add_rms_norm_backward(const uint16_t* grad_out_bf16, int64_t ld_grad_out
  *               may overlap neither another out nor another entry's gradient
  *               (MOE_ERR_INVALID_ARG). A gradient in place that is not scaled is
  *               not written.
- *   sumsq       fp64 [1]. norm fp32 [1], or NULL.
+ *   sumsq       fp64 [1] (moe_clip_grad_norm: or NULL). norm fp32 [1], or NULL.
  *   max_norm    >= 0, infinity included.
  *   workspace   >= moe_grad_norm_workspace_bytes(n) bytes, 16-byte aligned;
  *               contents on entry do not matter. One for a larger n serves

@@ -396,9 +396,8 @@ def clip_grad_norm(grads, max_norm: float, out=None, workspace: torch.Tensor | N
         raise ValueError("no gradients")
     device = grads[0].device
     workspace = _grads_workspace(grads, device, workspace, stream)
-    with _memory_of(stream, device):
-        sumsq = torch.empty(1, dtype=torch.float64, device=device)
-        if norm is None:
+    if norm is None:
+        with _memory_of(stream, device):
             norm = torch.empty(1, dtype=torch.float32, device=device)
-    moe_clip_grad_norm(grads, grads if out is None else out, max_norm, sumsq, workspace, norm=norm, stream=stream)
+    moe_clip_grad_norm(grads, grads if out is None else out, max_norm, workspace, norm=norm, stream=stream)
     return norm

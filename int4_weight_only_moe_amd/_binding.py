@@ -659,10 +659,10 @@ def moe_grad_clip(grads, outs, sumsq: torch.Tensor, max_norm: float, norm: torch
                _shaped(norm, torch.float32, (1,), "norm", dev))
 
 
-def moe_clip_grad_norm(grads, outs, max_norm: float, sumsq: torch.Tensor, workspace: torch.Tensor,
+def moe_clip_grad_norm(grads, outs, max_norm: float, workspace: torch.Tensor, sumsq: torch.Tensor | None = None,
                        norm: torch.Tensor | None = None, stream=None) -> None:
     """moe_grad_sumsq and moe_grad_clip in one call."""
-    dev = sumsq.device
+    dev = workspace.device
     _on_device(dev, "moe_clip_grad_norm", stream, *_clip_arrays(grads, outs, dev), len(grads), max_norm,
                _shaped(sumsq, torch.float64, (1,), "sumsq", dev), _shaped(norm, torch.float32, (1,), "norm", dev),
                *_buffer(workspace, "workspace", dev))

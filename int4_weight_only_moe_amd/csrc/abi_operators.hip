@@ -106,8 +106,7 @@ bool outs_apart(const void* const* grads, void* const* outs, const int64_t* size
 
 int check_outs(const void* const* grads, void* const* outs, const int64_t* sizes, const int32_t* dtypes, int32_t n,
                const double* sumsq, float max_norm, const float* norm) {
-  if (!(max_norm >= 0.0f) || !sumsq || !aligned(sumsq, 8) || !aligned(norm, 4) || (n > 0 && !outs))
-    return MOE_ERR_INVALID_ARG;
+  if (!(max_norm >= 0.0f) || !aligned(sumsq, 8) || !aligned(norm, 4) || (n > 0 && !outs)) return MOE_ERR_INVALID_ARG;
   for (int32_t i = 0; i < n; ++i)
     if ((sizes[i] > 0 && !outs[i]) || !aligned(outs[i], dtypes[i] == MOE_DTYPE_F32 ? 4 : 2)) return MOE_ERR_INVALID_ARG;
   return outs_apart(grads, outs, sizes, dtypes, n) ? MOE_OK : MOE_ERR_INVALID_ARG;
@@ -347,7 +346,7 @@ int moe_add_rms_norm_backward(const uint16_t* grad_out_bf16, int64_t ld_grad_out
 
 int64_t moe_grad_norm_workspace_bytes(int32_t n) {
   if (n < 0 || n > moe::kClipMaxTensors) return -1;
-  return (n ? moe::clip_launches(n) : 1) * moe::kSumsqBlocks * 8;
+  return (moe::clip_parts(n) + 2) * 8;
 }
 
 int moe_grad_sumsq(const void* const* grads, const int64_t* sizes, const int32_t* dtypes, int32_t n, double* sumsq,
@@ -365,6 +364,7 @@ int moe_grad_clip(const void* const* grads, void* const* outs, const int64_t* si
                   const double* sumsq, float max_norm, float* norm, void* stream) {
   int st = check_grads(grads, sizes, dtypes, n);
   if (st != MOE_OK) return st;
+  if (!sumsq) return MOE_ERR_INVALID_ARG;
   st = check_outs(grads, outs, sizes, dtypes, n, sumsq, max_norm, norm);
   if (st != MOE_OK) return st;
   moe::ClipArgs a{};

@@ -20,12 +20,16 @@ constexpr int kPasses = 2;  // of 8 elements a thread
 constexpr int kUnit = 8 * kThreads * kPasses;
 constexpr int kTensors = kClipTensorsPerLaunch;
 
+// The tensors of a launch, in its arguments. Few tensors have a small table: the
+// host writes all of it for each launch.
+constexpr int kFewTensors = 12;
+template <int kN>
 struct Table {
-  const void* grad[kTensors];
-  void* out[kTensors];
-  int64_t size[kTensors];
-  int64_t end[kTensors];  // units up to and including this tensor's
-  uint8_t f32[kTensors];
+  const void* grad[kN];
+  void* out[kN];
+  int64_t size[kN];
+  int64_t end[kN];  // units up to and including this tensor's
+  uint8_t f32[kN];
   int n;
 };
 
@@ -38,7 +42,8 @@ __device__ __forceinline__ double wave_sum64(double v) {
 __device__ __forceinline__ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // The first tensor that holds unit u or a later one.
-__device__ __forceinline__ int tensor_of(const Table& tab, int64_t u) {
+template <int kN>
+__device__ __forceinline__ int tensor_of(const Table<kN>& tab, int64_t u) {
   int lo = 0, hi = tab.n;
   while (lo < hi) {
     const int mid = (lo + hi) / 2;
@@ -91,8 +96,8 @@ __device__ __forceinline__ void store_one(void* p, bool f32, int64_t i, float v)
 // Workgroup b's units, with `blocks` of them, one after another: whole(i, first)
 // for a unit of tensor i from element `first` on, part(i, first, last) for
 // elements that are to be taken one by one. Back: from the last unit to the first.
-template <bool kBack, typename Whole, typename Part>
-__device__ __forceinline__ void walk(const Table& tab, int64_t b, int64_t blocks, Whole whole, Part part) {
+template <bool kBack, int kN, typename Whole, typename Part>
+__device__ __forceinline__ void walk(const Table<kN>& tab, int64_t b, int64_t blocks, Whole whole, Part part) {
   const int64_t units = tab.end[tab.n - 1];
   int i = kBack ? tab.n - 1 : 0;
   for (int64_t k = b; k < units; k += blocks) {
@@ -117,7 +122,8 @@ __device__ __forceinline__ double block_sum(double s, double (&room)[kWaves]) {
   return s;
 }
 
-__global__ __launch_bounds__(kThreads) void grad_sumsq_kernel(Table tab, double* parts, double* direct) {
+template <int kN>
+__global__ __launch_bounds__(kThreads) void grad_sumsq_kernel(Table<kN> tab, double* parts, double* direct) {
   __shared__ double room[kThreads / 64];
   double s = 0.0;
   if (tab.n) {
@@ -183,7 +189,8 @@ __device__ __forceinline__ void put(uint4* p, uint4 v) {
 // n_parts > 0: sumsq is still in that many parts, which every workgroup adds
 // itself, in the same order: one launch less, and up to kJoinParts of them cost less
 // than that.
-__global__ __launch_bounds__(kThreads) void grad_clip_kernel(Table tab, const double* parts, int n_parts,
+template <int kN>
+__global__ __launch_bounds__(kThreads) void grad_clip_kernel(Table<kN> tab, const double* parts, int n_parts,
                                                              double* sumsq, float max_norm, float* norm) {
   __shared__ double room[kThreads / 64];
   double total;
@@ -243,11 +250,13 @@ __global__ __launch_bounds__(kThreads) void grad_clip_kernel(Table tab, const do
       });
 }
 
-// The tensors [from, from + kTensors) of the call.
-Table table_of(const ClipArgs& a, int64_t from, int64_t& units) {
-  Table tab{};
-  units = 0;
-  for (int64_t i = from; i < a.n && i < from + kTensors; ++i) {
+// fn(table, units) of the tensors [from, from + kTensors) of the call.
+template <int kN, typename F>
+void with_table_of(const ClipArgs& a, int64_t from, F fn) {
+  Table<kN> tab;
+  tab.n = 0;
+  int64_t units = 0;
+  for (int64_t i = from; i < a.n && i < from + kN; ++i) {
     const int k = tab.n++;
     tab.grad[k] = a.grads[i];
     tab.out[k] = a.outs ? a.outs[i] : const_cast<void*>(a.grads[i]);
@@ -256,7 +265,12 @@ Table table_of(const ClipArgs& a, int64_t from, int64_t& units) {
     units += ceil_div(a.sizes[i], kUnit);
     tab.end[k] = units;
   }
-  return tab;
+  fn(tab, units);
+}
+template <typename F>
+void with_table(const ClipArgs& a, int64_t from, F fn) {
+  if (a.n - from <= kFewTensors) with_table_of<kFewTensors>(a, from, fn);
+  else with_table_of<kTensors>(a, from, fn);
 }
 
 constexpr int64_t kJoinParts = 2 * kSumsqBlocks;
@@ -272,14 +286,15 @@ static hipError_t launch_squares(const ClipArgs& a, double* direct, int64_t& par
   const int64_t launches = clip_launches(a.n);
   parts = 0;
   for (int64_t i = 0; i < (launches ? launches : 1); ++i) {
-    int64_t units;
-    const Table tab = table_of(a, i * kTensors, units);
-    const unsigned blocks = blocks_for(units);
-    const bool only = direct && launches <= 1 && blocks == 1;
-    grad_sumsq_kernel<<<blocks, kThreads, 0, stream>>>(tab, a.parts + parts, only ? direct : nullptr);
+    bool only = false;
+    with_table(a, i * kTensors, [&](const auto& tab, int64_t units) {
+      const unsigned blocks = blocks_for(units);
+      only = direct && launches <= 1 && blocks == 1;
+      grad_sumsq_kernel<<<blocks, kThreads, 0, stream>>>(tab, a.parts + parts, only ? direct : nullptr);
+      parts += only ? 0 : blocks;
+    });
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess || only) return err;
-    parts += blocks;
   }
   return hipSuccess;
 }
@@ -292,11 +307,11 @@ static hipError_t launch_join(const double* parts, int64_t n, double* sumsq, hip
 static hipError_t launch_scale(const ClipArgs& a, int n_parts, hipStream_t stream) {
   const int64_t launches = clip_launches(a.n);
   for (int64_t i = (launches ? launches : 1) - 1; i >= 0; --i) {
-    int64_t units;
-    const Table tab = table_of(a, i * kTensors, units);
-    // (sumsq is written by one launch, and by none that others read it in)
-    grad_clip_kernel<<<blocks_for(units), kThreads, 0, stream>>>(
-        tab, a.parts, n_parts, n_parts == 0 || i == 0 ? a.sumsq : nullptr, a.max_norm, i == 0 ? a.norm : nullptr);
+    with_table(a, i * kTensors, [&](const auto& tab, int64_t units) {
+      // (with parts, sumsq is written by one launch and read by none)
+      grad_clip_kernel<<<blocks_for(units), kThreads, 0, stream>>>(
+          tab, a.parts, n_parts, n_parts == 0 || i == 0 ? a.sumsq : nullptr, a.max_norm, i == 0 ? a.norm : nullptr);
+    });
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
   }
@@ -316,8 +331,10 @@ hipError_t launch_clip_grad_norm(const ClipArgs& a, hipStream_t stream) {
   hipError_t err = launch_squares(a, nullptr, parts, stream);
   if (err != hipSuccess) return err;
   if (parts <= kJoinParts) return launch_scale(a, (int)parts, stream);
-  err = launch_join(a.parts, parts, a.sumsq, stream);
-  return err != hipSuccess ? err : launch_scale(a, 0, stream);
+  ClipArgs joined = a;
+  if (!joined.sumsq) joined.sumsq = a.parts + clip_parts(a.n);
+  err = launch_join(a.parts, parts, joined.sumsq, stream);
+  return err != hipSuccess ? err : launch_scale(joined, 0, stream);
 }
 
 }  // namespace moe

@@ -183,9 +183,10 @@ struct ClipArgs {
   double* sumsq;
   float max_norm;            // clip only
   float* norm;               // clip only, or null
-  double* parts;             // sumsq only: up to kSumsqBlocks a launch
+  double* parts;             // up to kSumsqBlocks a launch, and a sum of them
 };
 inline int64_t clip_launches(int64_t n) { return ceil_div(n, kClipTensorsPerLaunch); }
+inline int64_t clip_parts(int64_t n) { return (n ? clip_launches(n) : 1) * kSumsqBlocks; }
 hipError_t launch_grad_sumsq(const ClipArgs& a, hipStream_t stream);
 hipError_t launch_grad_clip(const ClipArgs& a, hipStream_t stream);
 hipError_t launch_clip_grad_norm(const ClipArgs& a, hipStream_t stream);

@@ -655,10 +655,15 @@ __global__ __launch_bounds__(kThreads) void route_scored_backward_kernel(ScoredB
   const float* row = a.logits + (active ? t : (int64_t)a.M - 1) * E;
   float v[N];
   if constexpr (Full) load_row<Lanes, NV, Vec>(row, E, l, v);
-  const int e = active && l < k ? a.ids[t * k + l] : -1;
+  // (unconditional loads go out together)
+  const int64_t slot = (active ? t : (int64_t)a.M - 1) * k + (l < k ? l : 0);
+  const int e0 = a.ids[slot];
+  const float g0 = a.dweights[slot];
+  const int e = active && l < k ? e0 : -1;
   const bool has = (unsigned)e < (unsigned)E;
-  const float g = has ? a.scale * a.dweights[t * k + l] : 0.0f;
-  const float lg = has ? row[e] : -INFINITY;
+  const float g = has ? a.scale * g0 : 0.0f;
+  const float l0 = row[has ? e : 0];
+  const float lg = has ? l0 : -INFINITY;
   const bool any = row_any<Lanes>(has);
   RowSoftmax soft{0.0f, 0.0f, 0.0f};
   float d;  // what goes to the slot's expert

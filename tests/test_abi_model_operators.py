@@ -148,7 +148,7 @@ def test_clip_grad_norm_validation():
         return moe.lib().moe_clip_grad_norm(a, (ctypes.c_void_p * len(outs))(*outs), s, k, len(ptrs), most, sumsq, norm, ws,
                                             nbytes, None)
 
-    for bad in (dict(most=-1.0), dict(most=float("nan")), dict(sumsq=None), dict(ws=None), dict(ws=P + 8), dict(norm=P + 2),
+    for bad in (dict(most=-1.0), dict(most=float("nan")), dict(sumsq=P + 4), dict(ws=None), dict(ws=P + 8), dict(norm=P + 2),
                 dict(outs=(P + 4,)), dict(outs=(None,)), dict(ptrs=(None,)), dict(sizes=(-1,)),
                 dict(ptrs=(P, P), outs=(P, P), sizes=(4, 4))):
         assert call(**bad) == ARG, bad

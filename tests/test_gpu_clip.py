@@ -57,7 +57,7 @@ def check(grads, ratio, in_place=False):
 
 @pytest.mark.parametrize("sizes", [(1,), (0,), (0, 3, 0), (8,), (2047,), (2048,), (2049,), (5000, 1, 2048, 0, 4096, 77),
                                    (100_000,), (2_000_003, 17), tuple([33] * 95), tuple([4097, 5] * 48), tuple([64] * 97),
-                                   tuple([3000] * 300), (2048 * 2048, 2048 * 2048 + 1)])
+                                   tuple([3000] * 300), tuple([100_001] * 300), (2048 * 2048, 2048 * 2048 + 1)])
 def test_clip_sizes(sizes):
     mixed = [(F32, BF16)[i % 2] for i in range(len(sizes))]
     for kinds in ([F32] * len(sizes), [BF16] * len(sizes), mixed):
@@ -174,7 +174,7 @@ def test_clip_same_bits_streams_and_replays():
     def call(stream=None):
         moe.grad_sumsq(grads, sumsq=s, workspace=ws, stream=stream)
         moe.grad_clip(grads, s, 0.5, out=out, norm=norm, stream=stream)
-        moe.moe_clip_grad_norm(grads[:60], few, 0.4, few_s, ws, norm=few_norm, stream=stream)
+        moe.moe_clip_grad_norm(grads[:60], few, 0.4, ws, sumsq=few_s, norm=few_norm, stream=stream)
         return [s, norm, *out, *few, few_s, few_norm]
 
     first = [t.clone() for t in call()]
