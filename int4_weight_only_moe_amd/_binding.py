@@ -10,7 +10,9 @@ raised.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
+from array import array
 
 import torch
 
@@ -28,6 +30,8 @@ MOE_ERR_SCRATCH = -6
 MOE_DTYPE_BF16 = 0
 MOE_DTYPE_F32 = 1
 _SIDE_DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32}
+_DTYPE_OF = operator.attrgetter("dtype")
+
 
 MOE_SCORE_SOFTMAX = 0
 MOE_SCORE_SIGMOID = 1
@@ -621,19 +625,25 @@ def moe_grad_norm_workspace_bytes(n: int) -> int:
 
 
 def _grad_arrays(grads, device: torch.device) -> tuple:
-    """(pointers, sizes, types) of contiguous bf16 or fp32 tensors, as host arrays."""
-    n = len(grads)
-    kinds = [_SIDE_DTYPES.get(t.dtype, -1) if t.device == device and t.is_contiguous() else -1 for t in grads]
-    if -1 in kinds:
+    """(pointers, sizes, types) of contiguous bf16 or fp32 tensors, as host arrays
+    (filled by map: a list of tensors is gone through six times, but not in Python)."""
+    T = torch.Tensor
+    kinds = list(map(_SIDE_DTYPES.get, map(_DTYPE_OF, grads)))
+    if device.type != "cuda" or None in kinds or not set(map(T.get_device, grads)) <= {device.index} or \
+            not all(map(T.is_contiguous, grads)):
         raise ValueError(f"gradients must be contiguous bfloat16 or float32 tensors on {device}")
-    return ((_vp * n)(*[t.data_ptr() for t in grads]), (_i64 * n)(*[t.numel() for t in grads]), (_i32 * n)(*kinds))
+    return array("Q", map(T.data_ptr, grads)), array("q", map(T.numel, grads)), array("i", kinds)
+
+
+def _address(values: array) -> int:
+    return values.buffer_info()[0]
 
 
 def moe_grad_sumsq(grads, sumsq: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
     """grads: a sequence of tensors; sumsq: float64 [1]."""
     dev = sumsq.device
-    ptrs, sizes, kinds = _grad_arrays(grads, dev)
-    _on_device(dev, "moe_grad_sumsq", stream, ptrs, sizes, kinds, len(grads),
+    lists = _grad_arrays(grads, dev)
+    _on_device(dev, "moe_grad_sumsq", stream, *map(_address, lists), len(grads),
                _shaped(sumsq, torch.float64, (1,), "sumsq", dev), *_buffer(workspace, "workspace", dev))
 
 
@@ -645,7 +655,7 @@ def _clip_arrays(grads, outs, device: torch.device) -> tuple:
     if len(outs) != len(grads):
         raise ValueError("outs must have as many tensors as grads")
     to, osizes, okinds = _grad_arrays(outs, device)
-    if bytes(osizes) != bytes(sizes) or bytes(okinds) != bytes(kinds):
+    if osizes != sizes or okinds != kinds:
         raise ValueError("outs must have the sizes and types of grads")
     return ptrs, to, sizes, kinds
 
@@ -654,7 +664,8 @@ def moe_grad_clip(grads, outs, sumsq: torch.Tensor, max_norm: float, norm: torch
                   stream=None) -> None:
     """outs: a sequence of tensors like grads (the same one: in place)."""
     dev = sumsq.device
-    _on_device(dev, "moe_grad_clip", stream, *_clip_arrays(grads, outs, dev), len(grads),
+    lists = _clip_arrays(grads, outs, dev)
+    _on_device(dev, "moe_grad_clip", stream, *map(_address, lists), len(grads),
                _shaped(sumsq, torch.float64, (1,), "sumsq", dev), max_norm,
                _shaped(norm, torch.float32, (1,), "norm", dev))
 
@@ -663,7 +674,8 @@ def moe_clip_grad_norm(grads, outs, max_norm: float, workspace: torch.Tensor, su
                        norm: torch.Tensor | None = None, stream=None) -> None:
     """moe_grad_sumsq and moe_grad_clip in one call."""
     dev = workspace.device
-    _on_device(dev, "moe_clip_grad_norm", stream, *_clip_arrays(grads, outs, dev), len(grads), max_norm,
+    lists = _clip_arrays(grads, outs, dev)
+    _on_device(dev, "moe_clip_grad_norm", stream, *map(_address, lists), len(grads), max_norm,
                _shaped(sumsq, torch.float64, (1,), "sumsq", dev), _shaped(norm, torch.float32, (1,), "norm", dev),
                *_buffer(workspace, "workspace", dev))
 
