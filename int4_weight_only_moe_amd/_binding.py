@@ -32,7 +32,6 @@ MOE_DTYPE_F32 = 1
 _SIDE_DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32}
 _DTYPE_OF = operator.attrgetter("dtype")
 
-
 MOE_SCORE_SOFTMAX = 0
 MOE_SCORE_SIGMOID = 1
 _SCORINGS = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
