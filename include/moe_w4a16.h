@@ -471,7 +471,7 @@ int moe_lora_backward(const void* grad_out, int64_t ld_grad_out, int32_t out_dty
  *          scores: the lower group);
  *   topk_ids: the top_k of these experts with the highest c, highest first
  *          (equal c: the lower expert). Without a bias that is the order of the
- *          logits;
+ *          logits, and where group_top is 1 that of the groups' highest logits;
  *   topk_weights[j] = scale * s[e_j], or with renormalise scale * s[e_j] / sum
  *          of the kept s (softmax: the softmax over the kept logits; sigmoid:
  *          the sum plus 1e-20).

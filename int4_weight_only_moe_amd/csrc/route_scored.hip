@@ -135,8 +135,10 @@ __device__ __attribute__((noinline)) void route_row_exact(const float* row, cons
                                                           uint64_t* keys, Chosen* sel) {
   const int lane = threadIdx.x & 63;
   const bool grouped = top_groups < G;
+  // without scores in it the choice is that of the logits
+  const bool logits = !bias && (!grouped || group_top == 1);
   double m = -INFINITY, sum = 1.0;
-  if (!sigmoid) {
+  if (!sigmoid && !logits) {
 #pragma unroll 1
     for (int e = lane; e < E; e += 64) m = fmax(m, (double)row[e]);
 #pragma unroll 1
@@ -152,7 +154,7 @@ __device__ __attribute__((noinline)) void route_row_exact(const float* row, cons
     const double l = row[e], b = bias ? (double)bias[e] : 0.0;
     uint64_t key = 0;
     if (l != -INFINITY && b != -INFINITY) {
-      if (!bias && !grouped) key = key64(l);
+      if (logits) key = key64(l);
       else key = key64((sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - m) / sum) + b);
     }
     keys[e] = key;
@@ -244,7 +246,7 @@ struct RouteShared {
   union {
     // the candidates: (order key of c) << 32 | ~expert, zeros behind them
     __align__(16) uint64_t key[kMaxCand + kStep];
-    float groups[64];  // before that, the groups' scores
+    float groups[64][2];  // before that, the groups' scores and what they may be off
   } row[kRows];
   // with a bias: what c is computed from, and the candidates by rank
   float l[General ? kRows : 1][kMaxCand], b[General ? kRows : 1][kMaxCand];
@@ -284,7 +286,8 @@ __device__ __forceinline__ void route_rows(const ScoredArgs& a, int64_t t0, Rout
   if constexpr (General) {
     // fp32 errors in roundings of 2^-24: a sigmoid's are (1 - s) s (1.3 |l| + 2) + 3 s
     // < 4; a softmax value's p = pmax e^-x are (1.5 x + 50) p < 50 pmax (x from the
-    // exponent, the rest from the row's sum). c adds |c|. Twice that is `near`.
+    // exponent, the rest from the row's sum). c adds |c|, a sum of two c its own. Twice
+    // the first is `near`; what |c| adds is counted where c is known.
     const float score_error = a.sigmoid ? 0x1p-22f : 0x1p-18f * soft.inv;
 #pragma unroll
     for (int i = 0; i < N; ++i) largest = fmaxf(largest, inside(i) ? fabsf(v[i]) : 0.0f);
@@ -360,30 +363,33 @@ __device__ __forceinline__ void route_rows(const ScoredArgs& a, int64_t t0, Rout
         if (P > 1) join(dpp<kQuadSwap1>(__float_as_uint(m1)), dpp<kQuadSwap1>(__float_as_uint(m2)));
         if (P > 2) join(dpp<kQuadSwap2>(__float_as_uint(m1)), dpp<kQuadSwap2>(__float_as_uint(m2)));
         if (P > 4) join(dpp<kRowHalfMirror>(__float_as_uint(m1)), dpp<kRowHalfMirror>(__float_as_uint(m2)));
-        sh.row[r].groups[g] = a.group_top == 2 ? m1 + m2 : m1;
+        const bool two = a.group_top == 2;
+        const float off = !two && !a.bias ? 0.0f
+                                          : (two ? 2.0f : 1.0f) * score_error +
+                                                0x1p-22f * (fabsf(m1) + (two ? fabsf(m2) : 0.0f));
+        *(float2*)sh.row[r].groups[g] = make_float2(two ? m1 + m2 : m1, off);
       }
       wave_sync();
       uint64_t chosen = 0;
       float in = INFINITY, out = -INFINITY;
       for (int g0 = 0; g0 < G; g0 += Lanes) {
         const int g = g0 + l;
-        const float s = g < G ? sh.row[r].groups[g] : 0.0f;
+        const float s = g < G ? sh.row[r].groups[g][0] : 0.0f, off = g < G ? sh.row[r].groups[g][1] : 0.0f;
         int rank = 0;
 #pragma unroll 8
         for (int h = 0; h < G; ++h) {
-          const float o = sh.row[r].groups[h];
+          const float o = sh.row[r].groups[h][0];
           rank += (int)(o > s) | ((int)(o == s) & (int)(h < g));
         }
         const bool take = g < G && rank < a.top_groups;
         const uint64_t m = __ballot(take) >> (lane & (64 - Lanes));
         chosen |= (Lanes == 32 ? (m & 0xffffffffu) : (m & 0xffffu)) << g0;
-        in = take ? fminf(in, s) : in;
-        out = g < G && !take ? fmaxf(out, s) : out;
+        in = take ? fminf(in, s - off) : in;
+        out = g < G && !take ? fmaxf(out, s + off) : out;
       }
       in = -row_max<Lanes>(-in);
       out = row_max<Lanes>(out);
-      if (a.bias || a.group_top == 2)
-        bad |= !(in - out > 4.0f * score_error + 0x1p-21f * fmaxf(fabsf(in), fabsf(out)));
+      if (a.bias || a.group_top == 2) bad |= !(in > out);
       // The values in another order: a lane's experts lie `Lanes` apart, so that
       // a group's are spread over all lanes. (Neighbours of 4 a lane leave lanes
       // empty, the threshold is then low and the candidates are many: ranking
@@ -491,8 +497,9 @@ __device__ __forceinline__ void route_rows(const ScoredArgs& a, int64_t t0, Rout
       bool close = false;
       for (int i = l; i + 1 < n; i += Lanes) {
         const int u = sh.by_rank[r][i], w = sh.by_rank[r][i + 1];
-        const float apart = key_value((uint32_t)(sh.row[r].key[u] >> 32)) - key_value((uint32_t)(sh.row[r].key[w] >> 32));
-        close |= (apart <= near) & ((sh.l[r][u] != sh.l[r][w]) | (sh.b[r][u] != sh.b[r][w]));
+        const float cu = key_value((uint32_t)(sh.row[r].key[u] >> 32)), cw = key_value((uint32_t)(sh.row[r].key[w] >> 32));
+        close |= (cu - cw <= near + 0x1p-22f * fmaxf(fabsf(cu), fabsf(cw))) &
+                 ((sh.l[r][u] != sh.l[r][w]) | (sh.b[r][u] != sh.b[r][w]));
       }
       if (__any(close && live)) {  // the candidates again, in fp64
         uint64_t* c64 = (uint64_t*)buffer + sub * kMaxCand;

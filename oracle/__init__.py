@@ -441,7 +441,9 @@ def route_scored(logits, k, scoring="softmax", bias=None, n_groups=1, top_groups
         if top_groups < n_groups:
             best = []
             for g in range(n_groups):
-                inside = sorted((c[e] for e in there if e // size == g), key=_rank_key)
+                # without a bias the highest score is the highest logit's, however close they are
+                value = row if bias is None and group_top == 1 else c
+                inside = sorted((value[e] for e in there if e // size == g), key=_rank_key)
                 if inside:
                     best.append((_rank_key(sum(inside[:group_top])), g))
             chosen = {g for _, g in sorted(best)[:top_groups]}

@@ -200,6 +200,43 @@ def test_route_scored_masked_experts(scoring, biased, groups):
                 check(x, k, scoring, bias, groups, renormalise)
 
 
+@pytest.mark.parametrize("groups", ((1, 1, 1), (8, 3, 1), (8, 3, 2)))
+def test_route_scored_large_biases_close_together(groups):
+    """A few biases far above the others (100, whose fp32 sums are 4e-6 off) and nearly equal c among
+    them; of both signs within a group, so that a group's sum is smaller than its terms' errors."""
+    rng = np.random.default_rng(70)
+    M, E, k = 400, 64, 6
+    logits = normal(M, E, 71)
+    bias = (0.05 * rng.standard_normal(E)).astype(np.float32)
+    s = 1 / (1 + np.exp(-logits[0].astype(np.float64)))
+    logits[:200] = logits[0] + rng.integers(-3, 4, (200, E)).astype(np.float32) * np.float32(2.0 ** -18)
+    for where, value in ((rng.permutation(E)[:5], 100.0), (np.arange(0, E, 8), 100.0), (np.arange(1, E, 8), -100.0)):
+        bias[where] = (value - s[where]).astype(np.float32)
+        check(logits, k, "sigmoid", bias, groups, False)
+    rest = np.setdiff1d(np.arange(E), np.concatenate([np.arange(0, E, 8), np.arange(1, E, 8)]))
+    bias[rest] = -100.0 - 0.01 * rng.random(len(rest)).astype(np.float32)
+    check(logits, k, "sigmoid", bias, groups, False)
+    bias[rest] = -np.inf  # the two left in a group add up to nearly 0
+    check(logits, k, "sigmoid", bias, groups, False)
+    bias[rest] = -1e6
+    check(logits, k, "sigmoid", bias, groups, False)
+
+
+def test_route_scored_groups_of_saturated_scores():
+    """Logits whose scores are the same in fp64: without a bias the logits decide, between groups as well."""
+    M, E, k = 40, 48, 5
+    rng = np.random.default_rng(72)
+    for logits in (50 + 9 * rng.random((M, E)), -800 - 9 * rng.random((M, E)), 1e-20 * rng.standard_normal((M, E))):
+        lg = logits.astype(np.float32)
+        for bad in (False, True):
+            if bad:
+                lg[:, 7] = -np.inf  # (by the exact path)
+            for scoring in ("sigmoid", "softmax"):
+                check(lg, k, scoring, None, (6, 2, 1))
+                if scoring == "softmax" or lg.max() > -700:
+                    check(lg, k, scoring, None, (6, 2, 2), False)
+
+
 def test_route_scored_nan_bias_and_infinite_logits():
     """A NaN bias or logit counts as the highest c; +inf saturates a sigmoid and makes a softmax NaN."""
     M, E, k = 12, 80, 4
