@@ -186,7 +186,7 @@ __device__ __forceinline__ void put(uint4* p, uint4 v) {
 
 // The workgroups go through the tensors from the last to the first: what the
 // pass over the squares read last is still in the cache. 705 MB read and written:
-// 251 us (5.6 TB/s); from the first to the last the two passes take 383 us, not 372.
+// 252 us (5.6 TB/s); from the first to the last the two passes take 383 us, not 372.
 //
 // n_parts > 0: sumsq is still in that many parts, which every workgroup adds
 // itself, in the same order: one launch less, and up to kJoinParts of them cost less

@@ -231,8 +231,8 @@ __device__ __forceinline__ void to_e4m3(const float (&h)[8], const float (&w)[8]
 }
 
 // One row a team. [16384, 7168] bf16: 161 us for 940 MB (5.8 TB/s; a copy of as much
-// takes 181), [2048, 7168] of an fp32 stream with bf16 and 8-bit results 42 to 44 us for
-// 191 MB (4.4 TB/s): there 46 vector instructions a column of a lane, 17 us of issue,
+// takes 181), [2048, 7168] of an fp32 stream with bf16 and 8-bit results 45 us for
+// 191 MB (4.3 TB/s): there 46 vector instructions a column of a lane, 17 us of issue,
 // run beside the loads of only two workgroups a CU (93 registers).
 template <bool Wide, int C, bool Vec, typename S, bool Quant>
 __global__ __launch_bounds__(Wide ? 64 * kMaxWaves : 256) void norm_kernel(NormArgs a) {
@@ -444,7 +444,7 @@ struct BackwardRow {
 
 // A workgroup takes the rows kRows (blockIdx.x + n gridDim.x) + 0 .. kRows - 1
 // and leaves their sums for dw in parts[blockIdx.x]: they stay in registers over
-// all its rows. [16384, 7168] bf16: 173 us for 947 MB (5.5 TB/s).
+// all its rows. [16384, 7168] bf16: 176 us for 947 MB (5.4 TB/s).
 template <bool Wide, int C, bool Vec, typename S>
 __global__ __launch_bounds__(Wide ? 64 * kMaxWaves : 256) void norm_backward_kernel(NormBackwardArgs a) {
   using T = Team<Wide>;

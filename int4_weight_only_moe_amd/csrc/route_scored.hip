@@ -575,10 +575,9 @@ __device__ __forceinline__ void route_rows(const ScoredArgs& a, int64_t t0, Rout
 // One pass of rows a workgroup, from row `first_row` on: in a loop the compiler
 // keeps what does not depend on the row (biases, groups of the experts) in
 // registers, twice as many as fit 4 waves a SIMD.
-// [16384, 384] softmax, top 8: 8.5 us (26 MB, 5.0 us at the rate of a copy): some 146
-// vector instructions a row, 3.9 us of issue, beside the loads. Sigmoid and a bias
-// 11.5 us; [16384, 256] in 8 groups 16.1, where the groups' two passes through LDS take
-// 5. [4096, 256] in groups has two waves a SIMD and takes 10 us of latency.
+// [16384, 384] softmax, top 8: 9.1 us (26 MB, 5.0 us at the rate of a copy): 146 vector
+// instructions a row, 3.9 us of issue, beside the loads. Sigmoid and a bias 11.5 us; [16384, 256] in 8 groups 16.1, where the groups' two passes through LDS take
+// 5. [4096, 256] in groups has two waves a SIMD and takes 10.7 us of latency.
 template <int Lanes, int NV, bool Vec, bool General>
 __global__ __launch_bounds__(kThreads) void route_scored_kernel(ScoredArgs a, int64_t first_row) {
   extern __shared__ __align__(16) float buffer[];
@@ -594,7 +593,7 @@ __global__ __launch_bounds__(kThreads) void route_scored_kernel(ScoredArgs a, in
 
 // Up to 16 rows: routing and grouping in one workgroup and one launch (two launches
 // follow each other every 3.6 us). The grouping's tables take the dynamic LDS after
-// the routing. One row of 384: 7.2 us, the latency of one wave's steps.
+// the routing. One row of 384: 7.4 us, the latency of one wave's steps.
 template <int Lanes, int NV, bool Vec, bool General>
 __global__ __launch_bounds__(kThreads) void route_scored_small_kernel(ScoredArgs a) {
   extern __shared__ __align__(16) float buffer[];
@@ -654,7 +653,8 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 // experts): every logit has a gradient. Otherwise only the kept ones have;
 // the rest of the row is grad_base or zeros, and is not touched in place.
 // The slots' values reach the row's order through LDS.
-// Bound by HBM: [16384, 384] full 9.6 us for 51 MB (5.4 TB/s).
+// Bound by HBM: [16384, 384] full: calls back to back every 9.6 us for 51 MB
+// (5.4 TB/s).
 template <int Lanes, int NV, bool Vec, bool Full>
 __global__ __launch_bounds__(kThreads) void route_scored_backward_kernel(ScoredBackwardArgs a, int64_t first_row) {
   extern __shared__ __align__(16) float buffer[];
