@@ -540,6 +540,8 @@ int moe_route_scored_backward(const float* logits, int32_t M, int32_t E, int32_t
  *   rstd        fp32 [M]: r, for the backward call, or NULL.
  * At least one of out_bf16 and out8_e4m3. A row that holds NaN is NaN, one that
  * holds an infinity has r = 0.
+ * out_bf16 and rstd take r in fp32: with eps 0 a row whose root of the mean square
+ * is below some 2^-128 has an infinite rstd and no finite out_bf16 (zeros: NaN).
  * Sums are fp64. Results are identical on every call.
  *
  * moe_add_rms_norm_backward, from grad_out (bf16 [M, N]):

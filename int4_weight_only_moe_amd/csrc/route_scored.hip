@@ -576,8 +576,9 @@ __device__ __forceinline__ void route_rows(const ScoredArgs& a, int64_t t0, Rout
 // keeps what does not depend on the row (biases, groups of the experts) in
 // registers, twice as many as fit 4 waves a SIMD.
 // [16384, 384] softmax, top 8: 9.1 us (26 MB, 5.0 us at the rate of a copy): 146 vector
-// instructions a row, 3.9 us of issue, beside the loads. Sigmoid and a bias 11.5 us; [16384, 256] in 8 groups 16.1, where the groups' two passes through LDS take
-// 5. [4096, 256] in groups has two waves a SIMD and takes 10.7 us of latency.
+// instructions a row, 3.9 us of issue, beside the loads. Sigmoid and a bias 11.5 us;
+// [16384, 256] in 8 groups 16.1, where the groups' two passes through LDS take 5.
+// [4096, 256] in groups has two waves a SIMD and takes 10.7 us of latency.
 template <int Lanes, int NV, bool Vec, bool General>
 __global__ __launch_bounds__(kThreads) void route_scored_kernel(ScoredArgs a, int64_t first_row) {
   extern __shared__ __align__(16) float buffer[];

@@ -144,6 +144,21 @@ def test_norm_magnitudes():
     assert not bufs.out.any() and (bufs.scales == 2.0 ** -126).all() and not bufs.out8.view(torch.uint8).any()
 
 
+def test_norm_beyond_the_range_of_rstd():
+    """Without eps: r of rows below 2^-128 is infinite in fp32, other rows are not touched by it."""
+    N = 256
+    h = torch.ones((4, N), dtype=F32)
+    h[0] *= 2.0 ** -140
+    h[1] *= -(2.0 ** -120)
+    h[2] = 0.0
+    w = torch.ones(N, dtype=BF16, device="cuda")
+    bufs = moe.alloc_norm_buffers(4, N, F32, rstd=True)
+    moe.add_rms_norm(None, w, bufs, residual=h.cuda(), eps=0.0)
+    assert torch.isinf(bufs.rstd[[0, 2]]).all() and bufs.rstd[1] == 2.0 ** 120 and bufs.rstd[3] == 1.0
+    assert torch.isinf(bufs.out[0]).all() and (bufs.out[0] > 0).all() and torch.isnan(bufs.out[2]).all()
+    assert (bufs.out[1] == -1.0).all() and (bufs.out[3] == 1.0).all()
+
+
 def test_norm_nan_and_infinity():
     N = 256
     x, _, w = tensors(4, N, BF16, 9)
