@@ -552,7 +552,8 @@ int moe_route_scored_backward(const float* logits, int32_t M, int32_t E, int32_t
  *   grad_residual [M, N] of res_dtype, what reaches h beside the norm, or NULL.
  *   grad_h      [M, N] of res_dtype; may be the same matrix as grad_residual
  *               or, where the type is the same, as grad_out or h; or NULL.
- *   grad_weight fp32 [N], every element written (M = 0: zeros), or NULL.
+ *   grad_weight fp32 [N], every element written (M = 0: zeros), or NULL. Runs of
+ *               at most 64 rows are summed in fp32, the runs in fp64.
  *   workspace   >= moe_add_rms_norm_workspace_bytes(M, N) bytes, 16-byte
  *               aligned; contents on entry do not matter. One for a larger M
  *               serves smaller ones. Not used (may be NULL) without grad_weight.

@@ -442,16 +442,28 @@ struct BackwardRow {
   }
 };
 
+// Rows that a lane adds for dw in fp32 one after another: at most so many roundings
+// of 2^-24, however many rows there are. (Equal rows lost 6e-5 of a sum of 4096.)
+constexpr int kRunRows = 64;
+constexpr int kRunsMaxWidth = 16384;  // 128 KB of fp64 sums
+
 // A workgroup takes the rows kRows (blockIdx.x + n gridDim.x) + 0 .. kRows - 1
 // and leaves their sums for dw in parts[blockIdx.x]: they stay in registers over
 // all its rows. [16384, 7168] bf16: 176 us for 947 MB (5.4 TB/s).
-template <bool Wide, int C, bool Vec, typename S>
+// Runs: more than kRunRows rows a lane. After each run of so many the sums are added
+// to fp64 ones in LDS, where each lane has places of its own. Back to back calls of
+// [131072, 7168] bf16: 1402 us (1399 with one fp32 sum over all rows; 1436 with the
+// fp64 sums in HBM, whose loads nothing hides; 1459 with the run's end tested in the
+// loop over rows, which then waits for the row in flight).
+template <bool Wide, int C, bool Vec, typename S, bool Runs>
 __global__ __launch_bounds__(Wide ? 64 * kMaxWaves : 256) void norm_backward_kernel(NormBackwardArgs a) {
   using T = Team<Wide>;
   constexpr bool kAhead = Vec && C <= 2 && sizeof(S) == 2;
   __shared__ float room[kMaxWaves];
-  extern __shared__ __align__(16) float sums[];  // not Wide: [kRows][N]
+  extern __shared__ __align__(16) float sums[];  // not Wide: [kRows][N]; before that with Runs [kRows][8 C lanes] in fp64
   const int lane = T::lane(), lanes = T::lanes(), N = a.N;
+  double* whole = (double*)sums + T::row() * (8 * C * lanes) + lane;  // of this lane, `lanes` apart
+  bool any = false;  // whether there are sums in `whole`
   const int64_t step = (int64_t)gridDim.x * T::kRows;
   float acc[C][8];
 #pragma unroll
@@ -466,58 +478,79 @@ __global__ __launch_bounds__(Wide ? 64 * kMaxWaves : 256) void norm_backward_ker
   int64_t t = (int64_t)blockIdx.x * T::kRows + T::row();
   BackwardRow<C, Vec, S> next;
   if (kAhead && t < a.M) next.load(a, t, lane, lanes);
-  for (; t < a.M; t += step) {
-    BackwardRow<C, Vec, S> row;
-    if constexpr (kAhead) {
-      row = next;
-      next.load(a, t + step < a.M ? t + step : t, lane, lanes);
-    } else {
-      row.load(a, t, lane, lanes);
-    }
-    float dot = 0.0f;
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-      float g[8], n[8], wv[8];
-      row.g[i].values(g);
-      row.h[i].values(n);
-      if (C > 2) w[i].load(a.w, i, lane, lanes, N);
-      w[i].values(wv);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        if (column<Vec>(i, Vec ? 0 : q, lane, lanes) >= N) g[q] = n[q] = 0.0f;  // (Vec: N % 8 == 0)
-        n[q] *= row.r;
-        acc[i][q] = fmaf(g[q], n[q], acc[i][q]);
-        dot = fmaf(g[q] * wv[q], n[q], dot);
-        // now, not behind the row's sum: that would keep g and n unpacked over it
-        asm volatile("" : "+v"(acc[i][q]));
+  for (;;) {
+    const int64_t stop = Runs && t + kRunRows * step < a.M ? t + kRunRows * step : a.M;
+    for (; t < stop; t += step) {
+      BackwardRow<C, Vec, S> row;
+      if constexpr (kAhead) {
+        row = next;
+        next.load(a, t + step < a.M ? t + step : t, lane, lanes);
+      } else {
+        row.load(a, t, lane, lanes);
       }
-    }
-    dot = T::sum(dot, room) * inv_n;
-    if (a.dh) {
+      float dot = 0.0f;
 #pragma unroll
       for (int i = 0; i < C; ++i) {
-        float y[8], n[8], wv[8];
-        row.g[i].forget();
-        row.h[i].forget();
-        w[i].forget();
-        row.g[i].values(y);
+        float g[8], n[8], wv[8];
+        row.g[i].values(g);
         row.h[i].values(n);
         if (C > 2) w[i].load(a.w, i, lane, lanes, N);
         w[i].values(wv);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) y[q] = row.r * (y[q] * wv[q] - n[q] * row.r * dot);
-        if (a.dres) {
-          float d[8];
-          if (C > 2) row.d[i].load((const S*)a.dres + t * a.ld_dres, i, lane, lanes, N);
-          row.d[i].values(d);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) y[q] += d[q];
+        for (int q = 0; q < 8; ++q) {
+          if (column<Vec>(i, Vec ? 0 : q, lane, lanes) >= N) g[q] = n[q] = 0.0f;  // (Vec: N % 8 == 0)
+          n[q] *= row.r;
+          acc[i][q] = fmaf(g[q], n[q], acc[i][q]);
+          dot = fmaf(g[q] * wv[q], n[q], dot);
+          // now, not behind the row's sum: that would keep g and n unpacked over it
+          asm volatile("" : "+v"(acc[i][q]));
         }
-        store_chunk<Vec>((S*)a.dh + t * a.ld_dh, i, lane, lanes, N, y);
+      }
+      dot = T::sum(dot, room) * inv_n;
+      if (a.dh) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+          float y[8], n[8], wv[8];
+          row.g[i].forget();
+          row.h[i].forget();
+          w[i].forget();
+          row.g[i].values(y);
+          row.h[i].values(n);
+          if (C > 2) w[i].load(a.w, i, lane, lanes, N);
+          w[i].values(wv);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) y[q] = row.r * (y[q] * wv[q] - n[q] * row.r * dot);
+          if (a.dres) {
+            float d[8];
+            if (C > 2) row.d[i].load((const S*)a.dres + t * a.ld_dres, i, lane, lanes, N);
+            row.d[i].values(d);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) y[q] += d[q];
+          }
+          store_chunk<Vec>((S*)a.dh + t * a.ld_dh, i, lane, lanes, N, y);
+        }
       }
     }
+    if (!Runs || t >= a.M) break;
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        double& s = whole[(8 * i + q) * lanes];
+        s = (any ? s : 0.0) + (double)acc[i][q];
+        acc[i][q] = 0.0f;
+      }
+    any = true;
   }
   if (!a.dw) return;
+  if constexpr (Runs) {
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (any) acc[i][q] = (float)(whole[(8 * i + q) * lanes] + (double)acc[i][q]);
+    if (!Wide) __syncthreads();  // `sums` take the place of the waves' fp64 ones
+  }
   float* part = a.parts + (int64_t)blockIdx.x * N;
   if constexpr (Wide) {
 #pragma unroll
@@ -574,7 +607,7 @@ void by_width(int N, F fn) {
   auto all = [&](auto c) { fn(std::true_type{}, c, 64u * (unsigned)ceil_div(N, 512 * decltype(c)::value)); };
   if (N <= 512) one(integral_constant<int, 1>{});
   else if (N <= 1024) one(integral_constant<int, 2>{});
-  else if (N <= 16384) all(integral_constant<int, 2>{});
+  else if (N <= kRunsMaxWidth) all(integral_constant<int, 2>{});
   else all(integral_constant<int, 4>{});
 }
 
@@ -634,8 +667,11 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
 // in flight while it computes another; more of them only leave more sums and
 // spread the rows in flight ([16384, 7168] bf16: 173 us with 256, 189 with 512, 196
 // with 1024; of 2048 columns 76, 58 and 58).
+// Rows too wide for fp64 sums in LDS have a workgroup for every kRunRows of them.
 int norm_backward_parts(int64_t M, int64_t N) {
-  const int64_t most = N > 2048 ? 256 : N > 1024 ? 512 : 1024, n = N > 1024 ? M : ceil_div(M, 4);
+  int64_t most = N > 2048 ? 256 : N > 1024 ? 512 : 1024;
+  if (N > kRunsMaxWidth) most *= ceil_div(M, most * kRunRows);
+  const int64_t n = N > 1024 ? M : ceil_div(M, 4);
   return (int)(n < 1 ? 1 : n < most ? n : most);
 }
 
@@ -643,18 +679,36 @@ hipError_t launch_norm_backward(const NormBackwardArgs& a, hipStream_t stream) {
   const int size = a.f32 ? 4 : 2;
   const int teams = norm_backward_parts(a.M, a.N);
   if (a.M > 0 && (a.dh || a.dw)) {
+    hipError_t allowed = hipSuccess;
     const bool vec = a.N % 8 == 0 && chunks_ok(a.dout, a.ld_dout, 2) && chunks_ok(a.h, a.ld_h, size) &&
                      chunks_ok(a.w, 8, 2) && chunks_ok(a.dres, a.ld_dres, size) && chunks_ok(a.dh, a.ld_dh, size);
     by_width(a.N, [&](auto wide, auto c, unsigned threads) {
       constexpr bool W = decltype(wide)::value;
       constexpr int C = decltype(c)::value;
-      const unsigned lds = W ? 0u : (unsigned)(Team<W>::kRows * a.N * 4);
+      const int rows = Team<W>::kRows;
       auto go = [&](auto v, auto s) {
-        norm_backward_kernel<W, C, decltype(v)::value, decltype(s)><<<teams, threads, lds, stream>>>(a);
+        constexpr bool V = decltype(v)::value;
+        using S = decltype(s);
+        if constexpr (C <= 2) {
+          if (a.M > (int64_t)kRunRows * rows * teams) {
+            const unsigned lds = 8u * 8 * C * (W ? threads : 64u * rows);
+            constexpr auto kernel = norm_backward_kernel<W, C, V, S, true>;
+            if (lds > 64 * 1024) {  // (the limit of a kernel that does not ask for more)
+              allowed = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+              if (allowed != hipSuccess) return;
+            }
+            kernel<<<teams, threads, lds, stream>>>(a);
+            return;
+          }
+        }
+        const unsigned lds = W ? 0u : (unsigned)(rows * a.N * 4);
+        norm_backward_kernel<W, C, V, S, false><<<teams, threads, lds, stream>>>(a);
       };
       auto typed = [&](auto v) { a.f32 ? go(v, float{}) : go(v, uint16_t{}); };
       vec ? typed(std::true_type{}) : typed(std::false_type{});
     });
+    if (allowed != hipSuccess) return allowed;
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
   }

@@ -356,6 +356,75 @@ def test_norm_workspace_of_a_larger_batch_and_offsets_past_32_bits():
     assert torch.equal(small[0], dh[-64:])
 
 
+@pytest.mark.parametrize("M,N,dtype", [(2**24, 8, BF16), (2**20 + 5, 1000, F32), (2**20 + 77, 1028, BF16),
+                                       (2**20 + 3, 2056, BF16), (2**19 + 1, 2056, F32), (2**18 + 9, 7001, BF16),
+                                       (2**18 + 1, 16384, BF16), (2**18 + 3, 16392, BF16)])
+def test_norm_weight_gradient_of_long_batches(M, N, dtype):
+    """Terms of one sign, the same in most rows: what a running sum in fp32 loses over thousands of rows.
+    The bound does not grow with M: n 1 rounding, 63 of the fp32 sum of a run of rows (the first is added to
+    0), 1 for a wave's sum of its runs, 3 to join the waves of narrow rows, the rest is fp64, 1 for the result."""
+    g = torch.Generator().manual_seed(N)
+    h, dy = torch.empty((M, N), dtype=dtype, device="cuda"), torch.empty((M, N), dtype=BF16, device="cuda")
+    h[:] = (0.5 + torch.rand(N, generator=g)).to(dtype).cuda()
+    dy[:] = (0.5 + torch.rand(N, generator=g)).to(BF16).cuda()
+    odd = torch.randint(0, M, (500,), generator=g).unique()  # some rows are others, the first and the last too
+    odd = torch.cat([odd, torch.tensor([0, M - 1])]).unique().cuda()
+    dy[odd] = (40 * torch.rand(len(odd), N, generator=g)).to(BF16).cuda()
+    r = torch.full((M,), 0.7, device="cuda")
+    r[odd] = (0.5 + torch.rand(len(odd), generator=g)).cuda()
+    want = torch.zeros(N, dtype=torch.float64, device="cuda")
+    for part in range(0, M, 2**16):
+        rows = slice(part, part + 2**16)
+        want += (dy[rows].double() * h[rows].double() * r[rows].double()[:, None]).sum(0)
+    w = torch.ones(N, dtype=BF16, device="cuda")
+    need = moe.moe_add_rms_norm_workspace_bytes(M, N)
+    ws = torch.full((need + 4096,), 255, dtype=torch.uint8, device="cuda")
+    for _ in range(2):  # (what the workspace holds does not matter)
+        _, dw = moe.add_rms_norm_backward(dy, h, r, w, need_h=False, workspace=ws[:need])
+        assert (dw.double() - want).abs().le((1 + 63 + 1 + 3 + 1) * U * want).all()
+    assert (ws[need:] == 255).all()
+
+
+@pytest.mark.parametrize("N,rows", [(40, 2**18), (1032, 2**15), (2056, 2**14), (16384, 2**14), (16392, 2**14)])
+def test_norm_backward_around_the_longest_run(N, rows):
+    """One row more than every lane's run of 64 holds, with a last workgroup that has only some of its rows."""
+    for dtype in (BF16, F32):
+        g = torch.Generator(device="cuda").manual_seed(N)
+        M = rows + 3
+        h = torch.randn((M, N), generator=g, device="cuda").to(dtype)
+        dy = torch.randn((M, N), generator=g, device="cuda").to(BF16)
+        r = 0.5 + torch.rand(M, generator=g, device="cuda")
+        w = torch.randn(N, generator=g, device="cuda").to(BF16)
+        some = moe.add_rms_norm_backward(dy[:100], h[:100], r[:100], w)[0]
+        for m in (rows - 1, rows, rows + 1, rows + 3):
+            dh, dw = moe.add_rms_norm_backward(dy[:m], h[:m], r[:m], w)
+            assert torch.equal(dh[:100], some)
+            t = dy[:m].double() * h[:m].double() * r[:m].double()[:, None]
+            assert (dw.double() - t.sum(0)).abs().le((1 + 63 + 1 + 3 + 1) * U * t.abs().sum(0)).all()
+            last = moe.add_rms_norm_backward(dy[m - 100:m], h[m - 100:m], r[m - 100:m], w)[0]
+            assert torch.equal(dh[-100:], last)
+
+
+def test_norm_backward_of_a_long_batch_replays():
+    M, N = 2**14 + 40, 9000  # fp64 sums of more than 64 KB of LDS
+    h, dy = torch.randn((M, N), device="cuda").to(BF16), torch.randn((M, N), device="cuda").to(BF16)
+    keep, r, w = dy.clone(), 0.5 + torch.rand(M, device="cuda"), torch.randn(N, device="cuda").to(BF16)
+    ws = torch.empty(moe.moe_add_rms_norm_workspace_bytes(M, N), dtype=torch.uint8, device="cuda")
+    grads = (torch.empty_like(h), torch.empty(N, device="cuda"))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        moe.add_rms_norm_backward(dy, h, r, w, grads=grads, workspace=ws)
+    for rep in range(4):
+        dy.copy_(keep * (1 + rep % 2))
+        for t in (*grads, ws):
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        replayed = [t.clone() for t in grads]
+        eager = moe.add_rms_norm_backward(dy, h, r, w)
+        assert all(torch.equal(a, b) for a, b in zip(replayed, eager))
+
+
 def test_norm_wrapper_refusals():
     x = torch.zeros((4, 64), dtype=BF16, device="cuda")
     w = torch.zeros(64, dtype=BF16, device="cuda")
