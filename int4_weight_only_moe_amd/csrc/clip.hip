@@ -210,10 +210,12 @@ __global__ __launch_bounds__(kThreads) void grad_clip_kernel(Table<kN> tab, cons
     if (n_parts > 0 && sumsq) *sumsq = total;
   }
   const bool over = root > (double)max_norm && root < INFINITY;
-  // the factor in two steps where it is too small for a normal fp32 number
+  // in fp64 where the factor may be too small for a normal fp32 number (down to
+  // 2^-270 with results that are normal ones)
   const double ratio = over ? (double)max_norm / root : 1.0;
-  const float step = ratio < 0x1p-100 ? 0x1p-64f : 1.0f;
-  const float factor = (float)(ratio / (double)step);
+  const float factor = (float)ratio;
+  const bool tiny = ratio < 0x1p-100;
+  auto scaled = [&](float v) { return tiny ? (float)((double)v * ratio) : v * factor; };
   if (!tab.n) return;
   walk<true>(
       tab, blockIdx.x, gridDim.x,
@@ -228,8 +230,8 @@ __global__ __launch_bounds__(kThreads) void grad_clip_kernel(Table<kN> tab, cons
           for (int j = 0; j < 2 * kPasses; ++j) {
             float v[4];
             four(unit.v[j], v);
-            put(q + j * kThreads, make_uint4(__float_as_uint(v[0] * step * factor), __float_as_uint(v[1] * step * factor),
-                                         __float_as_uint(v[2] * step * factor), __float_as_uint(v[3] * step * factor)));
+            put(q + j * kThreads, make_uint4(__float_as_uint(scaled(v[0])), __float_as_uint(scaled(v[1])),
+                                             __float_as_uint(scaled(v[2])), __float_as_uint(scaled(v[3]))));
           }
         } else {
           uint4* q = (uint4*)((uint16_t*)tab.out[i] + first) + threadIdx.x;
@@ -240,7 +242,7 @@ __global__ __launch_bounds__(kThreads) void grad_clip_kernel(Table<kN> tab, cons
             uint32_t u[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              u[k] = (uint32_t)to_bf16(v[2 * k] * step * factor) | ((uint32_t)to_bf16(v[2 * k + 1] * step * factor) << 16);
+              u[k] = (uint32_t)to_bf16(scaled(v[2 * k])) | ((uint32_t)to_bf16(scaled(v[2 * k + 1])) << 16);
             put(q + j * kThreads, make_uint4(u[0], u[1], u[2], u[3]));
           }
         }
@@ -248,7 +250,7 @@ __global__ __launch_bounds__(kThreads) void grad_clip_kernel(Table<kN> tab, cons
       [&](int i, int64_t first, int64_t stop) {
         if (!over && tab.grad[i] == tab.out[i]) return;
         for (int64_t e = first + threadIdx.x; e < stop; e += kThreads)
-          store_one(tab.out[i], tab.f32[i], e, load_one(tab.grad[i], tab.f32[i], e) * step * factor);
+          store_one(tab.out[i], tab.f32[i], e, scaled(load_one(tab.grad[i], tab.f32[i], e)));
       });
 }
 

@@ -113,6 +113,25 @@ def test_clip_magnitudes():
     assert not g[0].any()
 
 
+@pytest.mark.parametrize("kind", (F32, BF16))
+def test_clip_factors_far_below_the_normal_numbers(kind):
+    """Gradients near fp32's largest value and bounds down to its smallest: factors to 2^-270, results of ordinary size."""
+    grads = make((5000, 300), (kind, kind), 15, scale=3e37)
+    keep = [t.double() for t in grads]
+    root = sum(float(t.square().sum()) for t in keep) ** 0.5
+    for most in (1e-15, 1e-20, 1e-22, 1e-25, 1e-30, 1e-35, 1e-40):
+        out = [torch.full_like(t, 7.0) for t in grads]
+        moe.clip_grad_norm(grads, most, out=out)
+        assert most < 1e-29 or all(t.abs().max() > 0 for t in out)
+        whole = [t.clone() for t in grads]
+        moe.clip_grad_norm(whole, most)
+        for a, b, c in zip(keep, out, whole):
+            exact = a * (float(np.float32(most)) / root)
+            half = HALF_BF16 if kind == BF16 else U
+            assert (b.double() - exact).abs().le((half + 2.1 * U) * exact.abs() + 2.0 ** -133 * (kind == BF16) + 2.0 ** -148).all()
+            assert torch.equal(b, c)
+
+
 @pytest.mark.parametrize("bad", (float("nan"), float("inf"), -float("inf")))
 def test_clip_not_finite_scales_nothing(bad):
     grads = make((3000, 50), (F32, BF16), 9)
