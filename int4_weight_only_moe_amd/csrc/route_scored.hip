@@ -118,6 +118,12 @@ __device__ __forceinline__ float sigmoid_of(float l) {  // to the last bits for 
   return l != l ? l : (l >= 0.0f ? 1.0f : e) / (1.0f + e);
 }
 
+// A score (or its slope, for logits of either sign) that may be subnormal in fp32 is
+// the square of half_exp, which is not: what it is divided or multiplied by goes in
+// between the two.
+__device__ __forceinline__ bool tiny_exp(float l) { return fabsf(l) > 80.0f; }
+__device__ __forceinline__ float half_exp(float l) { return expf(-0.5f * fabsf(l)); }
+
 // Scores as the fast path computes them.
 __device__ __forceinline__ float fast_sigmoid(float l) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * l));
@@ -551,10 +557,15 @@ __device__ __forceinline__ void route_rows(const ScoredArgs& a, int64_t t0, Rout
   const int e = slot.e;
   const bool has = e >= 0;
   const float lg = slot.l;
-  float w;
+  float w, scale = a.scale;
   if (a.sigmoid) {
     w = has ? sigmoid_of(lg) : 0.0f;
-    if (a.renorm) w = w / (row_sum<Lanes>(w) + kDenom);
+    const float total = a.renorm ? row_sum<Lanes>(w) + kDenom : 1.0f;
+    if (has && lg < 0.0f && tiny_exp(lg)) {
+      w = half_exp(lg);
+      scale *= w;
+    }
+    if (a.renorm) w = w / total;
   } else if (a.renorm) {
     // (a NaN has to reach the whole row; fmaxf leaves it out)
     const float top_l = row_max<Lanes>(lg);
@@ -566,7 +577,7 @@ __device__ __forceinline__ void route_rows(const ScoredArgs& a, int64_t t0, Rout
   }
   if (active && l < k) {
     a.ids[t * k + l] = e;
-    a.weights[t * k + l] = has ? a.scale * w : 0.0f;
+    a.weights[t * k + l] = has ? scale * w : 0.0f;
     if (copy) copy[t * k + l] = e;
   }
   wave_sync();
@@ -695,12 +706,13 @@ __global__ __launch_bounds__(kThreads) void route_scored_backward_kernel(ScoredB
   } else {
     const float x = expf(-fabsf(lg)), y = 1.0f + x;
     const float s = has ? (lg >= 0.0f ? 1.0f : x) / y : 0.0f;
-    const float slope = has ? x / (y * y) : 0.0f;
+    float slope = has ? x / (y * y) : 0.0f, half = 1.0f;
+    if (has && tiny_exp(lg)) slope = half = half_exp(lg);
     if (a.renorm) {
       const float total = row_sum<Lanes>(s) + kDenom;
-      d = slope / total * (g - row_sum<Lanes>(g * s / total));
+      d = half * (slope / total * (g - row_sum<Lanes>(g * s / total)));
     } else {
-      d = slope * g;
+      d = half * (slope * g);
     }
   }
   if (!Full && in_place) {

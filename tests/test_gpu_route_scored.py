@@ -439,6 +439,30 @@ def test_route_scored_backward_far_logits():
         check_backward(logits, ids, scoring, renormalise)
 
 
+@pytest.mark.parametrize("M,E,groups", [(5, 48, (1, 1, 1)), (40, 48, (6, 2, 2)), (60, 384, (1, 1, 1))])
+def test_route_scored_sigmoids_below_the_normal_numbers(M, E, groups):
+    """Scores that fp32 holds as subnormal numbers or not at all: weights and gradients made of them have all
+    their bits (renormalised, they are divided by 1e-20)."""
+    base = normal(M, E, 80)
+    rng = np.random.default_rng(81)
+    ids = np.stack([rng.permutation(E)[:4] for _ in range(M)]).astype(np.int32)
+    for shift in (-80.0, -86.0, -92.0, -100.0, -120.0):
+        logits = base + np.float32(shift)
+        mixed = logits.copy()
+        mixed[:, ::3] = base[:, ::3] - 40  # beside others
+        for lg in (logits, mixed):
+            for renormalise, scale in ((True, 2.5), (False, 1.0), (False, 1e9)):
+                want_ids, want = oracle.route_scored(lg, 4, "sigmoid", None, *groups, renormalise, scale)
+                rb = moe.route_scored(dev(lg), moe.alloc_route_buffers(M, E, 4, 16), "sigmoid", None, *groups,
+                                      renormalise=renormalise, scale=scale)
+                np.testing.assert_array_equal(rb.topk_ids.cpu().numpy(), want_ids)
+                # the exponential of half the logit counts twice, and a product more joins the halves
+                n = weight_roundings(lg, "sigmoid", renormalise) + 3
+                np.testing.assert_allclose(rb.topk_weights.cpu().numpy(), want, rtol=n * U, atol=2.0 ** -126)
+                check_backward(lg, ids, "sigmoid", renormalise, scale)
+                check_backward(-lg, ids, "sigmoid", renormalise, scale)  # the slope is as small
+
+
 def test_route_scored_backward_is_the_forwards_difference():
     """The gradient against differences of the device's own fp32 forward (E = 6,
     step 2^-7: its third derivatives are below 1, so off by at most 2^-14 / 6
