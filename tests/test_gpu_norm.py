@@ -107,6 +107,41 @@ def test_norm_strides_and_alignment(N, gap, shift, out_gap):
                 assert (whole[:5] == 99).all()
 
 
+def steps_apart(a, b):
+    """Of positive fp32 values: the numbers of the type from one to the other."""
+    return (a.view(torch.int32).long() - b.view(torch.int32).long()).abs().max().item()
+
+
+@pytest.mark.parametrize("N", (64, 384, 1000, 2176, 7168, 16392))
+def test_norm_layouts_agree(N):
+    """The same rows contiguous and in other layouts. Rows of whole 16-byte chunks are added in the same order
+    wherever they lie: the same bits. Others are added in another order, in fp64: rstd is at most the rounding of
+    a neighbouring value."""
+    for dtype in (BF16, F32):
+        def run(gap, shift, out_gap):
+            x, res, w = tensors(6, N, dtype, 60 + N, gap=gap, shift=shift)
+            bufs = moe.alloc_norm_buffers(6, N, dtype, rstd=True, quant_group=N)
+            if out_gap:
+                bufs.residual_out = placed(torch.zeros(6, N, dtype=dtype), out_gap, out_gap)
+                bufs.out = placed(torch.zeros(6, N, dtype=BF16), out_gap, out_gap)
+                bufs.out8 = torch.zeros((6, N + out_gap), dtype=torch.uint8, device="cuda")[:, :N]
+            return moe.add_rms_norm(x, w, bufs, residual=res)
+
+        a = run(0, 0, 0)
+        for layout in ((8, 0, 0), (0, 8, 0), (24, 16, 8), (0, 0, 16), (128, 0, 128)):
+            b = run(*layout)
+            assert torch.equal(a.rstd, b.rstd) and torch.equal(a.residual_out, b.residual_out), layout
+            assert torch.equal(a.out, b.out) and torch.equal(a.scales, b.scales), layout
+            assert torch.equal(a.out8.view(torch.uint8), b.out8.view(torch.uint8)), layout
+        for layout in ((3, 0, 0), (0, 1, 0), (0, 0, 5), (24, 8, 3)):
+            b = run(*layout)
+            assert torch.equal(a.residual_out, b.residual_out), layout
+            assert steps_apart(a.rstd, b.rstd) <= 1 and steps_apart(a.scales, b.scales) <= 1, layout
+            # r one step apart, then the rounding to bf16 on both sides
+            far = (a.out.double() - b.out.double()).abs()
+            assert far.le((2 * HALF_BF16 + 4 * U) * a.out.double().abs() + 2.0 ** -133).all(), layout
+
+
 def test_norm_many_rows_and_in_place():
     for N, M in ((256, 4099), (7168, 300)):
         x, res, w = tensors(M, N, BF16, N)
