@@ -122,7 +122,7 @@ __device__ __forceinline__ double block_sum(double s, double (&room)[kWaves]) {
   return s;
 }
 
-// 176 M fp32 values in 48 tensors (705 MB): 117 us (6.0 TB/s).
+// 176 M fp32 values in 48 tensors (705 MB): 117 us profiled (6.0 TB/s).
 template <int kN>
 __global__ __launch_bounds__(kThreads) void grad_sumsq_kernel(Table<kN> tab, double* parts, double* direct) {
   __shared__ double room[kThreads / 64];
@@ -186,7 +186,7 @@ __device__ __forceinline__ void put(uint4* p, uint4 v) {
 
 // The workgroups go through the tensors from the last to the first: what the
 // pass over the squares read last is still in the cache. 705 MB read and written:
-// 252 us (5.6 TB/s); from the first to the last the two passes take 383 us, not 372.
+// 251 us profiled (5.6 TB/s); from the first to the last the two passes take 383 us, not 372.
 //
 // n_parts > 0: sumsq is still in that many parts, which every workgroup adds
 // itself, in the same order: one launch less, and up to kJoinParts of them cost less

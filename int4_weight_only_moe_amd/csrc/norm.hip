@@ -206,8 +206,10 @@ __device__ __forceinline__ bool fp32_top(uint32_t m) {
 
 // e4m3 of h w rr / s, as 4 bytes a word. In fp32 that is off by at most 6
 // roundings: where it is nowhere near the middle between two e4m3 values (bits 0 to
-// 19 of a normal one) it rounds like the exact value. The other chunks (one in a
-// hundred) take fp64.
+// 19 of a normal one) it rounds like the exact value. A wave with another value takes
+// fp64 for its whole chunk of 512: with 128 columns a scale 6 of 100 chunks of normal
+// values and 21 of those with a hundredth of the columns 20 times as large, with a
+// scale a row 8 and 55, nearly all for values below 2^-6.
 __device__ __forceinline__ void to_e4m3(const float (&h)[8], const float (&w)[8], double rr, float s, uint32_t (&out)[2]) {
   const float f = (float)rr * __builtin_amdgcn_rcpf(s);
   float y[8];
@@ -230,9 +232,10 @@ __device__ __forceinline__ void to_e4m3(const float (&h)[8], const float (&w)[8]
   }
 }
 
-// One row a team. [16384, 7168] bf16: 161 us for 940 MB (5.8 TB/s; a copy of as much
-// takes 181), [2048, 7168] of an fp32 stream with bf16 and 8-bit results 45 us for
-// 191 MB (4.3 TB/s): there 46 vector instructions a column of a lane, 17 us of issue,
+// One row a team. Profiled: [16384, 7168] bf16 161 us for 940 MB (5.8 TB/s; a copy of
+// as much takes 181), [2048, 7168] of an fp32 stream with bf16 and 8-bit results of
+// 128 columns a scale 45 us for 191 MB (4.3 TB/s; back to back in a graph, from the
+// cache, 35.8, and 39 with a scale a row): there 46 vector instructions a column of a lane, 17 us of issue,
 // run beside the loads of only two workgroups a CU (93 registers).
 template <bool Wide, int C, bool Vec, typename S, bool Quant>
 __global__ __launch_bounds__(Wide ? 64 * kMaxWaves : 256) void norm_kernel(NormArgs a) {
@@ -449,7 +452,7 @@ constexpr int kRunsMaxWidth = 16384;  // 128 KB of fp64 sums
 
 // A workgroup takes the rows kRows (blockIdx.x + n gridDim.x) + 0 .. kRows - 1
 // and leaves their sums for dw in parts[blockIdx.x]: they stay in registers over
-// all its rows. [16384, 7168] bf16: 176 us for 947 MB (5.4 TB/s).
+// all its rows. [16384, 7168] bf16: 175 us profiled for 947 MB (5.4 TB/s).
 // Runs: more than kRunRows rows a lane. After each run of so many the sums are added
 // to fp64 ones in LDS, where each lane has places of its own. Back to back calls of
 // [131072, 7168] bf16: 1402 us (1399 with one fp32 sum over all rows; 1436 with the

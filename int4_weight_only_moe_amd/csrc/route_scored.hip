@@ -13,8 +13,12 @@
 // where fp32 values that decide the choice are closer than their error bound are
 // the candidates' c computed again in fp64. (Equal logits with equal biases need
 // no such decision: the lower expert goes first.) Where that decides between
-// groups, or something is not finite, or the candidates are too many, the wave
-// computes the whole row again in fp64 (route_row_exact).
+// groups, or a value is NaN (with a bias or groups: not finite, an absent expert's
+// too), or the candidates are too many, the wave computes the whole row again in
+// fp64 (route_row_exact), some 6 us for one row. Back to back in a graph, sigmoid and a
+// bias: [4096, 256] in 8 groups 7.1 to 7.6 us for inputs without such a row (about
+// three in four), 13.2 with one; [8192, 1024] in 16 groups 19.4 and 27.8; [16384, 384]
+// with every row there (one bias of -inf) 57 instead of 10.8.
 #include <type_traits>
 
 #include "device_common.h"
@@ -586,10 +590,12 @@ __device__ __forceinline__ void route_rows(const ScoredArgs& a, int64_t t0, Rout
 // One pass of rows a workgroup, from row `first_row` on: in a loop the compiler
 // keeps what does not depend on the row (biases, groups of the experts) in
 // registers, twice as many as fit 4 waves a SIMD.
-// [16384, 384] softmax, top 8: 9.1 us (26 MB, 5.0 us at the rate of a copy): 146 vector
-// instructions a row, 3.9 us of issue, beside the loads. Sigmoid and a bias 11.5 us;
-// [16384, 256] in 8 groups 16.1, where the groups' two passes through LDS take 5.
-// [4096, 256] in groups has two waves a SIMD and takes 10.7 us of latency.
+// [16384, 384] softmax, top 8: 9.2 us profiled (26 MB, 5.0 us at the rate of a copy):
+// 146 vector instructions a row, 3.9 us of issue, beside the loads. Back to back in a
+// graph (the logits then come from the cache) 6.3, sigmoid and a bias 10.8; [16384,
+// 256] 8.0, in 8 groups 15.0: the groups' two passes through LDS. [4096, 256] in
+// groups has two waves a SIMD and takes 7.3 us of latency (profiled: 10.0; with a row
+// on the exact path 15.5).
 template <int Lanes, int NV, bool Vec, bool General>
 __global__ __launch_bounds__(kThreads) void route_scored_kernel(ScoredArgs a, int64_t first_row) {
   extern __shared__ __align__(16) float buffer[];
@@ -605,7 +611,7 @@ __global__ __launch_bounds__(kThreads) void route_scored_kernel(ScoredArgs a, in
 
 // Up to 16 rows: routing and grouping in one workgroup and one launch (two launches
 // follow each other every 3.6 us). The grouping's tables take the dynamic LDS after
-// the routing. One row of 384: 7.4 us, the latency of one wave's steps.
+// the routing. One row of 384: 7.3 us profiled, the latency of one wave's steps.
 template <int Lanes, int NV, bool Vec, bool General>
 __global__ __launch_bounds__(kThreads) void route_scored_small_kernel(ScoredArgs a) {
   extern __shared__ __align__(16) float buffer[];
@@ -636,9 +642,12 @@ static_assert(kSmallMaxAssign <= kThreads, "one id a thread");
 
 // fn(Lanes, NV, Vec) for the row width. Few rows (kFewRows: below that 16 lanes a
 // row are less than two waves a SIMD) take 32 lanes from 65 experts on: the work of
-// a row is then done sooner ([64, 384] 4.5 us instead of 5.4, [4096, 256] in groups
-// 12.3 instead of 13.0), while a full device takes longer ([16384, 384] 10.3 instead
-// of 8.6).
+// a row is then done sooner (top 8, back to back in a graph: [64, 384] 4.3 us instead
+// of 5.6, [4096, 256] in groups 7.3 instead of 8.0), while a full device takes longer
+// ([16384, 384] softmax 8.5 instead of 6.5, with a bias 11.7 instead of 10.7). For top
+// 16 the lowest of 16 lanes' maxima is a low threshold, and more than 64 candidates
+// send many rows to the exact path: there 16 lanes take 49 us for [16384, 384]
+// (67 with a bias), 32 lanes would take 10.5 (15.1).
 constexpr int kFewRows = 8192;
 template <typename F>
 void by_width(int E, bool vec, bool few, F fn) {
@@ -665,8 +674,8 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 // experts): every logit has a gradient. Otherwise only the kept ones have;
 // the rest of the row is grad_base or zeros, and is not touched in place.
 // The slots' values reach the row's order through LDS.
-// Bound by HBM: [16384, 384] full: calls back to back every 9.6 us for 51 MB
-// (5.4 TB/s).
+// Bound by HBM: [16384, 384] full: calls of a program every 9.6 us for 51 MB
+// (5.4 TB/s; 10.4 us profiled).
 template <int Lanes, int NV, bool Vec, bool Full>
 __global__ __launch_bounds__(kThreads) void route_scored_backward_kernel(ScoredBackwardArgs a, int64_t first_row) {
   extern __shared__ __align__(16) float buffer[];

@@ -1,6 +1,7 @@
 // A row of values (the logits of a token) in the registers of 16 or 32 lanes:
-// sums and maxima over the row, loading, and its softmax's exponentials. Shared
-// by the balance loss and the routing by scores.
+// sums and maxima over the row and loading, shared by the balance loss and the
+// routing by scores; and the balance loss's exponentials (the routing keeps the
+// logits and has a form of its own, RowSoftmax).
 #pragma once
 
 #include "route_common.h"
